@@ -82,6 +82,10 @@ extern "C" {
                                           pivot (damped Hessian not positive
                                           definite in fp32); results unreliable */
 
+#define W4_ERR_PAGE_TABLE         -13  /* device flag: a page number outside
+                                          [0, pages), or a kv_len that is
+                                          negative or past the table or max_len */
+
 /* Size of the library's built-in split-K scratch used by
  * w4a16_linear_noalloc (4 MiB, held by every GPU that loads the library).  */
 #define W4_NOALLOC_SCRATCH_BYTES (4 << 20)
@@ -449,6 +453,170 @@ W4_API int w4a8_linear(const int8_t* qx, const float* sx, const uint8_t* packed,
                 const float* w_scales, const float* bias, uint16_t* y,
                 int32_t* acc_out, int M, int N, int K, int group_size,
                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ===========================================================================
+ * The operators of a decoder block between its linear layers: norms with the
+ * residual, rotary positions, a paged key-value cache and the attention that
+ * reads it (the block of "Lab 5: Gemma4 端到端推理优化", section 基础: grouped
+ * heads, sliding window, norms; a paged cache as the serving slides of "LLM
+ * 模型壓縮與推理加速實踐-陳磊.pdf" use one; the pages describe these parts, the
+ * kernels are this library's own).
+ *
+ * All sums, norms and softmax statistics are fp32; every bf16 output is
+ * rounded once.  Each call enqueues one kernel.  The kernels are launched with
+ * programmatic dependent launch and touch no memory before the kernel ahead of
+ * them on the stream has completed.
+ * ------------------------------------------------------------------------- */
+
+/* A paged key-value cache as one launch sees it (host struct; all pointers are
+ * device pointers).  Key j of sequence b, head h, is the head_dim contiguous
+ * bf16 values at
+ *   k + page * k_page_stride + h * k_head_stride + slot * k_slot_stride,
+ *   page = table[b * table_stride + j / page_size], slot = j % page_size
+ * (strides in elements; values the same way from v).  Pools laid out
+ * [pages, heads, page_size, head_dim], [pages, page_size, heads, head_dim] or
+ * with keys and values interleaved are all strides.
+ *  k, v 16-byte aligned, strides multiples of 8 and positive; page_size a
+ *  power of two, 16 .. 4096; head_dim 64 or 128 for the attention calls (a
+ *  multiple of 8 up to 256 for w4_rope_append); pages, max_pages >= 1.
+ *  kv_len[b] is the sequence's length with this step's tokens; 0 marks an
+ *  unused row of the batch.  table, kv_len and the token offsets are read on
+ *  the device: a length that is negative or past max_pages * page_size is
+ *  clamped, a page number outside [0, pages) is read as page 0, and either
+ *  raises W4_ERR_PAGE_TABLE in the device flag (that sequence's outputs are
+ *  then unspecified; nothing out of range is read or written).  Only the table
+ *  entries of pages that a call reads or writes have to be valid, and slots at
+ *  or past kv_len may hold anything. */
+typedef struct w4_paged_kv {
+    uint16_t*      k;
+    uint16_t*      v;
+    const int32_t* table;       /* [batch, max_pages], row stride table_stride */
+    const int32_t* kv_len;      /* [batch]                                     */
+    int64_t k_page_stride, k_head_stride, k_slot_stride;
+    int64_t v_page_stride, v_head_stride, v_slot_stride;
+    int64_t table_stride;
+    int32_t pages, page_size, heads, head_dim, batch, max_pages;
+} w4_paged_kv;
+
+/* ---------------------------------------------------------------------------
+ * w4_block_norm - the RMS norms after and before a block, fused with the
+ * block's gate, residual scale and residual sum:
+ *  u  = y * rsqrt(mean(y^2) + eps) * (w_offset + w_post)   (u = y: no w_post)
+ *  r' = r + res_scale * gate * u                           (gate 1: no gate)
+ *  x  = r' * rsqrt(mean(r'^2) + eps) * (w_offset + w_pre)
+ * over the K columns of each row; x is computed from r' before r' is rounded.
+ *
+ *  y      [M, K] bf16, the block's output, or NULL (r' = r: only the norm
+ *         before the first block; w_post, gate and r_out must then be NULL).
+ *  r      [M, K] bf16, the residual stream.
+ *  w_post, w_pre  [K] bf16 or NULL; w_pre may be NULL only when x_out is.
+ *  gate   [gate_rows, K] bf16 or NULL (gate_rows 0); gate_rows divides M and
+ *         row m uses gate row m / (M / gate_rows).
+ *  r_out  [M, K] bf16 out (may be r or y itself); required when y is given.
+ *  x_out  [M, K] bf16 out (may be y itself) or NULL.
+ *  eps >= 0; w_offset 0, or 1 for weights stored as offsets from one.
+ *  K <= W4_BLOCK_NORM_MAX_K.  Buffers need 2-byte alignment (16-byte aligned
+ *  rows, K % 8 == 0, run fastest).
+ * ------------------------------------------------------------------------- */
+#define W4_BLOCK_NORM_MAX_K 32768
+W4_API int w4_block_norm(const uint16_t* y, const uint16_t* r, const uint16_t* w_post,
+                         const uint16_t* gate, const uint16_t* w_pre, uint16_t* r_out,
+                         uint16_t* x_out, int M, int K, int gate_rows, float res_scale,
+                         float eps, float w_offset, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * w4_rope_freqs - rotary frequencies of rot_dim / 2 pairs, on the host, in
+ * double precision, rounded to fp32 once: f_i = base^(-2 i / rot_dim) scaled
+ * for contexts longer than orig_len by
+ *  W4_ROPE_PLAIN   not at all;
+ *  W4_ROPE_LINEAR  f_i / factor;
+ *  W4_ROPE_NTK     base' = base * factor^(rot_dim / (rot_dim - 2));
+ *  W4_ROPE_YARN    frequencies that turn at least beta_fast times over
+ *                  orig_len are kept, those that turn at most beta_slow times
+ *                  are divided by factor, between them a linear ramp in the
+ *                  pair index; *mscale = 0.1 ln(factor) + 1 (factor > 1).
+ *  inv_freq  host array of rot_dim / 2 floats, out.  mscale: host, out, the
+ *  factor on cos and sin (1 but for W4_ROPE_YARN).
+ * ------------------------------------------------------------------------- */
+#define W4_ROPE_PLAIN  0
+#define W4_ROPE_LINEAR 1
+#define W4_ROPE_NTK    2
+#define W4_ROPE_YARN   3
+W4_API int w4_rope_freqs(int rot_dim, double base, int kind, double factor, double orig_len,
+                         double beta_fast, double beta_slow, float* inv_freq, float* mscale);
+
+/* ---------------------------------------------------------------------------
+ * w4_rope_append - rotary positions on q and k, and k and v written into the
+ * cache.  Row t belongs to the sequence b with goff[b] <= t < goff[b+1] and is
+ * token p = kv_len[b] - (goff[b+1] - t) of it.  The first rot_dim values of
+ * each q and k head are rotated in pairs, the others kept:
+ *  (a, c) -> mscale * (a cos - c sin, a sin + c cos),  angle = P * inv_freq[i],
+ *  P = pos[t], or p when pos is NULL;
+ *  pair i is (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved != 0.
+ * The angle is reduced modulo 2 pi from the exact product, so it is good to
+ * 2^-20 rad at every |P| < 2^24.
+ *
+ *  q [T, q_heads, D], k, v [T, kv->heads, D] bf16: token and head strides in
+ *    elements, D contiguous (slices of one qkv projection are fine).
+ *  q_out  [T, q_heads, D] bf16 contiguous, out; may be q itself if q is
+ *    contiguous.
+ *  goff   [batch + 1] int32 on the device, or NULL: one token a sequence
+ *    (T == batch).  pos [T] int32 on the device or NULL.
+ *  inv_freq [rot_dim / 2] fp32 on the device; rot_dim even, 0 .. D.
+ *  A token with p < 0 (an unused batch row) writes nothing to the cache and
+ *  gets q_out = 0; rows outside every sequence are left as they are.  Offsets
+ *  outside [0, T] or decreasing raise W4_ERR_GROUP_TOKENS in the device flag
+ *  and that sequence's rows are left as they are.  Two sequences must not
+ *  write the same page slot.
+ * ------------------------------------------------------------------------- */
+W4_API int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
+                          long long q_head_stride, const uint16_t* k, long long k_token_stride,
+                          long long k_head_stride, const uint16_t* v, long long v_token_stride,
+                          long long v_head_stride, const int32_t* goff, const int32_t* pos,
+                          const float* inv_freq, float mscale, int rot_dim, int interleaved,
+                          uint16_t* q_out, int T, int q_heads, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * w4_attn_decode / w4_attn_prefill - softmax attention over the paged cache:
+ *  o = sum_j w_j v_j,  w = softmax over the visible j of scale * (q . k_j)
+ * Query head h reads key-value head h / (q_heads / heads).  The token at
+ * position p sees key j when
+ *  j <= p  and  (window == 0  or  p - j < window  or  j < sinks):
+ * a causal mask, optionally a sliding window of the last `window` keys
+ * (itself included) with the first `sinks` keys kept visible.  Keys that no
+ * token sees are not read and have no influence, whatever they hold.  A token
+ * that sees nothing gets o = 0 and lse = -inf.
+ *
+ *  w4_attn_decode: one token a sequence, p = kv_len[b] - 1 (its key already
+ *    written); q, out [batch, q_heads, D].
+ *  w4_attn_prefill: rows goff[b] .. goff[b+1] - 1 of q, out [T, q_heads, D]
+ *    are the last tokens of sequence b (a prompt, or a chunk behind a cached
+ *    prefix), placed as in w4_rope_append; goff as there.
+ *  q     bf16, 16-byte aligned; token and head strides in elements,
+ *        multiples of 8, D contiguous.
+ *  out   bf16 contiguous, 16-byte aligned.
+ *  lse   [rows, q_heads] fp32 out or NULL: log sum exp(scale q . k).
+ *  max_len, max_q   host upper bounds of kv_len and of a sequence's rows: they
+ *        size the launch, not the result.  A longer kv_len is clamped with
+ *        W4_ERR_PAGE_TABLE, longer rows raise W4_ERR_GROUP_TOKENS and stay
+ *        unwritten.
+ *  q_heads a multiple of heads, at most 128 times as many; scale > 0.
+ *  workspace: at least w4_attn_workspace_bytes(...) bytes, zero-filled once
+ *        (it starts with W4_WORKSPACE_COUNTER_BYTES of arrival counters that
+ *        every call leaves at zero; it can be the linear layers' workspace).
+ *        Calls that share one must not overlap on the GPU.
+ * ------------------------------------------------------------------------- */
+W4_API size_t w4_attn_workspace_bytes(int batch, int q_heads, int heads, int head_dim,
+                                      int max_q, int max_len);
+W4_API int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
+                          long long q_head_stride, uint16_t* out, float* lse, int q_heads,
+                          int max_len, float scale, int window, int sinks, void* workspace,
+                          size_t workspace_bytes, void* stream);
+W4_API int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
+                           long long q_head_stride, const int32_t* goff, uint16_t* out,
+                           float* lse, int T, int q_heads, int max_q, int max_len, float scale,
+                           int window, int sinks, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /* ---------------------------------------------------------------------------
  * w4_get_device_error - synchronizes `stream`, then returns and clears the

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -12,6 +13,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libw4.so")
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes); mirrors include/w4.h
 _SIGS = {
@@ -43,6 +45,15 @@ _SIGS = {
     "w4_decode_plan": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "w4a8_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                              _vp, _c_size, _vp]),
+    "w4_block_norm": (_c_int, [_vp] * 7 + [_c_int] * 3 + [ctypes.c_float] * 3 + [_vp]),
+    "w4_rope_freqs": (_c_int, [_c_int, ctypes.c_double, _c_int] + [ctypes.c_double] * 4 + [_vp] * 2),
+    "w4_rope_append": (_c_int, [_vp] + [_vp, _c_ll, _c_ll] * 3 + [_vp] * 3
+                       + [ctypes.c_float, _c_int, _c_int, _vp, _c_int, _c_int, _vp]),
+    "w4_attn_workspace_bytes": (_c_size, [_c_int] * 6),
+    "w4_attn_decode": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _c_int, _c_int, ctypes.c_float,
+                                _c_int, _c_int, _vp, _c_size, _vp]),
+    "w4_attn_prefill": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _vp] + [_c_int] * 4
+                        + [ctypes.c_float, _c_int, _c_int, _vp, _c_size, _vp]),
     "w4_get_device_error": (_c_int, [_vp]),
     "w4_set_wait_limit": (_c_int, [ctypes.c_longlong, _vp]),
     "w4_set_fault_injection": (_c_int, [_c_int, _vp]),
@@ -584,6 +595,199 @@ def w4a8_linear(qx: torch.Tensor, sx: torch.Tensor, packed: torch.Tensor,
         (_stream(qx, stream),), qx.device, workspace,
         lambda: lib.w4a8_workspace_bytes(M, N, K, group_size))
     return y, acc_out
+
+
+# ------------------------------------------------------------- decoder block
+# struct w4_paged_kv of include/w4.h
+_PAGED_KV = struct.Struct("4Q7q6i")
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _need_view(t, dtype, ndim, name):
+    """A CUDA tensor whose last dimension is contiguous (other strides free)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _paged_kv(k_cache, v_cache, kv_len, table):
+    """The packed w4_paged_kv of a pool [pages, heads, page_size, head_dim]."""
+    _need_view(k_cache, torch.bfloat16, 4, "k_cache")
+    _need_view(v_cache, torch.bfloat16, 4, "v_cache")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    _need_view(table, torch.int32, 2, "table")
+    _need(kv_len, torch.int32, (table.shape[0],), "kv_len")
+    pages, heads, page_size, d = k_cache.shape
+    batch, max_pages = table.shape
+    ks, vs = k_cache.stride(), v_cache.stride()
+    return _PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), kv_len.data_ptr(),
+                          ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table.stride(0),
+                          pages, page_size, heads, d, batch, max_pages)
+
+
+def w4_block_norm(y: Optional[torch.Tensor], r: torch.Tensor, w_pre: Optional[torch.Tensor],
+                  w_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  res_scale: float = 1.0, eps: float = 1e-6, w_offset: float = 0.0, r_out=None,
+                  x_out=None, stream=None):
+    """(r', x) of the norms around a block, all [M, K] bf16:
+    u = rmsnorm(y) * (w_offset + w_post) (u = y without w_post),
+    r' = r + res_scale * gate * u, x = rmsnorm(r') * (w_offset + w_pre).
+    gate [g, K]: row m uses gate row m // (M // g).  y None: (r, norm of r);
+    w_pre None: (r', None)."""
+    M, K = r.shape
+    _need(r, torch.bfloat16, (M, K), "r")
+    if y is not None:
+        _need(y, torch.bfloat16, (M, K), "y")
+        if r_out is None:
+            r_out = torch.empty_like(r)
+        _need(r_out, torch.bfloat16, (M, K), "r_out")
+    elif r_out is not None:
+        raise ValueError("r_out needs y")
+    if w_pre is not None:
+        _need(w_pre, torch.bfloat16, (K,), "w_pre")
+        if x_out is None:
+            x_out = torch.empty_like(r)
+        _need(x_out, torch.bfloat16, (M, K), "x_out")
+    if w_post is not None:
+        _need(w_post, torch.bfloat16, (K,), "w_post")
+    rows = 0
+    if gate is not None:
+        rows = gate.shape[0]
+        _need(gate, torch.bfloat16, (rows, K), "gate")
+    if M == 0:
+        return (r if y is None else r_out), x_out
+    _check("w4_block_norm", load().w4_block_norm(
+        _ptr(y), r.data_ptr(), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(r_out), _ptr(x_out), M, K,
+        rows, res_scale, eps, w_offset, _stream(r, stream)))
+    return (r if y is None else r_out), x_out
+
+
+def w4_rope_freqs(rot_dim: int, base: float = 1e4, kind: str = "plain", factor: float = 1.0,
+                  orig_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq [rot_dim / 2] fp32 on the CPU, mscale): the rotary frequencies,
+    scaled for long contexts by `kind` ("plain", "linear", "ntk", "yarn")."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {tuple(ROPE_KINDS)}, got {kind!r}")
+    inv = torch.empty(max(rot_dim // 2, 1), dtype=torch.float32)
+    m = ctypes.c_float()
+    _check("w4_rope_freqs", load().w4_rope_freqs(
+        rot_dim, base, ROPE_KINDS[kind], factor, orig_len, beta_fast, beta_slow, inv.data_ptr(),
+        ctypes.addressof(m)))
+    return inv, m.value
+
+
+def w4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor,
+                   inv_freq: torch.Tensor, goff: Optional[torch.Tensor] = None,
+                   pos: Optional[torch.Tensor] = None, interleaved: bool = False,
+                   mscale: float = 1.0, q_out=None, stream=None) -> torch.Tensor:
+    """q_out [T, Hq, D] = q with rotary positions; k (rotated) and v are written
+    into the paged cache (pools [pages, Hkv, page_size, D], any strides).  q, k,
+    v [T, heads, D] may be slices of one projection.  kv_len [B] counts this
+    step's tokens; goff [B + 1] are the sequences' first rows (None: one token a
+    sequence); pos [T] overrides the rotary positions.  The first
+    2 * len(inv_freq) values of a head are rotated."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _need_view(t, torch.bfloat16, 3, name)
+    kv = _paged_kv(k_cache, v_cache, kv_len, table)
+    T, Hq, D = q.shape
+    want = (T, k_cache.shape[1], k_cache.shape[3])
+    if k.shape != want or v.shape != want or D != want[2]:
+        raise ValueError(f"k and v must have shape {want} and q [{T}, heads, {want[2]}], got "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}, {tuple(q.shape)}")
+    _need(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
+    if goff is not None:
+        _need(goff, torch.int32, (table.shape[0] + 1,), "goff")
+    if pos is not None:
+        _need(pos, torch.int32, (T,), "pos")
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+    _need(q_out, torch.bfloat16, (T, Hq, D), "q_out")
+    if T == 0:
+        return q_out
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    _check("w4_rope_append", load().w4_rope_append(
+        kv, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+        _ptr(goff), _ptr(pos), inv_freq.data_ptr(), mscale, 2 * inv_freq.numel(),
+        1 if interleaved else 0, q_out.data_ptr(), T, Hq, _stream(q, stream)))
+    return q_out
+
+
+def w4_attn_workspace_bytes(batch: int, q_heads: int, heads: int, head_dim: int, max_q: int,
+                            max_len: int) -> int:
+    return int(load().w4_attn_workspace_bytes(batch, q_heads, heads, head_dim, max_q, max_len))
+
+
+def _attn_outputs(q, out, lse):
+    _need_view(q, torch.bfloat16, 3, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _need(out, torch.bfloat16, q.shape, "out")
+    if lse is not None:
+        _need(lse, torch.float32, q.shape[:2], "lse")
+    return out
+
+
+def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   kv_len: torch.Tensor, table: torch.Tensor, max_len: int,
+                   scale: Optional[float] = None, window: int = 0, sinks: int = 0, out=None,
+                   lse=None, workspace=None, stream=None) -> torch.Tensor:
+    """out [B, Hq, D] bf16: attention of one new token per sequence (q [B, Hq,
+    D], position kv_len - 1) over the paged cache; scale defaults to D**-0.5.
+    Key j is visible when j <= p and (window == 0 or p - j < window or
+    j < sinks).  max_len bounds kv_len; lse [B, Hq] fp32 receives the
+    log-sum-exp when given."""
+    kv = _paged_kv(k_cache, v_cache, kv_len, table)
+    B, Hq, D = q.shape
+    if B != table.shape[0] or D != k_cache.shape[3]:
+        raise ValueError(f"q must have shape [{table.shape[0]}, heads, {k_cache.shape[3]}], got {tuple(q.shape)}")
+    out = _attn_outputs(q, out, lse)
+    if q.numel() == 0:
+        return out
+    qs = q.stride()
+    lib = load()
+    _call_with_workspace(
+        lib.w4_attn_decode, "w4_attn_decode",
+        (kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), _ptr(lse), Hq, max_len,
+         D ** -0.5 if scale is None else scale, window, sinks),
+        (_stream(q, stream),), q.device, workspace,
+        lambda: lib.w4_attn_workspace_bytes(B, Hq, k_cache.shape[1], D, 1, max_len))
+    return out
+
+
+def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    goff: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,
+                    max_len: int, scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                    out=None, lse=None, workspace=None, stream=None) -> torch.Tensor:
+    """out [T, Hq, D] bf16: attention of many tokens per sequence over the paged
+    cache.  Rows goff[b] .. goff[b + 1] - 1 of q are the last tokens of sequence
+    b (their keys already written); max_q bounds their number, max_len kv_len.
+    The mask and the other arguments are w4_attn_decode's."""
+    kv = _paged_kv(k_cache, v_cache, kv_len, table)
+    T, Hq, D = q.shape
+    if D != k_cache.shape[3]:
+        raise ValueError(f"q must have shape [T, heads, {k_cache.shape[3]}], got {tuple(q.shape)}")
+    _need(goff, torch.int32, (table.shape[0] + 1,), "goff")
+    out = _attn_outputs(q, out, lse)
+    if q.numel() == 0:
+        return out
+    qs = q.stride()
+    lib = load()
+    _call_with_workspace(
+        lib.w4_attn_prefill, "w4_attn_prefill",
+        (kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(), _ptr(lse), T, Hq, max_q,
+         max_len, D ** -0.5 if scale is None else scale, window, sinks),
+        (_stream(q, stream),), q.device, workspace,
+        lambda: lib.w4_attn_workspace_bytes(table.shape[0], Hq, k_cache.shape[1], D, min(max_q, T),
+                                            max_len))
+    return out
 
 
 def w4_get_device_error(stream=None) -> int:

@@ -672,6 +672,8 @@ const char* w4_error_string(int code) {
             return "GPTQ met a non-positive Cholesky pivot (damped Hessian not positive definite)";
         case W4_ERR_GROUP_TOKENS:
             return "a group's token offsets were invalid (outside [0, T] or decreasing)";
+        case W4_ERR_PAGE_TABLE:
+            return "a page number or a cached length was out of range";
         default: return "unknown error code";
     }
 }

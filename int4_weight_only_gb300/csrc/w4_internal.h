@@ -203,4 +203,51 @@ int launch_gptq(const uint16_t* X, int T, const float* W, int N, int K, int Kp, 
 int launch_smooth(const uint16_t* X, int T, float* W, int N, int K, float alpha, float* s,
                   float* inv_s, cudaStream_t stream);
 
+
+// ---------------------------------------------------------------- decoder block
+// Norms after and before a block with gate, residual scale and residual
+// (norm.cu); arguments as w4_block_norm, checked by the caller.
+struct NormArgs {
+    const uint16_t *y, *r, *w_post, *gate, *w_pre;
+    uint16_t *r_out, *x_out;
+    int M, K, gate_div;            // row m uses gate row m / gate_div
+    float res_scale, eps, w_off;
+};
+int launch_block_norm(const NormArgs& a, int sm_count, cudaStream_t stream);
+
+// Rotary positions and the cache write (rope.cu).
+struct RopeArgs {
+    w4_paged_kv kv;
+    const uint16_t *q, *k, *v;
+    long long q_tok, q_head, k_tok, k_head, v_tok, v_head;
+    const int32_t *goff, *pos;
+    const float* inv_freq;
+    float mscale;
+    int rot, inter;
+    uint16_t* q_out;
+    int T, Hq;
+    int* err;
+};
+int launch_rope_append(const RopeArgs& a, cudaStream_t stream);
+
+// Attention over the paged cache (attn_decode.cu, attn_prefill.cu).
+struct AttnArgs {
+    w4_paged_kv kv;
+    const uint16_t* q;
+    long long q_tok, q_head;
+    const int32_t* goff;           // prefill; decode: nullptr
+    uint16_t* out;
+    float* lse;
+    int T, Hq, max_q, max_len;
+    float scale;                   // softmax scale times log2(e)
+    int window, sinks;             // window 0: none
+    int* tickets;
+    float* partial;
+    int* err;
+};
+size_t attn_decode_ws_bytes(int batch, int Hq, int Hkv, int D, int sm_count);
+size_t attn_prefill_ws_bytes(int batch, int Hq, int Hkv, int D, int max_q, int max_len, int sm_count);
+int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream);
+int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream);
+
 }  // namespace w4
