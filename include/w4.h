@@ -476,7 +476,8 @@ W4_API int w4a8_linear(const int8_t* qx, const float* sx, const uint8_t* packed,
  * (strides in elements; values the same way from v).  Pools laid out
  * [pages, heads, page_size, head_dim], [pages, page_size, heads, head_dim] or
  * with keys and values interleaved are all strides.
- *  k, v 16-byte aligned, strides multiples of 8 and positive; page_size a
+ *  k, v 16-byte aligned, strides multiples of 8 and positive (the stride of a
+ *  dimension of extent 1 is ignored); page_size a
  *  power of two, 16 .. 4096; head_dim 64 or 128 for the attention calls (a
  *  multiple of 8 up to 256 for w4_rope_append); pages, max_pages >= 1.
  *  kv_len[b] is the sequence's length with this step's tokens; 0 marks an
@@ -597,7 +598,7 @@ W4_API int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_
  *  out   bf16 contiguous, 16-byte aligned.
  *  lse   [rows, q_heads] fp32 out or NULL: log sum exp(scale q . k).
  *  max_len, max_q   host upper bounds of kv_len and of a sequence's rows: they
- *        size the launch, not the result.  A longer kv_len is clamped with
+ *        size the launch, not the result (max_len <= 2^30).  A longer kv_len is clamped with
  *        W4_ERR_PAGE_TABLE, longer rows raise W4_ERR_GROUP_TOKENS and stay
  *        unwritten.
  *  q_heads a multiple of heads, at most 128 times as many; scale > 0.

@@ -10,9 +10,14 @@ namespace {
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Checks of the cache that every call shares.
-int check_kv(const w4_paged_kv* kv) {
-    if (!kv || !kv->k || !kv->v || !kv->table || !kv->kv_len) return W4_ERR_NULL_PTR;
+// Checks of the cache that every call shares, on a copy in which the strides
+// of dimensions of extent 1 (never used) are replaced by valid ones.
+int check_kv(const w4_paged_kv* in, w4_paged_kv* kv) {
+    if (!in || !in->k || !in->v || !in->table || !in->kv_len) return W4_ERR_NULL_PTR;
+    *kv = *in;
+    if (kv->pages == 1) kv->k_page_stride = kv->v_page_stride = 8;
+    if (kv->heads == 1) kv->k_head_stride = kv->v_head_stride = 8;
+    if (kv->batch == 1) kv->table_stride = 0;
     if (kv->pages < 1 || kv->max_pages < 1 || kv->heads < 1 || kv->batch < 0 || kv->head_dim < 1 ||
         kv->table_stride < 0)
         return W4_ERR_INVALID_ARG;
@@ -29,19 +34,26 @@ int check_kv(const w4_paged_kv* kv) {
 }
 
 // The part of the attention calls' checks that does not depend on the form.
-int check_attn(const w4_paged_kv* kv, const uint16_t* q, long long q_tok, long long q_head,
-               const uint16_t* out, const float* lse, int q_heads, int max_len, float scale, int window,
-               int sinks) {
-    const int rc = check_kv(kv);
+int check_attn(const w4_paged_kv* in, const uint16_t* q, long long q_tok, long long q_head,
+               uint16_t* out, float* lse, int q_heads, int max_len, float scale, int window,
+               int sinks, AttnArgs* a) {
+    w4_paged_kv* kv = &a->kv;
+    const int rc = check_kv(in, kv);
     if (rc) return rc;
     if (!q || !out) return W4_ERR_NULL_PTR;
     if (kv->head_dim != 64 && kv->head_dim != 128) return W4_ERR_UNSUPPORTED_SHAPE;
     if (q_heads < 1 || q_heads % kv->heads || max_len < 0 || window < 0 || sinks < 0 || q_tok < 0 || q_head < 0 ||
         !(scale > 0.f) || !std::isfinite(scale))
         return W4_ERR_INVALID_ARG;
+    // positions, windows and their differences stay inside 32 bits
+    if (max_len > (1 << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
+    window = std::min(window, 1 << 30);
     if (q_heads / kv->heads > 128) return W4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(q, 16) || !aligned(out, 16) || q_tok % 8 || q_head % 8 || !aligned(lse, 4))
         return W4_ERR_MISALIGNED;
+    a->q = q; a->q_tok = q_tok; a->q_head = q_head;
+    a->out = out; a->lse = lse; a->Hq = q_heads; a->max_len = max_len;
+    a->scale = scale * 1.4426950408889634f; a->window = window; a->sinks = sinks;
     return W4_OK;
 }
 
@@ -127,7 +139,8 @@ int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
                    long long v_token_stride, long long v_head_stride, const int32_t* goff, const int32_t* pos,
                    const float* inv_freq, float mscale, int rot_dim, int interleaved, uint16_t* q_out, int T,
                    int q_heads, void* stream) {
-    const int rc = check_kv(kv);
+    RopeArgs a{};
+    const int rc = check_kv(kv, &a.kv);
     if (rc) return rc;
     if (!q || !k || !v || !q_out || (rot_dim > 0 && !inv_freq)) return W4_ERR_NULL_PTR;
     if (T < 0 || q_heads < 1 || rot_dim < 0 || rot_dim % 2 || rot_dim > kv->head_dim || !std::isfinite(mscale))
@@ -140,8 +153,6 @@ int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
         if (!aligned(p, 2)) return W4_ERR_MISALIGNED;
     if (!aligned(goff, 4) || !aligned(pos, 4) || !aligned(inv_freq, 4)) return W4_ERR_MISALIGNED;
     if (T == 0 || kv->batch == 0) return W4_OK;
-    RopeArgs a{};
-    a.kv = *kv;
     a.q = q; a.k = k; a.v = v;
     a.q_tok = q_token_stride; a.q_head = q_head_stride; a.k_tok = k_token_stride; a.k_head = k_head_stride;
     a.v_tok = v_token_stride; a.v_head = v_head_stride;
@@ -164,39 +175,42 @@ size_t w4_attn_workspace_bytes(int batch, int q_heads, int heads, int head_dim, 
 int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
                    uint16_t* out, float* lse, int q_heads, int max_len, float scale, int window, int sinks,
                    void* workspace, size_t workspace_bytes, void* stream) {
-    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks);
+    AttnArgs a{};
+    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
     if (rc) return rc;
     if (kv->batch == 0) return W4_OK;
-    AttnArgs a{};
     const int sms = current_sm_count();
     rc = attn_workspace(&a, attn_decode_ws_bytes(kv->batch, q_heads, kv->heads, kv->head_dim, sms), workspace,
                         workspace_bytes);
     if (rc) return rc;
-    a.kv = *kv; a.q = q; a.q_tok = q_token_stride; a.q_head = q_head_stride;
-    a.out = out; a.lse = lse; a.T = kv->batch; a.Hq = q_heads; a.max_q = 1; a.max_len = max_len;
-    a.scale = scale * 1.4426950408889634f; a.window = window; a.sinks = sinks;
+    a.T = kv->batch;
+    a.max_q = 1;
     return launch_attn_decode(a, sms, static_cast<cudaStream_t>(stream));
 }
 
 int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
                     const int32_t* goff, uint16_t* out, float* lse, int T, int q_heads, int max_q, int max_len,
                     float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
-    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks);
+    AttnArgs a{};
+    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
     if (rc) return rc;
     if (!goff) return W4_ERR_NULL_PTR;
     if (T < 0 || max_q < 0) return W4_ERR_INVALID_ARG;
     if (!aligned(goff, 4)) return W4_ERR_MISALIGNED;
     if (kv->batch > 65535 || kv->heads > 65535) return W4_ERR_UNSUPPORTED_SHAPE;
     if (kv->batch == 0 || T == 0 || max_q == 0) return W4_OK;
-    AttnArgs a{};
     const int sms = current_sm_count();
     max_q = std::min(max_q, T);
     rc = attn_workspace(&a, attn_prefill_ws_bytes(kv->batch, q_heads, kv->heads, kv->head_dim, max_q, max_len, sms),
                         workspace, workspace_bytes);
     if (rc) return rc;
-    a.kv = *kv; a.q = q; a.q_tok = q_token_stride; a.q_head = q_head_stride; a.goff = goff;
-    a.out = out; a.lse = lse; a.T = T; a.Hq = q_heads; a.max_q = max_q; a.max_len = max_len;
-    a.scale = scale * 1.4426950408889634f; a.window = window; a.sinks = sinks;
+    // strides of extent 1 are never used, but the tensor map wants valid ones
+    if (q_heads == 1) a.q_head = 8;
+    if (T == 1) a.q_tok = 8;
+    if (a.q_head == 0 || a.q_tok == 0) return W4_ERR_INVALID_ARG;
+    a.goff = goff;
+    a.T = T;
+    a.max_q = max_q;
     return launch_attn_prefill(a, sms, static_cast<cudaStream_t>(stream));
 }
 

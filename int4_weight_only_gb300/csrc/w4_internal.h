@@ -17,6 +17,10 @@ int* device_error_flag();               // device address of the error flag
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                     uint64_t dim0, uint64_t dim1, uint64_t row_stride_bytes,
                     uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle);
+// rank 3 to 5: dims and box innermost first, strides in bytes of dims 1 ..
+bool encode_tmap_nd(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int rank,
+                    const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+                    CUtensorMapSwizzle swizzle);
 
 // ---------------------------------------------------------------- decode
 // Decode kernels (M <= 16): persistent CTAs of 8 consumer warps + 1 producer

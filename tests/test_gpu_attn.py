@@ -229,6 +229,36 @@ def test_prefill_rows_without_a_key(w4):
     prefill(w4, [9, 140, 3], [4, 10, 0], 4, 2, 64, max_len=16)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_prefill_hidden_keys_have_no_influence(w4, bad):
+    """Keys and values that a row does not see, in blocks it reads: hidden by
+    the window from every row, and by the causal mask from the earlier ones."""
+    cache = Paged([600], 2, 64, 16)
+    kv = cache.fill_random()
+    k, v = (torch.tensor(x).bfloat16() for x in kv[0])
+    k[20:180], v[20:180] = bad, bad
+    cache.put(0, k, v)
+    prefill(w4, [200], [600], 4, 2, 64, window=220, sinks=20, cache=cache, kv=[(to64(k), to64(v))])
+    # the last key is not finite: only the last row sees it
+    cache = Paged([300, 40], 2, 128, 32)
+    kv = cache.fill_random()
+    k, v = (torch.tensor(x).bfloat16() for x in kv[0])
+    v[299, :, 5] = bad
+    cache.put(0, k, v)
+    qs = [290, 40]
+    q = randn_bf16(330, 6, 128, seed=9).cuda()
+    goff = torch.tensor([0, 290, 330], dtype=torch.int32, device="cuda")
+    lse = torch.empty(330, 6, device="cuda")
+    out = w4.w4_attn_prefill(q, cache.k, cache.v, goff, cache.kv_len, cache.table, 290, 300, lse=lse)
+    assert w4.w4_get_device_error() == 0
+    kk, vv = to64(k), to64(v)
+    check(out[:289], lse[:289], BO.attention(to64(q[:289]), kk, vv, np.arange(10, 299), 128 ** -0.5), "causal")
+    check(out[290:], lse[290:], BO.attention(to64(q[290:]), *kv[1], np.arange(40), 128 ** -0.5), "other sequence")
+    last = to64(out[289])
+    assert not np.isfinite(last[:, 5]).any() and np.isfinite(np.delete(last, 5, axis=1)).all()
+    assert sum(qs) == 330
+
+
 def test_prefill_long(w4):
     rows = [0, 1, 127, 128, 1000, 2047, 2048, 4099]
     prefill(w4, [4100], [4100], 7, 1, 128, 64, rows=rows)
