@@ -179,6 +179,9 @@ int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
     int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
     if (rc) return rc;
     if (kv->batch == 0) return W4_OK;
+    // the list of units is counted in 32 bits
+    const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)max_len);
+    if ((cap / 64 + 8) * q_heads * kv->batch > (1LL << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
     const int sms = current_sm_count();
     rc = attn_workspace(&a, attn_decode_ws_bytes(kv->batch, q_heads, kv->heads, kv->head_dim, sms), workspace,
                         workspace_bytes);

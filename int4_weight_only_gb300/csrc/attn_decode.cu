@@ -4,21 +4,39 @@
 //
 // The call is bound by reading the visible keys and values once (4 D bytes a
 // key and key-value head); the query heads of a group share that read as the
-// rows of one 16-row mma.sync operand (q_heads / heads > 16: several items).
+// columns of one matrix operand.
 //
-// Work: an item is (sequence, key-value head, group of 16 query heads), a unit
-// of it 64 keys.  The units of all items form one list, cut into equal
-// consecutive shares, one per CTA (two CTAs per SM), so ragged lengths balance
-// without the host knowing them.  An item that spans CTAs is joined from fp32
-// partial sums by the last of them to arrive, in the list's order: the same
-// inputs give the same bits.
+// Work: an item is (sequence, key-value head, group of up to 8 NT query heads),
+// a unit of it 16 keys for each warp of a CTA.  Lengths are known on the device
+// only.  A few items are cut into equal parts, one per CTA.  Otherwise the units
+// of all items form one list, cut into equal consecutive shares, one per CTA; an
+// item counts kItemUnits units more than it has keys for, which is about what
+// starting and joining one costs.  An item that several CTAs work on is joined
+// from fp32 partial sums by the last of them to arrive, in the order of the
+// keys: the same inputs give the same bits.
 //
-// A CTA's four warps take 16-key blocks in turn, each with its own online
-// softmax.  A lane copies exactly the 16-byte pieces that it will use as
-// matrix operands (attn_device.cuh) with cp.async into a private ring in
-// shared memory, kStages blocks deep: no barrier inside the loop, and enough
-// bytes in flight per SM to cover the latency of HBM.  Keys that the token
-// does not see are not read; their pieces are filled with zeros.
+// Both products run transposed, so that keys fill the 16-row side of
+// mma.sync m16n8k16 and the few query heads its 8 columns:
+//   S^T [16 keys x 8 heads] = K Q^T,   O^T [D x 8 heads] += V^T P^T
+// A block is 16 keys.  Each warp has its own blocks and its own ring of
+// kStages of them in shared memory, filled by one TMA each for K and V (a
+// page's 16 rows, 64-column panels, 128-byte swizzle) that its first lane
+// issues, also across the end of an item into the next one; no barrier is
+// shared inside the loop.  Both products sum over an index whose order is free
+// (the head dimension, the keys), so a lane's operand words are whole 16-byte
+// pieces, read without bank conflicts (pi(x) = x / 2 + 4 (x % 2)):
+//   K piece (c, h): key pi(lane / 4) + 8 h, values 32 c + 8 (lane % 4) .. + 7
+//   V piece (c, n): key lane % 4 + 4 n, values 64 c + 8 pi(lane / 4) .. + 7
+// Values of two keys are interleaved in registers (one byte permute a word)
+// and P is transposed with movmatrix.
+//
+// A block is read only if the token sees some of its keys; pieces of the
+// others (which may hold anything) are zeroed in registers and their scores
+// masked.
+//
+// The running maximum is lazy: a warp keeps the maximum it scaled by until a
+// score exceeds it by 2^8, so the common step has no shuffles and no rescaling.
+// l sums the fp32 weights; they are rounded to bf16 only as matrix operands.
 #include "attn_device.cuh"
 #include "w4_internal.h"
 
@@ -27,310 +45,560 @@
 namespace w4 {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr int kCtasPerSm = 2;
-constexpr int kUnitBlocks = kWarps;     // 16-key blocks per unit
-constexpr int kRows = 16;               // query heads per item
+constexpr int kItemUnits = 2;           // what starting and joining an item costs, in units
+constexpr float kLazy = 8.f;            // log2 units the maximum may lag behind
 
-template <int D> __host__ __device__ constexpr int stage_vecs() { return D / 32 * 2 + D / 64 * 4; }   // per lane
-template <int D> __host__ __device__ constexpr int ring_bytes() { return kWarps * kStages * stage_vecs<D>() * 32 * 16; }
-// a partial result: o [kRows][D], then m [kRows], l [kRows]
-template <int D> __host__ __device__ constexpr int slot_floats() { return kRows * D + 2 * kRows; }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
-    const int n = read ? 16 : 0;      // 0: fill with zeros, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
-}
-
-struct SeqWork {
-    int len;                // clamped length
-    KeyBlocks kb;           // its visible 16-key blocks
-    int units;              // per item
+// One CTA per SM; warps and ring depth fill its registers and shared memory.
+template <int D, int NT> struct Shape {
+    static constexpr int warps = D == 64 && NT == 1 ? 16 : 8;
+    static constexpr int threads = 32 * warps;
+    static constexpr int stages = D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 3 : 5);
+    static constexpr int heads = 8 * NT;                    // query heads per item
+    static constexpr int stage_bytes = 16 * D * 2 * 2;      // 16 keys, K and V
+    static constexpr int ring_bytes = warps * stages * stage_bytes;
+    static constexpr int orow = D + 4;                      // padded row of the warps' outputs
+    // join: threads of a part: D / 4 columns x `split` shares of the heads; parts summed at a time
+    static constexpr int split = warps == 16 || NT == 2 ? 4 : 2;
+    static constexpr int groups = threads / (D / 4) / split;
+    // the outputs of half the warps, or the sums of the join's groups
+    static constexpr int join_floats =
+        warps / 2 * heads * orow > groups * heads * D ? warps / 2 * heads * orow : groups * heads * D;
+    // a partial result: o [heads][D], then m [heads], l [heads]
+    static constexpr int slot_floats = heads * (D + 2);
+    static constexpr size_t smem = 1024 + ring_bytes + (size_t)join_floats * 4;
+    static_assert(smem + 2048 <= 227 * 1024, "a CTA fits the SM's shared memory");
 };
 
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b) {
-    SeqWork w;
-    w.len = kv_length(a.kv, b, a.max_len, a.err);
-    w.kb = key_blocks<16>(w.len - 1, w.len - 1, a.window, a.sinks);
-    w.units = max(1, (w.kb.n + kUnitBlocks - 1) / kUnitBlocks);   // 0 keys: the unit writes o = 0
-    return w;
+// Transpose of an 8 x 8 matrix of 16-bit values: lane holds (row lane / 4,
+// columns 2 (lane % 4) and + 1).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 
+// The part of an item that a CTA works on, as one of its warps sees it.
+struct Part {
+    KeyBlocks kb;           // the sequence's visible 16-key blocks
+    int b, it, len;         // sequence, item of it, clamped length
+    int units;              // of each of its items: kItemUnits without keys, then a block per warp each
+    int base;               // first unit of the sequence in the list
+    int first_unit, end;    // of the item; end of the part (in the list)
+    int len_after;          // length of the sequence after b (loaded ahead)
+    int first, n;           // the CTAs that hold parts of the item: the first, how many
+    int c0, nb;             // this warp's first block, number of blocks
+    int issued;             // blocks whose copies are on their way
+    int page;               // page of the next one
+};
+
+// A finished head's output row (four columns) and log-sum-exp.
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_attn_decode(const AttnArgs a) {
-    constexpr int SV = stage_vecs<D>();
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ long long s_scan[kWarps];
-    __shared__ long long s_start;           // first unit of the sequence the share starts in
-    __shared__ int s_b, s_last;
-    __shared__ float s_ml[kWarps][2][kRows];
+__device__ __forceinline__ void put_out(const AttnArgs& a, size_t row, int d, float4 o, float m, float l) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(a.out + row * D + d) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (a.lse && d == 0) a.lse[row] = l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::threads, 1)
+k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+    using S = Shape<D, NT>;
+    constexpr int W = S::warps, NS = S::stages, HP = S::heads, SF = S::slot_floats, OS = S::orow;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[W][NS];
+    __shared__ int s_last, s_abort;
+    __shared__ float s_m[W / 2][HP], s_l[W / 2][HP];
+    uint8_t* ring0 = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    float* so = reinterpret_cast<float*>(ring0 + S::ring_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int Hkv = a.kv.heads, g = a.Hq / Hkv, ngrp = (g + kRows - 1) / kRows;
+    uint8_t* ring = ring0 + warp * NS * S::stage_bytes;
+    const int Hkv = a.kv.heads, g = a.Hq / Hkv, ngrp = (g + HP - 1) / HP;
     const int items = Hkv * ngrp;           // per sequence
     const int B = a.kv.batch;
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(&full[warp][i], 1);
+        fence_mbar_init();
+        if (warp == 0) { s_abort = 0; tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV); }
+    }
+    __syncwarp();
     pdl_wait();
     pdl_launch();
 
-    // ---- this CTA's share of the unit list
-    auto cta_scan = [&](long long v, long long* total) {     // inclusive prefix sum over the CTA
+    // ---- this CTA's work (every warp finds it by itself)
+    const int G = (int)gridDim.x;
+    auto blocks_of = [&](int len) { return key_blocks<16>(len - 1, len - 1, a.window, a.sinks); };
+    auto len_of = [&](int b) { return b < B ? kv_length(a.kv, b, a.max_len, a.err) : 0; };
+    // 0 keys: a unit that writes o = 0
+    auto units_of = [&](int len) { return max(1, (blocks_of(len).n + W - 1) / W); };
+    auto warp_scan = [&](int v) {           // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, v, o);
+            const int t = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += t;
         }
-        __syncthreads();
-        if (lane == 31) s_scan[warp] = v;
-        __syncthreads();
-        long long before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s_scan[w];
-            all += s_scan[w];
-        }
-        *total = all;
-        return v + before;
+        return v;
     };
-    auto units_of = [&](int b) { return b < B ? (long long)seq_work(a, b).units * items : 0LL; };
-    long long total = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        long long t;
-        cta_scan(units_of(b0 + tid), &t);
-        total += t;
+    const int len0 = len_of(lane), real0 = lane < B ? units_of(len0) : 0;
+    int total = lane < B ? items * (real0 + kItemUnits) : 0;
+    for (int b = lane + 32; b < B; b += 32) total += items * (units_of(len_of(b)) + kItemUnits);
+    total = __reduce_add_sync(0xffffffffu, total);
+    // consecutive shares of the list
+    const int share = (total + G - 1) / G;
+    int u0 = share * (int)blockIdx.x, u1 = min(u0 + share, total);
+    Part cur, nxt;
+    cur.b = cur.base = 0;
+    int part = 0;                           // > 0: units of a part, items cut one by one
+    if (B <= 16 && B * items <= G) {
+        // each lane tries a size of part, from an equal share up; the smallest whose
+        // parts are no more than the CTAs wins
+        const int p = max(share - kItemUnits, 1) + lane * (1 + share / 64);
+        int parts = 0;
+        for (int i = 0; i < B; ++i) parts += (__shfl_sync(0xffffffffu, real0, i) + p - 1) / p;
+        const uint32_t fits = __ballot_sync(0xffffffffu, parts * items <= G);
+        const int best = __shfl_sync(0xffffffffu, p, __ffs(fits) - 1);
+        if (fits && best <= share + kItemUnits + share / 4) part = best;
     }
-    const long long share = (total + gridDim.x - 1) / gridDim.x;
-    const long long u0 = share * blockIdx.x, u1 = min(u0 + share, total);
-    if (u0 >= total) return;
-    long long run = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        long long t;
-        const long long n = units_of(b0 + tid), incl = run + cta_scan(n, &t);
-        if (n > 0 && incl > u0 && incl - n <= u0) { s_b = b0 + tid; s_start = incl - n; }
-        run += t;
-        if (run > u0) break;
-    }
-    __syncthreads();
-    int b = s_b;
-    long long base = s_start;
-
-    uint4* ring = reinterpret_cast<uint4*>(smem) + warp * kStages * SV * 32 + lane;
-    const uint32_t ring_s = smem_u32(ring);
-    const int lg = 31 - __clz(a.kv.page_size);
-    const int ki = lane & 3, kj = lane >> 2;
-
-    for (long long u = u0; u < u1;) {
-        const SeqWork w = seq_work(a, b);
-        const int it = (int)((u - base) / w.units);
-        const long long first_unit = base + (long long)it * w.units;
-        const int seg0 = (int)(u - first_unit);
-        const int seg1 = (int)(min(u1, first_unit + w.units) - first_unit);
-        const int hk = it / ngrp, h0 = hk * g + (it - hk * ngrp) * kRows;
-        const int rows = min(kRows, (hk + 1) * g - h0);
-        const int p = w.len - 1;
-
-        // ---- query pieces of the lane's two rows
-        uint4 qf[D / 32][2];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                qf[c][r] = kj + 8 * r < rows
-                    ? __ldg(reinterpret_cast<const uint4*>(a.q + b * a.q_tok + (h0 + kj + 8 * r) * a.q_head +
-                                                           c * 32 + ki * 8))
-                    : make_uint4(0, 0, 0, 0);
-
-        // ---- this warp's blocks of the segment: c0, c0 + kWarps, ... below c1
-        const int c0 = seg0 * kUnitBlocks + warp, c1 = min(seg1 * kUnitBlocks, w.kb.n);
-        const int nb = c0 < c1 ? (c1 - c0 + kWarps - 1) / kWarps : 0;
-        const uint16_t* kh = a.kv.k + (long long)hk * a.kv.k_head_stride;
-        const uint16_t* vh = a.kv.v + (long long)hk * a.kv.v_head_stride;
-        auto seen = [&](int j) { return key_visible(j, p, a.window, a.sinks); };
-        auto page_at = [&](int i) {
-            return i < nb ? page_of(a.kv, b, (w.kb(c0 + i * kWarps) * 16) >> lg, a.err) : 0;
-        };
-        auto issue = [&](int i, int page) {
-            if (i < nb) {
-                const int j0 = w.kb(c0 + i * kWarps) * 16, slot = j0 & (a.kv.page_size - 1);
-                const uint32_t dst = ring_s + (i % kStages) * SV * 512;
-                const uint16_t* kp = kh + page * a.kv.k_page_stride;
-                const uint16_t* vp = vh + page * a.kv.v_page_stride;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int key = kj + 8 * t;
-                    const bool rd = seen(j0 + key);
-                    const uint16_t* src = kp + (slot + key) * a.kv.k_slot_stride + ki * 8;
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) cp_async16(dst + (c * 2 + t) * 512, src + c * 32, rd);
-                }
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int key = 2 * ki + (n & 1) + 8 * (n >> 1);
-                    const bool rd = seen(j0 + key);
-                    const uint16_t* src = vp + (slot + key) * a.kv.v_slot_stride + kj * 8;
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        cp_async16(dst + (D / 32 * 2 + c * 4 + n) * 512, src + c * 64, rd);
-                }
+    if (part) {
+        const int mine = (real0 + part - 1) / part * items, v = warp_scan(mine);
+        const uint32_t past = __ballot_sync(0xffffffffu, v > (int)blockIdx.x);
+        if (!past) return;                  // more CTAs than parts
+        cur.b = __ffs(past) - 1;
+        u0 = (int)blockIdx.x - __shfl_sync(0xffffffffu, v - mine, cur.b);      // part of the sequence
+        cur.len = __shfl_sync(0xffffffffu, len0, cur.b);
+    } else {
+        if (u0 >= total) return;
+        for (int b0 = 0;; b0 += 32) {
+            const int len = b0 ? len_of(b0 + lane) : len0;
+            const int n = b0 + lane < B ? items * (units_of(len) + kItemUnits) : 0, v = warp_scan(n);
+            const uint32_t past = __ballot_sync(0xffffffffu, cur.base + v > u0);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                cur.b = b0 + f;
+                cur.base += __shfl_sync(0xffffffffu, v - n, f);
+                cur.len = __shfl_sync(0xffffffffu, len, f);
+                break;
             }
-            cp_commit();
-        };
-
-        RowState<D> st;
-        st.init();
-        int pg = page_at(0);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            const int nx = page_at(i + 1);
-            issue(i, pg);
-            pg = nx;
+            cur.base += __shfl_sync(0xffffffffu, v, 31);
         }
-        for (int i = 0; i < nb; ++i) {
-            cp_wait<kStages - 2>();
-            const uint4* sp = ring + (i % kStages) * SV * 32;
-            Frag<D> f;
+    }
+    __syncthreads();                        // s_abort is set
+
+    const int lg = 31 - __clz(a.kv.page_size);
+    const int ki = lane & 3, kj = lane >> 2, pj = (kj >> 1) + 4 * (kj & 1);
+    const float sc = a.scale;
+    // shared-memory offsets of the lane's pieces in a stage
+    const uint32_t k_off = pj * 128 + ((ki ^ pj) << 4);                   // ^ 64: the panel's other half
+    const uint32_t v_off = 16 * D * 2 + ki * 128 + ((pj ^ ki) << 4);      // n odd: ^ 64
+
+    auto page_at = [&](const Part& s, int i) {
+        return i < s.nb ? page_of(a.kv, s.b, (s.kb(s.c0 + i * W) * 16) >> lg, a.err) : 0;
+    };
+    // This warp's blocks of units s0 .. s1 - 1 (counted without the first kItemUnits).
+    auto take = [&](Part& s, int s0, int s1) {
+        s.c0 = s0 * W + warp;
+        const int c1 = min(s1 * W, s.kb.n);
+        s.nb = s.c0 < c1 ? (c1 - s.c0 + W - 1) / W : 0;
+        s.issued = 0;
+        s.page = page_at(s, 0);
+    };
+    // The part of sequence s.b's items that starts at unit u of the list.
+    auto start = [&](Part& s, int u) {
+        s.it = (u - s.base) / s.units;
+        s.first_unit = s.base + s.it * s.units;
+        s.end = min(u1, s.first_unit + s.units);
+        s.first = (s.first_unit + kItemUnits) / share;
+        s.n = (s.first_unit + s.units - 1) / share - s.first + 1;
+        take(s, max(u - s.first_unit - kItemUnits, 0), max(s.end - s.first_unit - kItemUnits, 0));
+    };
+    auto after = [&](const Part& s) {
+        Part n = s;
+        if (s.end == s.base + s.units * items) {
+            n.b = s.b + 1;
+            n.base = s.end;
+            n.len = s.len_after;
+            n.kb = blocks_of(n.len);
+            n.units = units_of(n.len) + kItemUnits;
+            n.len_after = len_of(n.b + 1);
+        }
+        start(n, s.end);
+        return n;
+    };
+    cur.kb = blocks_of(cur.len);
+    cur.units = units_of(cur.len) + kItemUnits;
+    if (part) {
+        // the item's units in n runs equal to one, on CTAs first .. first + n - 1
+        const int real = cur.units - kItemUnits;
+        cur.n = (real + part - 1) / part;
+        cur.it = u0 / cur.n;
+        const int x = u0 - cur.it * cur.n, each = real / cur.n, rest = real - each * cur.n;
+        const int s0 = x * each + min(x, rest);
+        cur.first = (int)blockIdx.x - x;
+        cur.first_unit = 0;
+        cur.end = u1 = kItemUnits + 1;        // no list: this part and no other
+        take(cur, s0, s0 + each + (x < rest ? 1 : 0));
+    } else {
+        cur.len_after = len_of(cur.b + 1);
+        start(cur, u0);
+    }
+    uint32_t put = 0, got = 0;              // blocks issued and consumed by this warp
+    bool ok = true;
+    auto issue = [&](Part& s) {
+        const int j0 = s.kb(s.c0 + s.issued * W) * 16;
+        if (lane == 0) {
+            uint64_t* bar = &full[warp][put % NS];
+            uint8_t* dst = ring + (put % NS) * S::stage_bytes;
+            const int slot = j0 & (a.kv.page_size - 1), hk = s.it / ngrp;
+            mbar_arrive_expect_tx(bar, S::stage_bytes);
+            tma_load_5d(dst, &tmK, 0, slot, 0, hk, s.page, bar);
+            tma_load_5d(dst + 16 * D * 2, &tmV, 0, slot, 0, hk, s.page, bar);
+        }
+        ++put;
+        ++s.issued;
+        s.page = page_at(s, s.issued);
+    };
+
+    while (true) {
+        const bool more = cur.end < u1;
+        if (more) nxt = after(cur);
+        if (cur.end - cur.first_unit <= kItemUnits) {      // no blocks, nothing to join
+            if (!more) break;
+            cur = nxt;
+            continue;
+        }
+        auto fill = [&] {                   // keep the ring full, into the next segment too
+            while (ok && put - got < (uint32_t)NS) {
+                if (cur.issued < cur.nb) issue(cur);
+                else if (more && nxt.issued < nxt.nb) issue(nxt);
+                else break;
+            }
+        };
+        fill();
+        const int hk = cur.it / ngrp, h0 = hk * g + (cur.it - hk * ngrp) * HP;
+        const int rows = min(HP, (hk + 1) * g - h0);
+        const int p = cur.len - 1;
+        auto seen = [&](int j) { return key_visible(j, p, a.window, a.sinks); };
+
+        // ---- query pieces: head 8 x + lane / 4
+        uint4 qf[NT][D / 32];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c)
+                qf[x][c] = 8 * x + kj < rows
+                    ? __ldg(reinterpret_cast<const uint4*>(a.q + cur.b * a.q_tok + (h0 + 8 * x + kj) * a.q_head + c * 32 + ki * 8))
+                    : make_uint4(0, 0, 0, 0);
+        // accumulators: o[x][mt][e]: head 8 x + 2 ki + (e & 1), column
+        // 64 (mt / 4) + 8 pj + 2 (mt % 4) + (e >> 1)
+        float o[NT][D / 16][4];
+        float m[NT][2], l[NT][2], off[NT][2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) f.k[c][t] = sp[(c * 2 + t) * 32];
+        for (int x = 0; x < NT; ++x) {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) f.v[c][n] = sp[(D / 32 * 2 + c * 4 + n) * 32];
-            // the slot of block i - 1 was read into registers before this point
-            const int nx = page_at(i + kStages);
-            issue(i + kStages - 1, pg);
-            pg = nx;
-            const int j0 = w.kb(c0 + i * kWarps) * 16;
-            bool vis[2][4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) vis[t][e] = seen(j0 + 8 * t + 2 * ki + (e & 1));
-            attn_step<D>(st, qf, f, vis, a.scale);
+            for (int i = 0; i < D / 16; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
+            m[x][0] = m[x][1] = kNegInf;
+            l[x][0] = l[x][1] = off[x][0] = off[x][1] = 0.f;
         }
-        cp_wait<0>();
-
-        // ---- join the warps in shared memory (the ring is idle)
+        for (int i = 0; i < cur.nb; ++i) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&full[warp][got % NS], (got / NS) & 1, &s_abort, a.err));
+            if (!ok) break;
+            const uint8_t* st = ring + (got % NS) * S::stage_bytes;
+            const int j0 = cur.kb(cur.c0 + i * W) * 16;
+            const bool all = j0 + 15 <= p && (a.window == 0 || p - j0 < a.window || j0 + 16 <= a.sinks);
+            float s[NT][2][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
-            st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 2);
-            if (ki == 0) { s_ml[warp][0][kj + 8 * r] = st.m[r]; s_ml[warp][1][kj + 8 * r] = st.l[r]; }
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[x][0][e] = s[x][1][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                const uint8_t* kp = st + (c >> 1) * 2048 + (k_off ^ ((c & 1) * 64));
+                const uint4 k0 = *reinterpret_cast<const uint4*>(kp), k1 = *reinterpret_cast<const uint4*>(kp + 1024);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) {
+                    mma_bf16_16816(s[x][0], k0.x, k1.x, k0.y, k1.y, qf[x][c].x, qf[x][c].y, s[x][0]);
+                    mma_bf16_16816(s[x][1], k0.z, k1.z, k0.w, k1.w, qf[x][c].z, qf[x][c].w, s[x][1]);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[x][0][e] += s[x][1][e];
+            if (!all) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!seen(j0 + pj + 8 * (e >> 1))) s[x][0][e] = kNegInf;
+            }
+            bool grow = false;
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grow |= (fmaxf(s[x][0][e], s[x][0][e + 2]) - m[x][e]) * sc > kLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(m[x][e], fmaxf(s[x][0][e], s[x][0][e + 2]));
+#pragma unroll
+                        for (int z = 4; z < 32; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+                        // both -inf (nothing seen yet): the factor multiplies zeros
+                        const float f = mx == m[x][e] ? 1.f : ex2_approx((m[x][e] - mx) * sc);
+                        m[x][e] = mx;
+                        off[x][e] = mx == kNegInf ? 0.f : -mx * sc;
+                        l[x][e] *= f;
+#pragma unroll
+                        for (int t = 0; t < D / 16; ++t) { o[x][t][e] *= f; o[x][t][e + 2] *= f; }
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                float w0[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w0[e] = ex2_approx(fmaf(s[x][0][e], sc, off[x][e & 1]));
+                l[x][0] += w0[0] + w0[2];
+                l[x][1] += w0[1] + w0[3];
+                pb[x][0] = movmatrix_trans(pack_bf16x2(w0[0], w0[1]));
+                pb[x][1] = movmatrix_trans(pack_bf16x2(w0[2], w0[3]));
+            }
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 v[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    v[n] = *reinterpret_cast<const uint4*>(st + c * 2048 + n * 512 + (v_off ^ ((n & 1) * 64)));
+                    if (!all && !seen(j0 + ki + 4 * n)) v[n] = make_uint4(0, 0, 0, 0);
+                }
+                const uint32_t *v0 = &v[0].x, *v1 = &v[1].x, *v2 = &v[2].x, *v3 = &v[3].x;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t a0 = prmt(v0[t], v1[t], 0x5410), a1 = prmt(v0[t], v1[t], 0x7632);
+                    const uint32_t a2 = prmt(v2[t], v3[t], 0x5410), a3 = prmt(v2[t], v3[t], 0x7632);
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+                        mma_bf16_16816(o[x][c * 4 + t], a0, a1, a2, a3, pb[x][0], pb[x][1], o[x][c * 4 + t]);
+                }
+            }
+            __syncwarp();                   // the stage is read: refill it
+            ++got;
+            fill();
         }
-        __syncthreads();
-        float* so = reinterpret_cast<float*>(smem);           // [kWarps][kRows][D]
-#pragma unroll
-        for (int nt = 0; nt < D / 8; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                so[(warp * kRows + kj + 8 * (e >> 1)) * D + out_col(nt, e, lane)] = st.o[nt][e];
-        __syncthreads();
 
-        const bool whole = seg0 == 0 && seg1 == w.units;
-        const int first = (int)(first_unit / share), last = (int)((first_unit + w.units - 1) / share);
-        float* slots = a.partial;
-        auto slot_of = [&](int cta) { return slots + (size_t)(2 * cta + (cta > first ? 0 : 1)) * slot_floats<D>(); };
-        float* mine = slot_of((int)blockIdx.x);
-        auto put = [&](int r, int d, float o, float m, float l) {       // a finished row's value
-            a.out[((size_t)b * a.Hq + h0 + r) * D + d] = f32_to_bf16_bits(l == 0.f ? 0.f : o / l);
-            if (a.lse && d == 0)
-                a.lse[(size_t)b * a.Hq + h0 + r] =
-                    l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
+        // ---- join the warps: the upper half's results go through shared memory
+        // into the lower half's, then the lower half's are added in warp order
+        float lw[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float t = l[x][e];
+#pragma unroll
+                for (int z = 4; z < 32; z <<= 1) t += __shfl_xor_sync(0xffffffffu, t, z);
+                lw[x][e] = t;
+            }
+        auto out_row = [&](int x, int e) { return so + ((warp % (W / 2)) * HP + 8 * x + 2 * ki + e) * OS + pj * 8; };
+        auto store_o = [&] {
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (kj == 0) {
+                        s_m[warp % (W / 2)][8 * x + 2 * ki + e] = m[x][e];
+                        s_l[warp % (W / 2)][8 * x + 2 * ki + e] = lw[x][e];
+                    }
+                    float* row = out_row(x, e);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                        for (int t = 0; t < 4; t += 2)
+                            *reinterpret_cast<float4*>(row + c * 64 + 2 * t) = make_float4(
+                                o[x][c * 4 + t][e], o[x][c * 4 + t][e + 2], o[x][c * 4 + t + 1][e], o[x][c * 4 + t + 1][e + 2]);
+                }
         };
-        for (int i = tid; i < rows * D; i += kThreads) {
-            const int r = i / D, d = i - r * D;
-            float m = kNegInf, l = 0.f, o = 0.f;
+        if (warp >= W / 2) store_o();
+        __syncthreads();
+        if (warp < W / 2) {
 #pragma unroll
-            for (int x = 0; x < kWarps; ++x) m = fmaxf(m, s_ml[x][0][r]);
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int x = 0; x < kWarps; ++x) {
-                const float mw = s_ml[x][0][r];
-                const float fac = mw == m ? 1.f : ex2_approx((mw - m) * a.scale);
-                l += fac * s_ml[x][1][r];
-                o += fac * so[(x * kRows + r) * D + d];
+                for (int e = 0; e < 2; ++e) {
+                    const float m2 = s_m[warp][8 * x + 2 * ki + e], mr = fmaxf(m[x][e], m2);
+                    const float f = m[x][e] == mr ? 1.f : ex2_approx((m[x][e] - mr) * sc);
+                    const float f2 = m2 == mr ? 1.f : ex2_approx((m2 - mr) * sc);
+                    lw[x][e] = lw[x][e] * f + s_l[warp][8 * x + 2 * ki + e] * f2;
+                    m[x][e] = mr;
+                    const float* row = out_row(x, e);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const float2 z = *reinterpret_cast<const float2*>(row + c * 64 + 2 * t);
+                            o[x][c * 4 + t][e] = o[x][c * 4 + t][e] * f + z.x * f2;
+                            o[x][c * 4 + t][e + 2] = o[x][c * 4 + t][e + 2] * f + z.y * f2;
+                        }
+                }
+            __syncwarp();                   // s_m and s_l of this warp are read
+            store_o();
+        }
+        __syncthreads();
+
+        const int n = cur.n;
+        // a CTA has at most two parts of items that others work on too: one that began
+        // before it, one that goes on after it
+        auto slot_of = [&](int x) { return a.partial + (size_t)(2 * (cur.first + x) + (x ? 0 : 1)) * SF; };
+        float* mine = slot_of((int)blockIdx.x - cur.first);
+        const size_t row0 = (size_t)cur.b * a.Hq + h0;
+        for (int i = tid; i < rows * (D / 4); i += S::threads) {
+            const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+            float mr = kNegInf, lr = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < W / 2; ++x) mr = fmaxf(mr, s_m[x][r]);
+#pragma unroll
+            for (int x = 0; x < W / 2; ++x) {
+                const float mw = s_m[x][r], f = mw == mr ? 1.f : ex2_approx((mw - mr) * sc);
+                const float4 t = *reinterpret_cast<const float4*>(so + (x * HP + r) * OS + d);
+                lr += f * s_l[x][r];
+                v.x += f * t.x; v.y += f * t.y; v.z += f * t.z; v.w += f * t.w;
             }
-            if (whole) {
-                put(r, d, o, m, l);
+            if (n == 1) {
+                put_out<D>(a, row0 + r, d, v, mr, lr);
             } else {
-                mine[r * D + d] = o;
-                if (d == 0) { mine[kRows * D + r] = m; mine[kRows * D + kRows + r] = l; }
+                *reinterpret_cast<float4*>(mine + r * D + d) = v;
+                if (d == 0) { mine[HP * D + r] = mr; mine[HP * D + HP + r] = lr; }
             }
         }
-        if (!whole) {
-            const int n = last - first + 1;
+        if (n > 1) {
             __syncthreads();
             if (tid == 0) {
-                const bool is_last = atom_add_acq_rel_gpu(a.tickets + first, 1) == n - 1;
-                if (is_last) a.tickets[first] = 0;
+                const bool is_last = atom_add_acq_rel_gpu(a.tickets + cur.first, 1) == n - 1;
+                if (is_last) a.tickets[cur.first] = 0;
                 s_last = is_last;
             }
             __syncthreads();
             if (s_last) {
-                // factors exp2((m_i - m) scale) of the parts, then the sums in part order
-                float* fac = reinterpret_cast<float*>(smem);          // [n][kRows]
-                for (int r = warp; r < rows; r += kWarps) {
-                    float m = kNegInf, l = 0.f;
-                    for (int i = lane; i < n; i += 32) m = fmaxf(m, ld_cg(slot_of(first + i) + kRows * D + r));
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                // the heads' maxima and sums, then the weighted sums of the parts, the
+                // thread groups taking parts in turn, their sums added in group order
+                for (int r = warp; r < rows; r += W) {
+                    float mr = kNegInf, lr = 0.f;
                     for (int i = lane; i < n; i += 32) {
-                        const float* s = slot_of(first + i) + kRows * D;
-                        const float mi = ld_cg(s + r), fi = mi == m ? 1.f : ex2_approx((mi - m) * a.scale);
-                        fac[i * kRows + r] = fi;
-                        l += fi * ld_cg(s + kRows + r);
+                        const float* s = slot_of(i) + HP * D + r;
+                        const float mi = __ldcg(s), li = __ldcg(s + HP), mx = fmaxf(mr, mi);
+                        lr = lr * (mr == mx ? 1.f : ex2_approx((mr - mx) * sc)) +
+                             li * (mi == mx ? 1.f : ex2_approx((mi - mx) * sc));
+                        mr = mx;
                     }
-                    l = warp_sum(l);
-                    if (lane == 0) { s_ml[0][0][r] = m; s_ml[0][1][r] = l; }
+                    float mx = mr;
+#pragma unroll
+                    for (int z = 16; z; z >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
+                    lr = warp_sum(lr * (mr == mx ? 1.f : ex2_approx((mr - mx) * sc)));
+                    if (lane == 0) { s_m[0][r] = mx; s_l[0][r] = lr; }
                 }
                 __syncthreads();
-                for (int i = tid; i < rows * D; i += kThreads) {
-                    const int r = i / D, d = i - r * D;
-                    float o = 0.f;
-#pragma unroll 8
-                    for (int x = 0; x < n; ++x)
-                        o += fac[x * kRows + r] * ld_cg(slot_of(first + x) + r * D + d);
-                    put(r, d, o, s_ml[0][0][r], s_ml[0][1][r]);
+                constexpr int HH = HP / S::split;
+                const int col = (tid % (D / 4)) * 4, h1 = tid / (D / 4) % S::split * HH, grp = tid / (D / 4) / S::split;
+                float4 acc[HH];
+                float mh[HH];
+#pragma unroll
+                for (int r = 0; r < HH; ++r) {
+                    acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    mh[r] = h1 + r < rows ? s_m[0][h1 + r] : 0.f;
+                }
+                constexpr int U = 24 / HH;          // parts whose loads are in flight together
+                for (int i0 = grp; i0 < n; i0 += U * S::groups) {
+                    float4 t[U][HH];
+                    float mi[U][HH];
+#pragma unroll
+                    for (int x = 0; x < U; ++x) {
+                        const int i = i0 + x * S::groups;
+                        const float* s = slot_of(min(i, n - 1));
+#pragma unroll
+                        for (int r = 0; r < HH; ++r) {
+                            const bool in = h1 + r < rows && i < n;
+                            mi[x][r] = in ? __ldcg(s + HP * D + h1 + r) : kNegInf;
+                            t[x][r] = in ? __ldcg(reinterpret_cast<const float4*>(s + (h1 + r) * D + col))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < U; ++x)
+#pragma unroll
+                        for (int r = 0; r < HH; ++r) {
+                            const float f = mi[x][r] == mh[r] ? 1.f : ex2_approx((mi[x][r] - mh[r]) * sc);
+                            acc[r].x += f * t[x][r].x; acc[r].y += f * t[x][r].y;
+                            acc[r].z += f * t[x][r].z; acc[r].w += f * t[x][r].w;
+                        }
+                }
+#pragma unroll
+                for (int r = 0; r < HH; ++r)
+                    *reinterpret_cast<float4*>(so + (grp * HP + h1 + r) * D + col) = acc[r];
+                __syncthreads();
+                for (int i = tid; i < rows * (D / 4); i += S::threads) {
+                    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < S::groups; ++x) {
+                        const float4 t = *reinterpret_cast<const float4*>(so + (x * HP + r) * D + d);
+                        v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+                    }
+                    put_out<D>(a, row0 + r, d, v, s_m[0][r], s_l[0][r]);
                 }
             }
         }
+        if (!more) break;
         __syncthreads();
-        u = first_unit + seg1;
-        if (u == base + (long long)w.units * items) { base = u; ++b; }
+        cur = nxt;
     }
+    // a wait ran out: the copies already issued land before the CTA ends
+    if (!ok && lane == 0)
+        for (; got != put; ++got) mbar_wait_drain(&full[warp][got % NS], (got / NS) & 1, a.err);
 }
 
-template <int D>
+template <int D, int NT>
 int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-    constexpr int bytes = ring_bytes<D>();
-    static_assert(kWarps * kRows * D * 4 <= bytes, "the warps' outputs fit the ring");
-    if (cudaFuncSetAttribute(k_attn_decode<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    using S = Shape<D, NT>;
+    CUtensorMap tmK, tmV;
+    const uint64_t dims[5] = {64, (uint64_t)a.kv.page_size, D / 64, (uint64_t)a.kv.heads, (uint64_t)a.kv.pages};
+    const uint64_t ks[4] = {(uint64_t)a.kv.k_slot_stride * 2, 128, (uint64_t)a.kv.k_head_stride * 2,
+                            (uint64_t)a.kv.k_page_stride * 2};
+    const uint64_t vs[4] = {(uint64_t)a.kv.v_slot_stride * 2, 128, (uint64_t)a.kv.v_head_stride * 2,
+                            (uint64_t)a.kv.v_page_stride * 2};
+    const uint32_t box[5] = {64, 16, D / 64, 1, 1};
+    if (!encode_tmap_nd(&tmK, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv.k, 5, dims, ks, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_nd(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv.v, 5, dims, vs, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4_ERR_CUDA;
+    const int grid = sm_count, bytes = (int)S::smem;
+    if (cudaFuncSetAttribute(k_attn_decode<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
         return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sm_count * kCtasPerSm));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(S::threads);
+    cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_decode<D>, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k_attn_decode<D, NT>, tmK, tmV, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
+
+// Two tiles of 8 heads share the keys and values that one would read twice.
+int head_tiles(int Hq, int Hkv) { return Hq / Hkv <= 8 ? 1 : 2; }
 
 }  // namespace
 
-size_t attn_decode_ws_bytes(int, int, int, int D, int sm_count) {
-    return (size_t)sm_count * kCtasPerSm * 2 * (kRows * D + 2 * kRows) * sizeof(float);
+size_t attn_decode_ws_bytes(int, int Hq, int Hkv, int D, int sm_count) {
+    return (size_t)sm_count * 2 * 8 * head_tiles(Hq, Hkv) * (D + 2) * sizeof(float);
 }
 
 int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-    return a.kv.head_dim == 128 ? go<128>(a, sm_count, stream) : go<64>(a, sm_count, stream);
+    const int nt = head_tiles(a.Hq, a.kv.heads);
+    if (a.kv.head_dim == 128) return nt == 1 ? go<128, 1>(a, sm_count, stream) : go<128, 2>(a, sm_count, stream);
+    return nt == 1 ? go<64, 1>(a, sm_count, stream) : go<64, 2>(a, sm_count, stream);
 }
 
 }  // namespace w4
