@@ -602,13 +602,12 @@ W4_API int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_
  *        W4_ERR_PAGE_TABLE, longer rows raise W4_ERR_GROUP_TOKENS and stay
  *        unwritten.
  *  q_heads a multiple of heads, at most 128 times as many; scale > 0.
- *  workspace: at least w4_attn_workspace_bytes(...) bytes, zero-filled once
- *        (it starts with W4_WORKSPACE_COUNTER_BYTES of arrival counters that
- *        every call leaves at zero; it can be the linear layers' workspace).
- *        Calls that share one must not overlap on the GPU.
+ *  workspace (decode): at least w4_attn_decode_workspace_bytes(...) bytes,
+ *        zero-filled once (it starts with W4_WORKSPACE_COUNTER_BYTES of arrival
+ *        counters that every call leaves at zero; it can be the linear layers'
+ *        workspace).  Calls that share one must not overlap on the GPU.
  * ------------------------------------------------------------------------- */
-W4_API size_t w4_attn_workspace_bytes(int batch, int q_heads, int heads, int head_dim,
-                                      int max_q, int max_len);
+W4_API size_t w4_attn_decode_workspace_bytes(int q_heads, int heads, int head_dim);
 W4_API int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
                           long long q_head_stride, uint16_t* out, float* lse, int q_heads,
                           int max_len, float scale, int window, int sinks, void* workspace,
@@ -616,8 +615,7 @@ W4_API int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_
 W4_API int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
                            long long q_head_stride, const int32_t* goff, uint16_t* out,
                            float* lse, int T, int q_heads, int max_q, int max_len, float scale,
-                           int window, int sinks, void* workspace, size_t workspace_bytes,
-                           void* stream);
+                           int window, int sinks, void* stream);
 
 /* ---------------------------------------------------------------------------
  * w4_get_device_error - synchronizes `stream`, then returns and clears the

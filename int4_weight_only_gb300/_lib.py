@@ -49,11 +49,11 @@ _SIGS = {
     "w4_rope_freqs": (_c_int, [_c_int, ctypes.c_double, _c_int] + [ctypes.c_double] * 4 + [_vp] * 2),
     "w4_rope_append": (_c_int, [_vp] + [_vp, _c_ll, _c_ll] * 3 + [_vp] * 3
                        + [ctypes.c_float, _c_int, _c_int, _vp, _c_int, _c_int, _vp]),
-    "w4_attn_workspace_bytes": (_c_size, [_c_int] * 6),
+    "w4_attn_decode_workspace_bytes": (_c_size, [_c_int] * 3),
     "w4_attn_decode": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _c_int, _c_int, ctypes.c_float,
                                 _c_int, _c_int, _vp, _c_size, _vp]),
     "w4_attn_prefill": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _vp] + [_c_int] * 4
-                        + [ctypes.c_float, _c_int, _c_int, _vp, _c_size, _vp]),
+                        + [ctypes.c_float, _c_int, _c_int, _vp]),
     "w4_get_device_error": (_c_int, [_vp]),
     "w4_set_wait_limit": (_c_int, [ctypes.c_longlong, _vp]),
     "w4_set_fault_injection": (_c_int, [_c_int, _vp]),
@@ -720,9 +720,8 @@ def w4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     return q_out
 
 
-def w4_attn_workspace_bytes(batch: int, q_heads: int, heads: int, head_dim: int, max_q: int,
-                            max_len: int) -> int:
-    return int(load().w4_attn_workspace_bytes(batch, q_heads, heads, head_dim, max_q, max_len))
+def w4_attn_decode_workspace_bytes(q_heads: int, heads: int, head_dim: int) -> int:
+    return int(load().w4_attn_decode_workspace_bytes(q_heads, heads, head_dim))
 
 
 def _attn_outputs(q, out, lse):
@@ -758,14 +757,14 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         (kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), _ptr(lse), Hq, max_len,
          D ** -0.5 if scale is None else scale, window, sinks),
         (_stream(q, stream),), q.device, workspace,
-        lambda: lib.w4_attn_workspace_bytes(B, Hq, k_cache.shape[1], D, 1, max_len))
+        lambda: lib.w4_attn_decode_workspace_bytes(Hq, k_cache.shape[1], D))
     return out
 
 
 def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     goff: torch.Tensor, kv_len: torch.Tensor, table: torch.Tensor, max_q: int,
                     max_len: int, scale: Optional[float] = None, window: int = 0, sinks: int = 0,
-                    out=None, lse=None, workspace=None, stream=None) -> torch.Tensor:
+                    out=None, lse=None, stream=None) -> torch.Tensor:
     """out [T, Hq, D] bf16: attention of many tokens per sequence over the paged
     cache.  Rows goff[b] .. goff[b + 1] - 1 of q are the last tokens of sequence
     b (their keys already written); max_q bounds their number, max_len kv_len.
@@ -779,14 +778,9 @@ def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if q.numel() == 0:
         return out
     qs = q.stride()
-    lib = load()
-    _call_with_workspace(
-        lib.w4_attn_prefill, "w4_attn_prefill",
-        (kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(), _ptr(lse), T, Hq, max_q,
-         max_len, D ** -0.5 if scale is None else scale, window, sinks),
-        (_stream(q, stream),), q.device, workspace,
-        lambda: lib.w4_attn_workspace_bytes(table.shape[0], Hq, k_cache.shape[1], D, min(max_q, T),
-                                            max_len))
+    _check("w4_attn_prefill", load().w4_attn_prefill(
+        kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(), _ptr(lse), T, Hq, max_q,
+        max_len, D ** -0.5 if scale is None else scale, window, sinks, _stream(q, stream)))
     return out
 
 

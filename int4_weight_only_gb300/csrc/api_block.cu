@@ -164,12 +164,10 @@ int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
     return launch_rope_append(a, static_cast<cudaStream_t>(stream));
 }
 
-size_t w4_attn_workspace_bytes(int batch, int q_heads, int heads, int head_dim, int max_q, int max_len) {
-    if (batch < 0 || q_heads < 1 || heads < 1 || q_heads % heads || head_dim < 1 || max_q < 0 || max_len < 0) return 0;
+size_t w4_attn_decode_workspace_bytes(int q_heads, int heads, int head_dim) {
+    if (q_heads < 1 || heads < 1 || q_heads % heads || head_dim < 1) return 0;
     const int sms = current_sm_count();
-    if (sms < 1) return 0;
-    return kCounterBytes + std::max(attn_decode_ws_bytes(batch, q_heads, heads, head_dim, sms),
-                                    attn_prefill_ws_bytes(batch, q_heads, heads, head_dim, max_q, max_len, sms));
+    return sms < 1 ? 0 : kCounterBytes + attn_decode_ws_bytes(q_heads, heads, head_dim, sms);
 }
 
 int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
@@ -183,7 +181,7 @@ int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
     const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)max_len);
     if ((cap / 64 + 8) * q_heads * kv->batch > (1LL << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
     const int sms = current_sm_count();
-    rc = attn_workspace(&a, attn_decode_ws_bytes(kv->batch, q_heads, kv->heads, kv->head_dim, sms), workspace,
+    rc = attn_workspace(&a, attn_decode_ws_bytes(q_heads, kv->heads, kv->head_dim, sms), workspace,
                         workspace_bytes);
     if (rc) return rc;
     a.T = kv->batch;
@@ -193,28 +191,24 @@ int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
 
 int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
                     const int32_t* goff, uint16_t* out, float* lse, int T, int q_heads, int max_q, int max_len,
-                    float scale, int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
+                    float scale, int window, int sinks, void* stream) {
     AttnArgs a{};
-    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
+    const int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
     if (rc) return rc;
     if (!goff) return W4_ERR_NULL_PTR;
     if (T < 0 || max_q < 0) return W4_ERR_INVALID_ARG;
     if (!aligned(goff, 4)) return W4_ERR_MISALIGNED;
-    if (kv->batch > 65535 || kv->heads > 65535) return W4_ERR_UNSUPPORTED_SHAPE;
     if (kv->batch == 0 || T == 0 || max_q == 0) return W4_OK;
-    const int sms = current_sm_count();
-    max_q = std::min(max_q, T);
-    rc = attn_workspace(&a, attn_prefill_ws_bytes(kv->batch, q_heads, kv->heads, kv->head_dim, max_q, max_len, sms),
-                        workspace, workspace_bytes);
-    if (rc) return rc;
+    a.err = device_error_flag();
+    if (!a.err) return W4_ERR_CUDA;
     // strides of extent 1 are never used, but the tensor map wants valid ones
     if (q_heads == 1) a.q_head = 8;
     if (T == 1) a.q_tok = 8;
     if (a.q_head == 0 || a.q_tok == 0) return W4_ERR_INVALID_ARG;
     a.goff = goff;
     a.T = T;
-    a.max_q = max_q;
-    return launch_attn_prefill(a, sms, static_cast<cudaStream_t>(stream));
+    a.max_q = std::min(max_q, T);
+    return launch_attn_prefill(a, current_sm_count(), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -591,7 +591,7 @@ int head_tiles(int Hq, int Hkv) { return Hq / Hkv <= 8 ? 1 : 2; }
 
 }  // namespace
 
-size_t attn_decode_ws_bytes(int, int Hq, int Hkv, int D, int sm_count) {
+size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count) {
     return (size_t)sm_count * 2 * 8 * head_tiles(Hq, Hkv) * (D + 2) * sizeof(float);
 }
 

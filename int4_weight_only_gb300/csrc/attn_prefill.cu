@@ -5,9 +5,17 @@
 //   S = Q K^T,  P = exp2(c S - c m),  O = P V / sum(P)
 //
 // A query tile is 128 rows (tokens x query heads of one key-value head, so the
-// heads of a group share the keys and values), a step 128 keys.  One CTA per
-// SM works on two tiles A and B over the same keys: while the tensor cores
-// compute one tile's S and O, the other tile's warps take its exponentials.
+// heads of a group share the keys and values), a step 128 keys.  An item is two
+// neighbouring tiles A and B over the same keys: while the tensor cores compute
+// one tile's S and O, the other tile's warps take its exponentials.
+//
+// Work: one CTA per SM.  Many items: each CTA takes whole items, those with the
+// most steps first (under a causal mask a sequence's last tokens), in turns that
+// alternate direction, so that the sums balance.  Few items, or a few more than
+// one turn: the CTAs of a thread-block cluster share an item's steps; at its end
+// each writes its partial O, m and l by rows into the shared memory of the
+// others, and each joins its own share of the rows, in the order of the keys.
+// Either way the same inputs give the same bits.
 //
 // TMEM (512 columns): S_A, S_B (128 each), O_A, O_B (D each).  P is written as
 // bf16 over the S it came from and is the next product's A operand, straight
@@ -19,18 +27,19 @@
 // the fp32 weights, before they are rounded to bf16 as matrix operands.
 //
 // Warp roles (384 threads):
-//   warps 0-3, 4-7  softmax of tile A, B: one row per thread
-//   warp 8          TMA: Q once, then K and V blocks into a ring of slots (K
-//                   in even, V in odd slots), one box per page and 64 columns;
-//                   pages past the sequence's end are read out of bounds of
-//                   the tensor map, which fills them with zeros
-//   warp 9          TMEM allocation; one thread issues the MMAs, for each step
+//   warps 0-3, 4-7  softmax of tile A, B (one row per thread), O to memory
+//   warp 8          TMA: Q of an item, then K and V blocks into a ring of slots
+//                   (K in even, V in odd slots), one box per page and 64
+//                   columns; pages past the sequence's end are read out of
+//                   bounds of the tensor map, which fills them with zeros.  It
+//                   runs ahead into the next item
+//   warp 9          TMEM allocation; issues the MMAs, for each step
 //                   O_A += P_A V, S_A = Q_A K', O_B += P_B V, S_B = Q_B K'
 //   warps 10, 11    release V blocks to the MMAs.  In a block that not every
 //                   row sees entirely, a weight of zero does not make a NaN
 //                   harmless: slots past the end are zeroed, and if a hidden
-//                   slot holds a NaN or infinity the tiles are recomputed row
-//                   by row at the end (attend_row)
+//                   slot holds a NaN or infinity the part is recomputed row by
+//                   row at its end (attend_row)
 // Every wait is bounded (mbar_wait); copies and MMAs in flight are drained
 // before the CTA ends.
 #include "attn_device.cuh"
@@ -51,40 +60,109 @@ template <int D> __host__ __device__ constexpr int slots() { return D == 128 ? 4
 template <int D> __host__ __device__ constexpr int slot_bytes() { return kN * D * 2; }
 
 struct Ctl {
-    uint64_t qfull;
+    uint64_t qfull, qempty;
     uint64_t full[8], empty[8], vready[8];
-    uint64_t sfull[2], pready[2], ofull[2];
+    uint64_t sfull[2], pready[2][2], ofull[2], oempty[2];
     uint64_t drain;
     uint32_t tmem;
     int abort;
-    int bad;            // a block that some row does not see holds a non-finite value
+    // by V-releasing warp and part number mod 4: a slot that some row does not see
+    // holds a non-finite value.  No warp is more than two parts ahead of another
+    int bad[2][4];
 };
+
+// The join of an item's parts, over the space of Q and the ring: rows of o by
+// tile, part and row of this CTA's share, padded so that a warp's rows fall into
+// different banks; then m and l of the same rows.
+template <int D> __host__ __device__ constexpr int join_row() { return D + 4; }
 
 template <int D> __host__ __device__ constexpr size_t smem_total() {
     return 1024 + 2 * kTile * D * 2 + (size_t)slots<D>() * slot_bytes<D>() + sizeof(Ctl);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc]: the A operand is 128 lanes of bf16
-// pairs, 8 columns per 16-wide step.
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        :: "r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+// Shared-memory descriptors for the 128-byte swizzled layouts differ only in
+// their low word (start address >> 4, and for MN-major operands the distance of
+// the 64-column panels >> 4 in the upper half); the high word holds the 1024
+// bytes between groups of 8 rows, the version and the swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr, uint32_t panel_bytes) {
+    return ((saddr >> 4) & 0x3FFFu) | ((panel_bytes >> 4) << 16);
 }
 
-// Shared-memory descriptor of a B operand stored [k][n] with n contiguous (MN
-// major), 128-byte swizzle: 64-column panels of 128-byte rows; panels LBO
-// apart, groups of 8 rows (1024 bytes) SBO apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t panel_bytes) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(panel_bytes >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
+// The MMA warp stays converged, so that operands can live in uniform registers,
+// and one elected lane (the same every time) issues: MMAs and the commits that
+// wait for them.
+// D[tmem] (+)= A[smem] * B[smem], operands by their descriptors' low words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi) : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]: the A operand is 128 lanes of bf16 pairs, 8
+// columns per 16-wide step.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHi) : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :: "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_nctas() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
+                 :: "r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 128 consecutive columns of this warp's 32 TMEM lanes (one lane per thread),
+// with the wait in the same statement.
+__device__ __forceinline__ void tmem_ld_x128(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+        "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+        "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+        "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+        "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]),
+          "=r"(r[64]), "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]),
+          "=r"(r[72]), "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]),
+          "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]),
+          "=r"(r[88]), "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]),
+          "=r"(r[96]), "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]),
+          "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+          "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]),
+          "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]), "=r"(r[127])
+        : "r"(taddr) : "memory");
 }
 
 // 16 TMEM columns of this warp's lanes from registers.
@@ -117,22 +195,107 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// One row by itself, straight from the definition: used only when a hidden
-// value is not finite, where the matrix product would let it through.
+// The items, and a CTA's work on them.
+struct Walk {
+    int b, hk, y;               // the item: sequence, key-value head, pair of tiles
+    int turn;                   // whole items: this CTA's turn
+    int x, n, c0, c1;           // the part: number x of n, steps c0 .. c1 - 1
+    // of the sequence
+    int t0, nq, len, pairs;
+    // of the item: first token, tokens, tiles, positions of the first and last token
+    int i0, n_tok, ntile, p0, p1;
+    KeyBlocks kb;
+    int steps;                  // kb.n, or 1 where no row sees a key (the step writes o = 0)
+
+    __device__ __forceinline__ void seq(const AttnArgs& a, int tpt, int o0, int o1, int len_b) {
+        t0 = o0;
+        nq = o1 - o0;
+        if (o0 < 0 || o1 < o0 || o1 > a.T || nq > a.max_q) {
+            atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
+            t0 = nq = 0;
+        }
+        len = len_b;
+        pairs = (nq + 2 * tpt - 1) / (2 * tpt);
+    }
+    __device__ __forceinline__ void item(const AttnArgs& a, int tpt) {
+        i0 = y * 2 * tpt;
+        n_tok = min(nq - i0, 2 * tpt);
+        ntile = n_tok > tpt ? 2 : 1;
+        p0 = len - nq + i0;
+        p1 = p0 + n_tok - 1;
+        kb = key_blocks<kN>(max(p0, 0), p1, a.window, a.sinks);
+        steps = max(kb.n, 1);
+    }
+    // item number q, in the order of the last pairs of all sequences and heads, the
+    // pairs before them, and so on; false where a sequence has no such pair
+    __device__ __forceinline__ bool pick(const AttnArgs& a, int tpt, int q) {
+        const int bh = a.kv.batch * a.kv.heads, back = q / bh, i = q - back * bh;
+        b = i / a.kv.heads;
+        hk = i - b * a.kv.heads;
+        seq(a, tpt, __ldg(a.goff + b), __ldg(a.goff + b + 1), kv_length(a.kv, b, a.max_len, a.err));
+        y = pairs - 1 - back;
+        if (y < 0) return false;
+        item(a, tpt);
+        return true;
+    }
+    // whole items: the one of this turn or a later one; false when there is none
+    __device__ __forceinline__ bool settle(const AttnArgs& a, int tpt) {
+        const int G = (int)gridDim.x;
+        const int items = (a.max_q + 2 * tpt - 1) / (2 * tpt) * a.kv.batch * a.kv.heads;
+        for (; turn * G < items; ++turn) {
+            const int q = turn * G + ((turn & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x);
+            if (q >= items || !pick(a, tpt, q)) continue;
+            x = c0 = 0;
+            n = 1;
+            c1 = steps;
+            return true;
+        }
+        return false;
+    }
+    template <bool SPLIT>
+    __device__ __forceinline__ bool next(const AttnArgs& a, int tpt) {
+        if (SPLIT) return false;            // one item per cluster
+        ++turn;
+        return settle(a, tpt);
+    }
+    // steps of tile i: tile A ends where its own last token does
+    __device__ __forceinline__ int tile_steps(int i, int tpt) const {
+        if (i == ntile - 1) return kb.n;
+        const int q = p0 + tpt - 1;
+        if (q < 0) return 0;
+        const int blk = q / kN;
+        return blk < kb.ns ? blk + 1 : kb.ns + max(blk - kb.w0 + 1, 0);
+    }
+    // first step of part i when an item's steps are cut into n runs equal to one
+    __device__ __forceinline__ int cut(int i) const {
+        const int each = steps / n, rest = steps - each * n;
+        return i * each + min(i, rest);
+    }
+    // every row of the item sees all of block j0
+    __device__ __forceinline__ bool all_see(const AttnArgs& a, int j0) const {
+        return j0 + kN - 1 <= p0 && (a.window == 0 || p1 - j0 < a.window || j0 + kN <= a.sinks);
+    }
+};
+
+// One row of a part by itself, straight from the definition: used only when a
+// hidden value is not finite, where the matrix product would let it through.
+// Blocks c0 .. c1 - 1; a whole row goes to `out`, a part's to the join's row at
+// shared::cluster address dst_o, m and l to dst_ml.
 template <int D>
-__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hk, int head, int tok, int p) {
+__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hk, int head, int tok, int p, KeyBlocks kb,
+                                        int c0, int c1, uint32_t dst_o, uint32_t dst_ml) {
     const int lg = 31 - __clz(a.kv.page_size);
     const uint16_t* q = a.q + tok * a.q_tok + head * a.q_head;
-    const KeyBlocks kb = key_blocks<16>(p, p, a.window, a.sinks);
+    const size_t row = (size_t)tok * a.Hq + head;
     float m = kNegInf, l = 0.f;
     for (int d0 = -32; d0 < D; d0 += 32) {          // first pass: m and l; then 32 columns a pass
         float o[32];
         for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        for (int c = 0; c < kb.n * 16; ++c) {
-            const int j = kb(c >> 4) * 16 + (c & 15);
+        for (int c = c0 * kN; c < c1 * kN; ++c) {
+            const int j = kb(c / kN) * kN + c % kN;
             if (!key_visible(j, p, a.window, a.sinks)) continue;
-            const int page = page_of(a.kv, b, j >> lg, a.err), slot = j & (a.kv.page_size - 1);
-            const uint16_t* k = a.kv.k + page * a.kv.k_page_stride + hk * a.kv.k_head_stride + slot * a.kv.k_slot_stride;
+            const int page = page_of(a.kv, b, j >> lg, a.err), at = j & (a.kv.page_size - 1);
+            const uint16_t* k = a.kv.k + page * a.kv.k_page_stride + hk * a.kv.k_head_stride + at * a.kv.k_slot_stride;
             float s = 0.f;
             for (int d = 0; d < D; ++d) s = fmaf(bf16_bits_to_f32(q[d]), bf16_bits_to_f32(k[d]), s);
             if (d0 < 0) {
@@ -141,18 +304,27 @@ __device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hk, int he
                 m = mn;
             } else {
                 const uint16_t* v = a.kv.v + page * a.kv.v_page_stride + hk * a.kv.v_head_stride +
-                                    slot * a.kv.v_slot_stride + d0;
-                const float w = ex2_approx((s - m) * a.scale) / l;
+                                    at * a.kv.v_slot_stride + d0;
+                const float w = ex2_approx((s - m) * a.scale);
                 for (int i = 0; i < 32; ++i) o[i] = fmaf(w, bf16_bits_to_f32(v[i]), o[i]);
             }
         }
-        if (d0 >= 0)
-            for (int i = 0; i < 32; ++i) a.out[((size_t)tok * a.Hq + head) * D + d0 + i] = f32_to_bf16_bits(o[i]);
+        if (d0 < 0) continue;
+        for (int i = 0; i < 32; ++i) {
+            if (dst_o) st_shared_cluster(dst_o + (d0 + i) * 4, o[i]);
+            else a.out[row * D + d0 + i] = f32_to_bf16_bits(l == 0.f ? 0.f : o[i] / l);
+        }
     }
-    if (a.lse) a.lse[(size_t)tok * a.Hq + head] = l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
+    if (dst_o) {
+        st_shared_cluster(dst_ml, m);
+        st_shared_cluster(dst_ml + 4, l);
+    } else if (a.lse) {
+        a.lse[row] = l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
+    }
 }
 
-template <int D>
+// SPLIT: the CTAs of a cluster share the steps of one item.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const int tpt) {
@@ -166,51 +338,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     Ctl* ctl = reinterpret_cast<Ctl*>(ring + NS * SB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    pdl_wait();
-    pdl_launch();
-    // ---- this CTA's tiles: the last tokens of every sequence first (under a
-    // causal mask they see the most keys)
-    const int nbh = a.kv.batch * a.kv.heads;
-    const int y = blockIdx.x / nbh, bh = blockIdx.x - y * nbh;
-    const int b = bh / a.kv.heads, hk = bh - b * a.kv.heads;
-    const int g = a.Hq / a.kv.heads;
-    int t0, t1;
-    seq_rows(a.goff, b, a.T, &t0, &t1, a.err);
-    const int nq = t1 - t0;
-    if (nq > a.max_q) {
-        if (threadIdx.x == 0) atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
-        return;
-    }
-    const int pairs = (nq + 2 * tpt - 1) / (2 * tpt);
-    if (y >= pairs) return;
-    const int i0 = (pairs - 1 - y) * 2 * tpt;             // first token of tile A in the sequence
-    const int n_tok = min(nq - i0, 2 * tpt);
-    const int ntile = n_tok > tpt ? 2 : 1;
-    const int len = kv_length(a.kv, b, a.max_len, a.err);
-    const int p0 = len - nq + i0, p1 = p0 + n_tok - 1;    // positions of the first and last token
-    const KeyBlocks kb = key_blocks<kN>(max(p0, 0), p1, a.window, a.sinks);
-    // row r of tile x: token i0 + x tpt + r / g, query head hk g + r % g
-    const int tile = warp >> 2;                           // of a softmax warp
-    const int r = threadIdx.x & 127, rt = r / g;
-    const int tok_in = tile * tpt + rt;
-    const bool have = warp < 8 && rt < tpt && tok_in < n_tok;
-    const int tok = t0 + i0 + tok_in, head = hk * g + (r - rt * g);
-    const int p = have ? p0 + tok_in : -1;
-    uint16_t* orow = a.out + ((size_t)tok * a.Hq + head) * D;
-    if (kb.n == 0) {                                      // no row sees a key
-        if (have) {
-            for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(orow + d) = make_uint4(0, 0, 0, 0);
-            if (a.lse) a.lse[(size_t)tok * a.Hq + head] = kNegInf;
-        }
-        return;
-    }
-    // block j0 is seen entirely by every row
-    auto all_see = [&](int j0) {
-        return j0 + kN - 1 <= p0 && (a.window == 0 || p1 - j0 < a.window || j0 + kN <= a.sinks);
-    };
-
     if (threadIdx.x == 0) {
         mbar_init(&ctl->qfull, 1);
+        mbar_init(&ctl->qempty, 1);
         for (int i = 0; i < NS; ++i) {
             mbar_init(&ctl->full[i], 1);
             mbar_init(&ctl->empty[i], 1);
@@ -218,15 +348,34 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->sfull[i], 1);
-            mbar_init(&ctl->pready[i], 4);
+            mbar_init(&ctl->pready[i][0], 4);
+            mbar_init(&ctl->pready[i][1], 4);
             mbar_init(&ctl->ofull[i], 1);
+            mbar_init(&ctl->oempty[i], 4);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
-        ctl->bad = 0;
         fence_mbar_init();
     }
+    if (warp == 8 && lane == 0) { tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV); }
     if (warp == 9) { tmem_alloc(&ctl->tmem, 512); tmem_relinquish(); }
+    pdl_wait();
+    pdl_launch();
+
+    // ---- this CTA's work (every thread finds it by itself)
+    const int Hkv = a.kv.heads, nc = SPLIT ? (int)cluster_nctas() : 1;
+    Walk w0;
+    bool mine;
+    if constexpr (SPLIT) {
+        mine = w0.pick(a, tpt, (int)blockIdx.x / nc);
+        w0.x = (int)cluster_ctarank();
+        w0.n = nc;
+        w0.c0 = mine ? w0.cut(w0.x) : 0;
+        w0.c1 = mine ? w0.cut(w0.x + 1) : 0;
+    } else {
+        w0.turn = 0;
+        mine = w0.settle(a, tpt);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -234,164 +383,261 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     auto s_col = [&](int x) { return tmem + (uint32_t)(x * kN); };
     auto o_col = [&](int x) { return tmem + (uint32_t)(2 * kN + x * D); };
     volatile int* abort = &ctl->abort;
-
+    // the join: row rr of this CTA's share, from part x of a tile
+    const int per = kTile / nc;
+    auto join_o = [&](int i, int x, int rr) {
+        return reinterpret_cast<float*>(qs) + (i * kTile + x * per + rr) * join_row<D>();
+    };
+    auto join_ml = [&](int i, int x, int rr) {
+        return reinterpret_cast<float*>(qs) + 2 * kTile * join_row<D>() + (i * kTile + x * per + rr) * 2;
+    };
+    const bool joins = SPLIT && mine && w0.kb.n > 0;      // the same in all CTAs of a cluster
     // the registers of 384 threads x 168: two softmax groups of 208, one of 88
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 8) {
             // -------------------------------------------------------- TMA
             const int lg = 31 - __clz(a.kv.page_size);
-            const int R = min(a.kv.page_size, kN), npg = kN / R;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&ctl->qfull, (uint32_t)(ntile * tpt * g * D * 2));
-                for (int x = 0; x < ntile; ++x)
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(qs + (x * (D / 64) + c) * kTile * 128, &tmQ, c * 64, hk * g, t0 + i0 + x * tpt,
-                                    &ctl->qfull);
-            }
-            __syncwarp();
-            uint32_t it = 0;
+            const int R = min(a.kv.page_size, kN), npg = kN / R, g = a.Hq / Hkv;
+            uint32_t it = 0, part = 0;
             bool ok = true;
-            for (int c = 0; c < kb.n && ok; ++c) {
-                const int j0 = kb(c) * kN;
-                // lane: page pg of the block, 64-column panel pn; a page past the end is out of bounds
-                const int pg = lane % npg, pn = lane / npg, jp = j0 + pg * R;
-                int page = a.kv.pages;
-                if (pn < D / 64 && jp < len) page = page_of(a.kv, b, jp >> lg, a.err);
-                for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
-                    const int st = it % NS;
-                    if (it >= (uint32_t)NS)
-                        ok = __all_sync(0xffffffffu, mbar_wait(&ctl->empty[st], ((it / NS) & 1) ^ 1, abort, a.err));
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], SB);
-                    __syncwarp();
-                    if (pn < D / 64)
-                        tma_load_4d(ring + st * SB + pn * kN * 128 + pg * R * 128, kv ? &tmV : &tmK, pn * 64,
-                                    jp & (a.kv.page_size - 1), hk, page, &ctl->full[st]);
+            Walk w = w0;
+            for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+                if (w.kb.n == 0 || w.c0 == w.c1) continue;
+                const int c0 = w.c0, c1 = w.c1;
+                // Q of the part before is no longer read
+                if (part > 0) ok = __all_sync(0xffffffffu, mbar_wait(&ctl->qempty, (part - 1) & 1, abort, a.err));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&ctl->qfull, (uint32_t)(w.ntile * tpt * g * D * 2));
+                    for (int x = 0; x < w.ntile; ++x)
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_3d(qs + (x * (D / 64) + c) * kTile * 128, &tmQ, c * 64, w.hk * g,
+                                        w.t0 + w.i0 + x * tpt, &ctl->qfull);
+                }
+                __syncwarp();
+                ++part;
+                for (int c = c0; c < c1 && ok; ++c) {
+                    const int j0 = w.kb(c) * kN;
+                    // lane: page pg of the block, 64-column panel pn; a page past the end is out of bounds
+                    const int pg = lane % npg, pn = lane / npg, jp = j0 + pg * R;
+                    int page = a.kv.pages;
+                    if (pn < D / 64 && jp < w.len) page = page_of(a.kv, w.b, jp >> lg, a.err);
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
+                        const int st = it % NS;
+                        if (it >= (uint32_t)NS)
+                            ok = __all_sync(0xffffffffu, mbar_wait(&ctl->empty[st], ((it / NS) & 1) ^ 1, abort, a.err));
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], SB);
+                        __syncwarp();
+                        if (pn < D / 64)
+                            tma_load_4d(ring + st * SB + pn * kN * 128 + pg * R * 128, kv ? &tmV : &tmK, pn * 64,
+                                        jp & (a.kv.page_size - 1), w.hk, page, &ctl->full[st]);
+                    }
                 }
             }
             if (lane == 0) {                              // every copy lands before the CTA ends
-                mbar_wait_drain(&ctl->qfull, 0, a.err);
+                if (part > 0) mbar_wait_drain(&ctl->qfull, (part - 1) & 1, a.err);
                 for (uint32_t j = it > (uint32_t)NS ? it - NS : 0; j < it; ++j)
                     mbar_wait_drain(&ctl->full[j % NS], (j / NS) & 1, a.err);
             }
         } else if (warp == 9) {
             // -------------------------------------------------------- MMA
-            if (lane == 0) {
+            {
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort, a.err));
+                };
+                const uint32_t q_lo = desc_k(smem_u32(qs)), k_lo = desc_k(smem_u32(ring));
+                const uint32_t v_lo = desc_mn(smem_u32(ring), kN * 128);
                 auto mma_s = [&](int x, int st) {         // S_x = Q_x K^T
-                    const uint32_t q = smem_u32(qs + x * (D / 64) * kTile * 128), k = smem_u32(ring + st * SB);
+                    const uint32_t q = q_lo + x * (kTile * D * 2 >> 4), k = k_lo + st * (SB >> 4);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t off = (i >> 2) * kTile * 128 + (i & 3) * 32;
-                        tc_mma_f16(s_col(x), smem_desc_sw128(q + off), smem_desc_sw128(k + off), IDESC_S, i > 0);
+                        const uint32_t off = ((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4;
+                        mma_ss(s_col(x), q + off, k + off, IDESC_S, i > 0);
                     }
                 };
-                auto mma_o = [&](int x, int st, bool acc) {   // O_x += P_x V
-                    const uint32_t v = smem_u32(ring + st * SB);
+                auto mma_o = [&](int x, int st, int half, uint32_t acc) {   // O_x += P_x V over 64 keys
+                    const uint32_t v = v_lo + st * (SB >> 4) + half * (4 * 2048 >> 4);
+                    const uint32_t p = s_col(x) + 32 * half;
 #pragma unroll
-                    for (int i = 0; i < kN / 16; ++i)
-                        tc_mma_f16_ta(o_col(x), s_col(x) + 8 * i, smem_desc_mn_sw128(v + i * 2048, kN * 128), IDESC_O,
-                                      acc || i > 0);
+                    for (int i = 0; i < 4; ++i)
+                        mma_ts(o_col(x), p + 8 * i, v + i * (2048 >> 4), IDESC_O, i > 0 ? 1u : acc);
                 };
-                bool ok = mbar_wait(&ctl->qfull, 0, abort, a.err) && mbar_wait(&ctl->full[0], 0, abort, a.err);
-                if (ok) {
-                    tc_fence_after();
-                    for (int x = 0; x < ntile; ++x) { mma_s(x, 0); tc_commit(&ctl->sfull[x]); }
-                    tc_commit(&ctl->empty[0]);
-                }
-                for (int c = 0; c < kb.n && ok; ++c) {
-                    const uint32_t iv = 2 * c + 1, ik = 2 * c + 2;      // ring items of V c and K c + 1
-                    const int sv = iv % NS, sk = ik % NS;
-                    const bool more = c + 1 < kb.n;
-                    for (int x = 0; x < ntile && ok; ++x) {
-                        ok = mbar_wait(&ctl->pready[x], c & 1, abort, a.err) &&
-                             (x > 0 || mbar_wait(&ctl->vready[sv], (iv / NS) & 1, abort, a.err));
+                uint32_t step = 0, part = 0;              // steps and parts of this CTA so far
+                uint32_t np[2] = {0, 0}, no[2] = {0, 0};  // steps, parts by tile
+                bool ok = true;
+                Walk w = w0;
+                for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+                    if (w.kb.n == 0 || w.c0 == w.c1) continue;
+                    const int c0 = w.c0, c1 = w.c1;
+                    int end[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) end[x] = x < w.ntile ? min(w.tile_steps(x, tpt), c1) : 0;
+                    const int ntile = w.ntile;
+                    {
+                        const uint32_t ik = 2 * step;
+                        ok = wait(&ctl->qfull, part & 1) &&
+                             wait(&ctl->full[ik % NS], (ik / NS) & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        mma_o(x, sv, c > 0);
-                        if (x == ntile - 1) tc_commit(&ctl->empty[sv]);
-                        if (!more) { tc_commit(&ctl->ofull[x]); continue; }
-                        if (x == 0) {
-                            ok = mbar_wait(&ctl->full[sk], (ik / NS) & 1, abort, a.err);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        mma_s(x, sk);
-                        tc_commit(&ctl->sfull[x]);
-                        if (x == ntile - 1) tc_commit(&ctl->empty[sk]);
-                    }
-                }
-                // every MMA completes before the CTA ends
-                tc_commit(&ctl->drain);
-                mbar_wait_drain(&ctl->drain, 0, a.err);
-            }
-        } else {
-            // -------------------------------------------------------- V release
-            for (int c = 0; c < kb.n; ++c) {
-                const uint32_t iv = 2 * c + 1;
-                const int st = iv % NS, j0 = kb(c) * kN;
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctl->full[st], (iv / NS) & 1, abort, a.err))) break;
-                if (!all_see(j0)) {
-                    uint8_t* v = ring + st * SB;
-                    bool bad = false;
-                    // 16-byte pieces: panel, row, piece (the swizzle only permutes a row's pieces)
-                    for (int i = (warp - 10) * 32 + lane; i < kN * D / 8; i += 64) {
-                        uint4* w = reinterpret_cast<uint4*>(v) + i;
-                        const int j = j0 + ((i >> 3) & (kN - 1));
-                        if (j >= len) {
-                            *w = make_uint4(0, 0, 0, 0);
-                        } else {
-                            const uint4 u = *w;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t z = (&u.x)[e];
-                                bad |= (z & 0x7F80u) == 0x7F80u || (z & 0x7F800000u) == 0x7F800000u;
+                        for (int x = 0; x < 2; ++x)
+                            if (c0 < end[x]) { mma_s(x, ik % NS); commit_elected(&ctl->sfull[x]); }
+                        commit_elected(&ctl->empty[ik % NS]);
+                        if (c0 + 1 == c1) commit_elected(&ctl->qempty);
+                    }
+                    for (int c = c0; c < c1 && ok; ++c, ++step) {
+                        const uint32_t iv = 2 * step + 1, ik = 2 * step + 2;    // ring items of V c and K c + 1
+                        const int sv = iv % NS, sk = ik % NS;
+                        bool v_here = false, k_here = false;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (!ok || c >= end[x]) continue;
+                            if (c == c0 && no[x] > 0)     // O of this tile's part before is read
+                                ok = wait(&ctl->oempty[x], (no[x] - 1) & 1);
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                if (!ok) break;
+                                ok = wait(&ctl->pready[x][half], np[x] & 1) &&
+                                     (v_here || wait(&ctl->vready[sv], (iv / NS) & 1));
+                                if (!ok) break;
+                                v_here = true;
+                                tc_fence_after();
+                                mma_o(x, sv, half, half || c > c0);
+                            }
+                            if (!ok) continue;
+                            ++np[x];
+                            if (x == ntile - 1) commit_elected(&ctl->empty[sv]);
+                            if (c + 1 == end[x]) {
+                                commit_elected(&ctl->ofull[x]);
+                                ++no[x];
+                            } else {
+                                if (!k_here) ok = wait(&ctl->full[sk], (ik / NS) & 1);
+                                if (!ok) continue;
+                                k_here = true;
+                                tc_fence_after();
+                                mma_s(x, sk);
+                                commit_elected(&ctl->sfull[x]);
+                            }
+                            if (x == ntile - 1 && c + 1 < c1) {
+                                commit_elected(&ctl->empty[sk]);
+                                if (c + 2 == c1) commit_elected(&ctl->qempty);
                             }
                         }
                     }
-                    if (bad) *(volatile int*)&ctl->bad = 1;
-                    fence_proxy_async_smem();
+                    ++part;
                 }
+                // every MMA completes before the CTA ends
+                commit_elected(&ctl->drain);
+                mbar_wait_drain(&ctl->drain, 0, a.err);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->vready[st]);
+            }
+        } else {
+            // -------------------------------------------------------- V release
+            uint32_t step = 0, part = 0;
+            bool ok = true;
+            Walk w = w0;
+            for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+                if (w.kb.n == 0 || w.c0 == w.c1) continue;
+                const int c0 = w.c0, c1 = w.c1;
+                bool bad = false;
+                for (int c = c0; c < c1; ++c, ++step) {
+                    const uint32_t iv = 2 * step + 1;
+                    const int st = iv % NS, j0 = w.kb(c) * kN;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&ctl->full[st], (iv / NS) & 1, abort, a.err));
+                    if (!ok) break;
+                    if (!w.all_see(a, j0)) {
+                        uint8_t* v = ring + st * SB;
+                        // 16-byte pieces: panel, row, piece (the swizzle only permutes a row's pieces)
+#pragma unroll 4
+                        for (int i = (warp - 10) * 32 + lane; i < kN * D / 8; i += 64) {
+                            uint4* p = reinterpret_cast<uint4*>(v) + i;
+                            if (j0 + ((i >> 3) & (kN - 1)) >= w.len) {
+                                *p = make_uint4(0, 0, 0, 0);
+                            } else {
+                                const uint4 u = *p;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t z = (&u.x)[e];
+                                    bad |= (z & 0x7F80u) == 0x7F80u || (z & 0x7F800000u) == 0x7F800000u;
+                                }
+                            }
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    const bool any = __any_sync(0xffffffffu, bad);
+                    if (lane == 0 && (c == c0 || any)) *(volatile int*)&ctl->bad[warp - 10][part & 3] = any;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->vready[st]);
+                }
+                ++part;
             }
         }
+        if (joins) { cluster_sync(); cluster_sync(); }
     } else {
         // ------------------------------------------------------------ softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        if (tile < ntile) {
-            const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t s_addr = s_col(tile) + lane_base, o_addr = o_col(tile) + lane_base;
-            const float sc = a.scale;
+        const int tile = warp >> 2, r = threadIdx.x & 127, g = a.Hq / Hkv, rt = r / g;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = s_col(tile) + lane_base, o_addr = o_col(tile) + lane_base;
+        const float sc = a.scale;
+        uint32_t ns = 0, no = 0, part = 0;                // steps and parts of this tile, parts of the CTA
+        bool ok = true;
+        Walk w = w0;
+        for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+            const int c0 = w.c0, c1 = w.c1;
+            const uint32_t bad_at = part & 3;
+            if (w.kb.n > 0 && c0 < c1) ++part;
+            // row r of tile x: token i0 + x tpt + r / g, query head hk g + r % g
+            const int tok_in = tile * tpt + rt;
+            const bool have = rt < tpt && tok_in < w.n_tok;
+            const int tok = w.t0 + w.i0 + tok_in, head = w.hk * g + (r - rt * g);
+            const int p = have ? w.p0 + tok_in : -1;
+            const size_t row = (size_t)tok * a.Hq + head;
+            const int n_steps = tile < w.ntile ? w.tile_steps(tile, tpt) : 0, end = min(n_steps, c1);
+            if (!joins && end <= c0) {
+                // rows that see no key (where parts are joined, the join writes them)
+                if (c0 == 0 && have) {
+                    for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(a.out + row * D + d) = make_uint4(0, 0, 0, 0);
+                    if (a.lse) a.lse[row] = kNegInf;
+                }
+                continue;
+            }
             float m = kNegInf, l = 0.f;
-            bool ok = true;
-            for (int c = 0; c < kb.n; ++c) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&ctl->sfull[tile], c & 1, abort, a.err));
+            for (int c = c0; c < end; ++c, ++ns) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl->sfull[tile], ns & 1, abort, a.err));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t su[kN];
-#pragma unroll
-                for (int i = 0; i < kN / 32; ++i) tmem_ld_32x32b_x32(s_addr + 32 * i, su + 32 * i);
+                tmem_ld_x128(s_addr, su);
                 float* s = reinterpret_cast<float*>(su);
-                const int j0 = kb(c) * kN;
-                if (!all_see(j0)) {
-                    const int hi = p - j0, lo = a.window ? hi - a.window + 1 : -(1 << 30), sk = a.sinks - j0;
+                const int j0 = w.kb(c) * kN;
+                if (!w.all_see(a, j0)) {
+                    // bit i of a word: key 32 z + i of the block is seen
+                    const int hi = p - j0, lo = a.window ? hi - a.window + 1 : 0, sk = a.sinks - j0;
+                    auto below = [](int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; };
 #pragma unroll
-                    for (int i = 0; i < kN; ++i)
-                        s[i] = i <= hi && (i >= lo || i < sk) ? s[i] : kNegInf;
+                    for (int z = 0; z < kN / 32; ++z) {
+                        const uint32_t see = below(hi + 1 - 32 * z) & (~below(lo - 32 * z) | below(sk - 32 * z));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(see & (1u << i))) s[32 * z + i] = kNegInf;
+                    }
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int i = 4; i < kN; i += 4)
+                for (int i = 4; i < kN; i += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[i + e]);
-                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = i + 4 < kN ? fmaxf(fmaxf(mx[e], s[i + e]), s[i + 4 + e]) : fmaxf(mx[e], s[i + e]);
+                const float mn = fmaxf(fmaxf(m, mx[0]), fmaxf(fmaxf(mx[1], mx[2]), mx[3]));
                 // S complete means this tile's O of the step before is complete too
                 if (__any_sync(0xffffffffu, (mn - m) * sc > kLazy)) {
                     const float f = mn == m ? 1.f : ex2_approx((m - mn) * sc);
                     m = mn;
                     l *= f;
-                    if (c > 0) {
+                    if (c > c0) {
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             uint32_t o[16];
@@ -418,44 +664,96 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         pk[e] = pack_bf16x2(x, z);
                     }
                     tmem_st_x16(s_addr + 16 * i, pk);
+                    if (i & 1) {                          // 64 keys of P: the MMAs may take them
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->pready[tile][i >> 1]);
+                    }
                 }
                 float x, z;
                 unpack2(add2(sum[0], sum[1]), &x, &z);
                 l += x + z;
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->pready[tile]);
             }
-            // -------------------------------------------------------- epilogue
-            if (ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[tile], 0, abort, a.err))) {
+            // -------------------------------------------------------- O to memory
+            const bool act = c0 < end;
+            if (act) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[tile], no & 1, abort, a.err));
+                ++no;
                 tc_fence_after();
-                if (*(volatile int*)&ctl->bad) {
-                    if (have && p >= 0) attend_row<D>(a, b, hk, head, tok, p);
-                    else if (have) {
-                        for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(orow + d) = make_uint4(0, 0, 0, 0);
-                        if (a.lse) a.lse[(size_t)tok * a.Hq + head] = kNegInf;
-                    }
-                } else {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+            }
+            // a part's row goes to the CTA that joins it
+            uint32_t dst_o = 0, dst_ml = 0;
+            if (joins) {
+                dst_o = mapa_shared(smem_u32(join_o(tile, w.x, r % per)), r / per);
+                dst_ml = mapa_shared(smem_u32(join_ml(tile, w.x, r % per)), r / per);
+                cluster_sync();             // every CTA is done with its Q and its ring
+            }
+            if (act && ok) {
+                const bool bad = ((volatile int*)ctl->bad[0])[bad_at] | ((volatile int*)ctl->bad[1])[bad_at];
+                const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(o_addr + 32 * i, o);
-                        if (have) {
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(o_addr + 32 * i, o);
+                    if (bad || !have) continue;
+                    if (SPLIT) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint32_t w[4];
+                        for (int e = 0; e < 32; e += 4)
+                            st_cluster_v4(dst_o + (32 * i + e) * 4, o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else {
 #pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    w[z] = pack_bf16x2(__uint_as_float(o[e + 2 * z]) * inv,
-                                                       __uint_as_float(o[e + 2 * z + 1]) * inv);
-                                *reinterpret_cast<uint4*>(orow + 32 * i + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t q[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                q[z] = pack_bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+                            *reinterpret_cast<uint4*>(a.out + row * D + 32 * i + e) = make_uint4(q[0], q[1], q[2], q[3]);
                         }
                     }
-                    if (have && a.lse)
-                        a.lse[(size_t)tok * a.Hq + head] = l == 0.f ? kNegInf : (m * sc + log2f(l)) * 0.6931471805599453f;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->oempty[tile]);      // O may be overwritten
+                if (bad) {
+                    if (have) attend_row<D>(a, w.b, w.hk, head, tok, p, w.kb, c0, end, dst_o, dst_ml);
+                } else if (SPLIT) {
+                    st_shared_cluster(dst_ml, m);
+                    st_shared_cluster(dst_ml + 4, l);
+                } else if (have && a.lse) {
+                    a.lse[row] = l == 0.f ? kNegInf : (m * sc + log2f(l)) * 0.6931471805599453f;
+                }
+            }
+            if (joins) {
+                cluster_sync();             // every part's rows have arrived
+                // eight threads a row of this CTA's share
+                constexpr int C = D / 8;
+                for (int i = threadIdx.x / 8; i < w.ntile * per && ok; i += 32) {
+                    const int jt = i / per, rr = i - jt * per, R = w.x * per + rr, t_in = R / g, d = (threadIdx.x & 7) * C;
+                    if (t_in >= tpt || jt * tpt + t_in >= w.n_tok) continue;
+                    const size_t out_row = (size_t)(w.t0 + w.i0 + jt * tpt + t_in) * a.Hq + w.hk * g + (R - t_in * g);
+                    const int steps = w.tile_steps(jt, tpt);
+                    float mt = kNegInf, lt = 0.f, v[C];
+#pragma unroll
+                    for (int e = 0; e < C; ++e) v[e] = 0.f;
+                    for (int x = 0; x < nc && w.cut(x) < steps; ++x) mt = fmaxf(mt, join_ml(jt, x, rr)[0]);
+                    for (int x = 0; x < nc && w.cut(x) < steps; ++x) {
+                        const float mi = join_ml(jt, x, rr)[0], f = mi == mt ? 1.f : ex2_approx((mi - mt) * sc);
+                        lt += f * join_ml(jt, x, rr)[1];
+#pragma unroll
+                        for (int e = 0; e < C; e += 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(join_o(jt, x, rr) + d + e);
+                            v[e] += f * q.x; v[e + 1] += f * q.y; v[e + 2] += f * q.z; v[e + 3] += f * q.w;
+                        }
+                    }
+                    const float it = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+                    for (int e = 0; e < C; e += 8)
+                        *reinterpret_cast<uint4*>(a.out + out_row * D + d + e) =
+                            make_uint4(pack_bf16x2(v[e] * it, v[e + 1] * it), pack_bf16x2(v[e + 2] * it, v[e + 3] * it),
+                                       pack_bf16x2(v[e + 4] * it, v[e + 5] * it), pack_bf16x2(v[e + 6] * it, v[e + 7] * it));
+                    if (a.lse && d == 0)
+                        a.lse[out_row] = lt == 0.f ? kNegInf : (mt * sc + log2f(lt)) * 0.6931471805599453f;
                 }
             }
         }
@@ -465,14 +763,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-bool encode_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box) {
-    return encode_tmap_nd(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box,
-                          CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <int D>
-int go(const AttnArgs& a, cudaStream_t stream) {
+int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     const int g = a.Hq / a.kv.heads, tpt = kTile / g;
     const uint32_t R = (uint32_t)std::min(a.kv.page_size, kN);
     CUtensorMap tmQ, tmK, tmV;
@@ -485,33 +777,55 @@ int go(const AttnArgs& a, cudaStream_t stream) {
     const uint64_t vs[3] = {(uint64_t)a.kv.v_slot_stride * 2, (uint64_t)a.kv.v_head_stride * 2,
                             (uint64_t)a.kv.v_page_stride * 2};
     const uint32_t kbx[4] = {64, R, 1, 1};
-    if (!encode_map(&tmQ, a.q, 3, qd, qst, qb) || !encode_map(&tmK, a.kv.k, 4, kd, ks, kbx) ||
-        !encode_map(&tmV, a.kv.v, 4, kd, vs, kbx))
+    auto encode = [](CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+        return encode_tmap_nd(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box,
+                              CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (!encode(&tmQ, a.q, 3, qd, qst, qb) || !encode(&tmK, a.kv.k, 4, kd, ks, kbx) ||
+        !encode(&tmV, a.kv.v, 4, kd, vs, kbx))
         return W4_ERR_CUDA;
-    const long long grid = ((long long)a.max_q + 2 * tpt - 1) / (2 * tpt) * a.kv.batch * a.kv.heads;
-    if (grid > 0x7fffffffLL) return W4_ERR_UNSUPPORTED_SHAPE;
+    const long long items = ((long long)a.max_q + 2 * tpt - 1) / (2 * tpt) * a.kv.heads * a.kv.batch;
+    if (items > (1LL << 26)) return W4_ERR_UNSUPPORTED_SHAPE;
+    // CTAs of a cluster that share an item: the fewest with the shortest last turn,
+    // from upper bounds of the items and of an item's steps.  In units of a step
+    // (1.8 us for heads of 128), starting and finishing an item costs about 3, with
+    // the join of its parts 5: 2048 tokens behind 14336 take 425 us in two turns of
+    // whole items and 16 tokens behind 8176 take 132 us on one CTA each.
+    const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)a.max_len);
+    long long keys = cap;
+    if (a.window) keys = std::min(cap, (long long)a.window + 2 * tpt + kN + std::min<long long>(a.sinks, cap));
+    const long long steps = std::max((keys + kN - 1) / kN, 1LL);
+    int nc = 1;
+    long long best = (items + sm_count - 1) / sm_count * (steps + 3);
+    for (int c = 2; c <= 8; c *= 2) {
+        const long long cost = (items * c + sm_count - 1) / sm_count * ((steps + c - 1) / c + 5);
+        if (cost < best) { best = cost; nc = c; }
+    }
     constexpr size_t bytes = smem_total<D>();
-    if (cudaFuncSetAttribute(k_attn_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+    auto kern = nc > 1 ? k_attn_prefill<D, true> : k_attn_prefill<D, false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
         return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(nc > 1 ? items * nc : std::min<long long>(items, sm_count)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)nc;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_prefill<D>, tmQ, tmK, tmV, a, tpt) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    cfg.numAttrs = nc > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, a, tpt) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 }  // namespace
 
-size_t attn_prefill_ws_bytes(int, int, int, int, int, int, int) { return 0; }
-
-int launch_attn_prefill(const AttnArgs& a, int, cudaStream_t stream) {
-    return a.kv.head_dim == 128 ? go<128>(a, stream) : go<64>(a, stream);
+int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+    return a.kv.head_dim == 128 ? go<128>(a, sm_count, stream) : go<64>(a, sm_count, stream);
 }
 
 }  // namespace w4

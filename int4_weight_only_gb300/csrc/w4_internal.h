@@ -245,12 +245,11 @@ struct AttnArgs {
     int T, Hq, max_q, max_len;
     float scale;                   // softmax scale times log2(e)
     int window, sinks;             // window 0: none
-    int* tickets;
+    int* tickets;                  // decode: arrival counters and partial results
     float* partial;
     int* err;
 };
-size_t attn_decode_ws_bytes(int batch, int Hq, int Hkv, int D, int sm_count);
-size_t attn_prefill_ws_bytes(int batch, int Hq, int Hkv, int D, int max_q, int max_len, int sm_count);
+size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count);   // of partial results
 int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream);
 int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream);
 

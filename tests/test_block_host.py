@@ -82,10 +82,9 @@ def _decode(lib, kv=None, q=OK16, qt=128 * 28, qh=128, out=OK16, lse=None, hq=28
                               sinks, ws, wsb, None)
 
 
-def _prefill(lib, kv=None, q=OK16, goff=OK16, out=OK16, T=8, hq=28, max_q=8, max_len=64, scale=0.1, ws=OK16,
-             wsb=1 << 30):
+def _prefill(lib, kv=None, q=OK16, goff=OK16, out=OK16, T=8, hq=28, max_q=8, max_len=64, scale=0.1):
     return lib.w4_attn_prefill(kv if kv is not None else _kv(), q, 128 * hq, 128, goff, out, None, T, hq, max_q,
-                               max_len, scale, 0, 0, ws, wsb, None)
+                               max_len, scale, 0, 0, None)
 
 
 def test_cache_refusals(w4):
@@ -123,11 +122,11 @@ def test_attention_refusals(w4):
         assert _prefill(lib, **kw) == c["W4_ERR_" + code], kw
     # nothing to do: no workspace needed, nothing enqueued
     assert _decode(lib, _kv(batch=0), ws=None, wsb=0) == c["W4_OK"]
-    assert _prefill(lib, T=0, ws=None, wsb=0) == c["W4_OK"]
-    assert _prefill(lib, max_q=0, ws=None, wsb=0) == c["W4_OK"]
+    assert _prefill(lib, T=0) == c["W4_OK"]
+    assert _prefill(lib, max_q=0) == c["W4_OK"]
     assert _decode(lib, ws=None) == c["W4_ERR_WORKSPACE"]
     assert _decode(lib, wsb=16) == c["W4_ERR_WORKSPACE"]
-    assert lib.w4_attn_workspace_bytes(1, 30, 4, 128, 1, 64) == 0
+    assert lib.w4_attn_decode_workspace_bytes(30, 4, 128) == 0
 
 
 def _rope(lib, kv=None, q=OK16, k=OK16, v=OK16, goff=None, pos=None, inv=OK16, m=1.0, rot=128, out=OK16, T=2, hq=28,

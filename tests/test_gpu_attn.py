@@ -136,7 +136,7 @@ def test_decode_more_sequences_than_threads(w4):
 
 def test_workspace_is_left_ready(w4):
     """The caller's workspace: counters back at zero, any call order."""
-    n = w4.w4_attn_workspace_bytes(4, 8, 2, 128, 100, 5000)
+    n = w4.w4_attn_decode_workspace_bytes(8, 2, 128)
     ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
     for lens in ([5000, 3], [4000, 4999, 1, 77], [64]):
         decode(w4, lens, 8, 2, 128, 32, workspace=ws)
@@ -323,7 +323,7 @@ def test_streams(w4):
     q = randn_bf16(2, 4, 64, seed=1).cuda()
     want = w4.w4_attn_decode(q, cache.k, cache.v, cache.kv_len, cache.table, 700)
     torch.cuda.synchronize()
-    ws = torch.zeros(w4.w4_attn_workspace_bytes(2, 4, 2, 64, 1, 700), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(w4.w4_attn_decode_workspace_bytes(4, 2, 64), dtype=torch.uint8, device="cuda")
     q2 = torch.zeros_like(q)
     out = torch.empty_like(q)
     s.wait_stream(torch.cuda.current_stream())
@@ -340,7 +340,7 @@ def test_graph_replay_follows_the_lengths(w4):
     cache = Paged([100, 230], 2, 64, 16)
     kv = cache.fill_random()
     q = randn_bf16(2, 4, 64, seed=1).cuda()
-    ws = torch.zeros(w4.w4_attn_workspace_bytes(2, 4, 2, 64, 1, 230), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(w4.w4_attn_decode_workspace_bytes(4, 2, 64), dtype=torch.uint8, device="cuda")
     out = torch.empty_like(q)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
