@@ -122,6 +122,12 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
         :: "r"(smem_u32(bar)) : "memory");
 }
 
+// A whole 32-byte sector.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_nctas() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
@@ -549,21 +555,28 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     if (!ok) break;
                     if (!w.all_see(a, j0)) {
                         uint8_t* v = ring + st * SB;
-                        // 16-byte pieces: panel, row, piece (the swizzle only permutes a row's pieces)
-#pragma unroll 4
-                        for (int i = (warp - 10) * 32 + lane; i < kN * D / 8; i += 64) {
-                            uint4* p = reinterpret_cast<uint4*>(v) + i;
-                            if (j0 + ((i >> 3) & (kN - 1)) >= w.len) {
-                                *p = make_uint4(0, 0, 0, 0);
-                            } else {
-                                const uint4 u = *p;
+                        // rows that some query does not see: past the first token, or out of
+                        // the last one's window
+                        const int hi = max(w.p0 + 1 - j0, 0), lo = a.window ? min(max(w.p1 - a.window + 1 - j0, 0), hi) : 0;
+                        // 16-byte pieces of 128-byte rows (the swizzle only permutes a row's pieces)
+                        auto check = [&](int r0, int r1) {
+                            for (int panel = 0; panel < D / 64; ++panel)
+                                for (int i = 8 * r0 + (warp - 10) * 32 + lane; i < 8 * r1; i += 64) {
+                                    uint4* p = reinterpret_cast<uint4*>(v + panel * kN * 128) + i;
+                                    if (j0 + (i >> 3) >= w.len) {
+                                        *p = make_uint4(0, 0, 0, 0);
+                                        continue;
+                                    }
+                                    const uint4 u = *p;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const uint32_t z = (&u.x)[e];
-                                    bad |= (z & 0x7F80u) == 0x7F80u || (z & 0x7F800000u) == 0x7F800000u;
+                                    for (int e = 0; e < 4; ++e) {
+                                        const uint32_t z = (&u.x)[e];
+                                        bad |= (z & 0x7F80u) == 0x7F80u || (z & 0x7F800000u) == 0x7F800000u;
+                                    }
                                 }
-                            }
-                        }
+                        };
+                        check(0, min(lo, kN));
+                        check(min(hi, kN), kN);
                         fence_proxy_async_smem();
                     }
                     const bool any = __any_sync(0xffffffffu, bad);
@@ -692,6 +705,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (act && ok) {
                 const bool bad = ((volatile int*)ctl->bad[0])[bad_at] | ((volatile int*)ctl->bad[1])[bad_at];
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                // rows lie apart, so a store is one sector a lane: whole sectors where `out` allows
+                const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
@@ -703,12 +718,18 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                             st_cluster_v4(dst_o + (32 * i + e) * 4, o[e], o[e + 1], o[e + 2], o[e + 3]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t q[4];
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t q[8];
 #pragma unroll
-                            for (int z = 0; z < 4; ++z)
+                            for (int z = 0; z < 8; ++z)
                                 q[z] = pack_bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
-                            *reinterpret_cast<uint4*>(a.out + row * D + 32 * i + e) = make_uint4(q[0], q[1], q[2], q[3]);
+                            uint16_t* to = a.out + row * D + 32 * i + e;
+                            if (wide) {
+                                st_global_v8(to, q);
+                            } else {
+                                reinterpret_cast<uint4*>(to)[0] = make_uint4(q[0], q[1], q[2], q[3]);
+                                reinterpret_cast<uint4*>(to)[1] = make_uint4(q[4], q[5], q[6], q[7]);
+                            }
                         }
                     }
                 }
