@@ -92,7 +92,7 @@ int w4_block_norm(const uint16_t* y, const uint16_t* r, const uint16_t* w_post, 
     a.r_out = r_out; a.x_out = x_out;
     a.M = M; a.K = K; a.gate_div = gate ? M / gate_rows : 1;
     a.res_scale = res_scale; a.eps = eps; a.w_off = w_offset;
-    return launch_block_norm(a, current_sm_count(), static_cast<cudaStream_t>(stream));
+    return launch_block_norm(a, static_cast<cudaStream_t>(stream));
 }
 
 int w4_rope_freqs(int rot_dim, double base, int kind, double factor, double orig_len, double beta_fast,

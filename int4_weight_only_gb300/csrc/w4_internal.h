@@ -217,7 +217,7 @@ struct NormArgs {
     int M, K, gate_div;            // row m uses gate row m / gate_div
     float res_scale, eps, w_off;
 };
-int launch_block_norm(const NormArgs& a, int sm_count, cudaStream_t stream);
+int launch_block_norm(const NormArgs& a, cudaStream_t stream);
 
 // Rotary positions and the cache write (rope.cu).
 struct RopeArgs {
