@@ -605,7 +605,12 @@ ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 def _need_view(t, dtype, ndim, name):
-    """A CUDA tensor whose last dimension is contiguous (other strides free)."""
+    """A CUDA tensor whose last dimension is contiguous (other strides free);
+    returns its strides."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype:
+        s = t.stride()
+        if len(s) == ndim and s[-1] == 1:
+            return s
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -614,22 +619,24 @@ def _need_view(t, dtype, ndim, name):
         raise ValueError(f"{name} must have {ndim} dimensions, got {t.dim()}")
     if t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.stride()
 
 
 def _paged_kv(k_cache, v_cache, kv_len, table):
-    """The packed w4_paged_kv of a pool [pages, heads, page_size, head_dim]."""
-    _need_view(k_cache, torch.bfloat16, 4, "k_cache")
-    _need_view(v_cache, torch.bfloat16, 4, "v_cache")
-    if k_cache.shape != v_cache.shape:
+    """The packed w4_paged_kv of a pool [pages, heads, page_size, head_dim],
+    the pool's shape and the batch."""
+    ks = _need_view(k_cache, torch.bfloat16, 4, "k_cache")
+    vs = _need_view(v_cache, torch.bfloat16, 4, "v_cache")
+    ts = _need_view(table, torch.int32, 2, "table")
+    shape = k_cache.shape
+    if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    _need_view(table, torch.int32, 2, "table")
-    _need(kv_len, torch.int32, (table.shape[0],), "kv_len")
-    pages, heads, page_size, d = k_cache.shape
     batch, max_pages = table.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
+    _need(kv_len, torch.int32, (batch,), "kv_len")
+    pages, heads, page_size, d = shape
     return _PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), kv_len.data_ptr(),
-                          ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], table.stride(0),
-                          pages, page_size, heads, d, batch, max_pages)
+                          ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts[0],
+                          pages, page_size, heads, d, batch, max_pages), shape, batch
 
 
 def w4_block_norm(y: Optional[torch.Tensor], r: torch.Tensor, w_pre: Optional[torch.Tensor],
@@ -647,14 +654,16 @@ def w4_block_norm(y: Optional[torch.Tensor], r: torch.Tensor, w_pre: Optional[to
         _need(y, torch.bfloat16, (M, K), "y")
         if r_out is None:
             r_out = torch.empty_like(r)
-        _need(r_out, torch.bfloat16, (M, K), "r_out")
+        else:
+            _need(r_out, torch.bfloat16, (M, K), "r_out")
     elif r_out is not None:
         raise ValueError("r_out needs y")
     if w_pre is not None:
         _need(w_pre, torch.bfloat16, (K,), "w_pre")
         if x_out is None:
             x_out = torch.empty_like(r)
-        _need(x_out, torch.bfloat16, (M, K), "x_out")
+        else:
+            _need(x_out, torch.bfloat16, (M, K), "x_out")
     if w_post is not None:
         _need(w_post, torch.bfloat16, (K,), "w_post")
     rows = 0
@@ -694,28 +703,30 @@ def w4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     step's tokens; goff [B + 1] are the sequences' first rows (None: one token a
     sequence); pos [T] overrides the rotary positions.  The first
     2 * len(inv_freq) values of a head are rotated."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _need_view(t, torch.bfloat16, 3, name)
-    kv = _paged_kv(k_cache, v_cache, kv_len, table)
+    qs = _need_view(q, torch.bfloat16, 3, "q")
+    ks = _need_view(k, torch.bfloat16, 3, "k")
+    vs = _need_view(v, torch.bfloat16, 3, "v")
+    kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
     T, Hq, D = q.shape
-    want = (T, k_cache.shape[1], k_cache.shape[3])
+    want = (T, pool[1], pool[3])
     if k.shape != want or v.shape != want or D != want[2]:
         raise ValueError(f"k and v must have shape {want} and q [{T}, heads, {want[2]}], got "
                          f"{tuple(k.shape)}, {tuple(v.shape)}, {tuple(q.shape)}")
-    _need(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
+    n = inv_freq.numel()
+    _need(inv_freq, torch.float32, (n,), "inv_freq")
     if goff is not None:
-        _need(goff, torch.int32, (table.shape[0] + 1,), "goff")
+        _need(goff, torch.int32, (batch + 1,), "goff")
     if pos is not None:
         _need(pos, torch.int32, (T,), "pos")
     if q_out is None:
-        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-    _need(q_out, torch.bfloat16, (T, Hq, D), "q_out")
+        q_out = q.new_empty(q.shape)
+    else:
+        _need(q_out, torch.bfloat16, (T, Hq, D), "q_out")
     if T == 0:
         return q_out
-    qs, ks, vs = q.stride(), k.stride(), v.stride()
     _check("w4_rope_append", load().w4_rope_append(
         kv, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-        _ptr(goff), _ptr(pos), inv_freq.data_ptr(), mscale, 2 * inv_freq.numel(),
+        _ptr(goff), _ptr(pos), inv_freq.data_ptr(), mscale, 2 * n,
         1 if interleaved else 0, q_out.data_ptr(), T, Hq, _stream(q, stream)))
     return q_out
 
@@ -725,10 +736,10 @@ def w4_attn_decode_workspace_bytes(q_heads: int, heads: int, head_dim: int) -> i
 
 
 def _attn_outputs(q, out, lse):
-    _need_view(q, torch.bfloat16, 3, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    _need(out, torch.bfloat16, q.shape, "out")
+        out = q.new_empty(q.shape)
+    else:
+        _need(out, torch.bfloat16, q.shape, "out")
     if lse is not None:
         _need(lse, torch.float32, q.shape[:2], "lse")
     return out
@@ -743,21 +754,21 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     Key j is visible when j <= p and (window == 0 or p - j < window or
     j < sinks).  max_len bounds kv_len; lse [B, Hq] fp32 receives the
     log-sum-exp when given."""
-    kv = _paged_kv(k_cache, v_cache, kv_len, table)
+    kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
+    qs = _need_view(q, torch.bfloat16, 3, "q")
     B, Hq, D = q.shape
-    if B != table.shape[0] or D != k_cache.shape[3]:
-        raise ValueError(f"q must have shape [{table.shape[0]}, heads, {k_cache.shape[3]}], got {tuple(q.shape)}")
+    if B != batch or D != pool[3]:
+        raise ValueError(f"q must have shape [{batch}, heads, {pool[3]}], got {tuple(q.shape)}")
     out = _attn_outputs(q, out, lse)
-    if q.numel() == 0:
+    if B == 0 or Hq == 0:
         return out
-    qs = q.stride()
     lib = load()
     _call_with_workspace(
         lib.w4_attn_decode, "w4_attn_decode",
         (kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), _ptr(lse), Hq, max_len,
          D ** -0.5 if scale is None else scale, window, sinks),
         (_stream(q, stream),), q.device, workspace,
-        lambda: lib.w4_attn_decode_workspace_bytes(Hq, k_cache.shape[1], D))
+        lambda: lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D))
     return out
 
 
@@ -769,15 +780,15 @@ def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     cache.  Rows goff[b] .. goff[b + 1] - 1 of q are the last tokens of sequence
     b (their keys already written); max_q bounds their number, max_len kv_len.
     The mask and the other arguments are w4_attn_decode's."""
-    kv = _paged_kv(k_cache, v_cache, kv_len, table)
+    kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
+    qs = _need_view(q, torch.bfloat16, 3, "q")
     T, Hq, D = q.shape
-    if D != k_cache.shape[3]:
-        raise ValueError(f"q must have shape [T, heads, {k_cache.shape[3]}], got {tuple(q.shape)}")
-    _need(goff, torch.int32, (table.shape[0] + 1,), "goff")
+    if D != pool[3]:
+        raise ValueError(f"q must have shape [T, heads, {pool[3]}], got {tuple(q.shape)}")
+    _need(goff, torch.int32, (batch + 1,), "goff")
     out = _attn_outputs(q, out, lse)
-    if q.numel() == 0:
+    if T == 0 or Hq == 0:
         return out
-    qs = q.stride()
     _check("w4_attn_prefill", load().w4_attn_prefill(
         kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(), _ptr(lse), T, Hq, max_q,
         max_len, D ** -0.5 if scale is None else scale, window, sinks, _stream(q, stream)))

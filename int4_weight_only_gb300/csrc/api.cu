@@ -47,6 +47,8 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 }  // namespace
 
+int current_device() { return device_index(); }
+
 int current_sm_count() {
     static int cache[kMaxDevices] = {0};
     const int d = device_index();

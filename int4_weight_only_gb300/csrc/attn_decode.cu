@@ -571,8 +571,8 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
         !encode_tmap_nd(&tmV, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv.v, 5, dims, vs, box, CU_TENSOR_MAP_SWIZZLE_128B))
         return W4_ERR_CUDA;
     const int grid = sm_count, bytes = (int)S::smem;
-    if (cudaFuncSetAttribute(k_attn_decode<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return W4_ERR_CUDA;
+    static SmemLimit limit;
+    if (!limit.raise(k_attn_decode<D, NT>, bytes)) return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(S::threads);

@@ -825,8 +825,8 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     }
     constexpr size_t bytes = smem_total<D>();
     auto kern = nc > 1 ? k_attn_prefill<D, true> : k_attn_prefill<D, false>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
-        return W4_ERR_CUDA;
+    static SmemLimit limit[2];
+    if (!limit[nc > 1].raise(kern, (int)bytes)) return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(nc > 1 ? items * nc : std::min<long long>(items, sm_count)));
     cfg.blockDim = dim3(kThreads);

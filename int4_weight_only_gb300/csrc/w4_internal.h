@@ -2,6 +2,7 @@
 // units (launchers, planning, device set-up).  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -14,6 +15,7 @@ namespace w4 {
 // ---------------------------------------------------------------- device
 int current_sm_count();                 // SMs of the current device (cached)
 int* device_error_flag();               // device address of the error flag
+int current_device();                   // -1: no device
 bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                     uint64_t dim0, uint64_t dim1, uint64_t row_stride_bytes,
                     uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle);
@@ -209,6 +211,21 @@ int launch_smooth(const uint16_t* X, int T, float* W, int N, int K, float alpha,
 
 
 // ---------------------------------------------------------------- decoder block
+// Raises a kernel's dynamic shared memory limit, once per device (one object of
+// this per kernel).
+struct SmemLimit {
+    std::atomic<unsigned long long> done{0};
+    template <typename K> bool raise(K* kern, int bytes) {
+        const int d = current_device();
+        if (d < 0) return false;
+        const unsigned long long bit = 1ull << (d & 63);
+        if (d < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        if (d < 64) done.fetch_or(bit, std::memory_order_relaxed);
+        return true;
+    }
+};
+
 // Norms after and before a block with gate, residual scale and residual
 // (norm.cu); arguments as w4_block_norm, checked by the caller.
 struct NormArgs {
