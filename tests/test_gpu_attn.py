@@ -259,6 +259,51 @@ def test_prefill_hidden_keys_have_no_influence(w4, bad):
     assert sum(qs) == 330
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefill_hidden_values_in_a_large_batch(w4, bad):
+    """The same with enough items that each is worked on whole: the last key of
+    every sequence is seen by its last row only."""
+    lens, H = [45] * 8, 16
+    cache = Paged(lens, H, 64, 16)
+    kv = cache.fill_random()
+    for b in range(8):
+        k, v = (torch.tensor(x).bfloat16() for x in kv[b])
+        v[44, b] = bad
+        cache.put(b, k, v)
+    q = randn_bf16(8 * 40, H, 64, seed=9).cuda()
+    goff = torch.arange(0, 321, 40, dtype=torch.int32, device="cuda")
+    out = w4.w4_attn_prefill(q, cache.k, cache.v, goff, cache.kv_len, cache.table, 40, 45)
+    assert w4.w4_get_device_error() == 0
+    for b in range(8):
+        rows = slice(40 * b, 40 * b + 39)
+        want = BO.attention(to64(q[rows]), kv[b][0], kv[b][1], np.arange(5, 44), 0.125)
+        check(out[rows], None, want, f"sequence {b}")
+        last = to64(out[40 * b + 39])
+        assert not np.isfinite(last[b]).any() and np.isfinite(np.delete(last, b, axis=0)).all()
+
+
+def test_page_offsets_past_32_bits(w4):
+    """Pools of more than 2^32 elements: pages at both ends of one pool."""
+    H, ps, D = 8, 64, 128
+    pages = (1 << 32) // (H * ps * D) + 40
+    free = torch.cuda.mem_get_info()[0]
+    if free < 5 * pages * H * ps * D:
+        pytest.skip("not enough device memory")
+    pool = torch.empty(2, pages, H, ps, D, dtype=torch.bfloat16, device="cuda")
+    c = Paged([150, 70], H, D, ps)
+    ids = torch.tensor([[pages - 1, 3, pages - 7], [pages - 20, 0, 1 << 30]], dtype=torch.int32)
+    c.table_cpu, c.table, c.k, c.v = ids, ids.cuda(), pool[0], pool[1]
+    kv = c.fill_random()
+    decode(w4, [150, 70], 16, H, D, ps, cache=c, kv=kv)
+    prefill(w4, [130, 70], [150, 70], 16, H, D, ps, cache=c, kv=kv, rows=[0, 40, 69, 129])
+    # the cache write: the last position of the first sequence, on its last page
+    q, k, v = (randn_bf16(2, h, D, seed=h).cuda() for h in (16, H, H))
+    inv = w4.w4_rope_freqs(D)[0].cuda()
+    w4.w4_rope_append(q, k, k, c.k, c.v, c.kv_len, c.table, inv)
+    assert torch.equal(c.v[pages - 7, :, 149 - 128], k[0]) and torch.equal(c.v[0, :, 69 - 64], k[1])
+    assert v.shape == k.shape and w4.w4_get_device_error() == 0
+
+
 def test_prefill_long(w4):
     rows = [0, 1, 127, 128, 1000, 2047, 2048, 4099]
     prefill(w4, [4100], [4100], 7, 1, 128, 64, rows=rows)
