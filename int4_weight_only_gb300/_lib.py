@@ -598,6 +598,8 @@ def w4a8_linear(qx: torch.Tensor, sx: torch.Tensor, packed: torch.Tensor,
 
 
 # ------------------------------------------------------------- decoder block
+# (these calls are a few microseconds on the GPU, so their checks are kept to one
+# pass over what the common call has; a failed one is looked at more closely)
 # struct w4_paged_kv of include/w4.h
 _PAGED_KV = struct.Struct("4Q7q6i")
 
@@ -632,7 +634,9 @@ def _paged_kv(k_cache, v_cache, kv_len, table):
     if shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     batch, max_pages = table.shape
-    _need(kv_len, torch.int32, (batch,), "kv_len")
+    if (type(kv_len) is not torch.Tensor or kv_len.dtype is not torch.int32 or not kv_len.is_cuda
+            or kv_len.shape != (batch,) or not kv_len.is_contiguous()):
+        _need(kv_len, torch.int32, (batch,), "kv_len")
     pages, heads, page_size, d = shape
     return _PAGED_KV.pack(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), kv_len.data_ptr(),
                           ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ts[0],
@@ -672,9 +676,14 @@ def w4_block_norm(y: Optional[torch.Tensor], r: torch.Tensor, w_pre: Optional[to
         _need(gate, torch.bfloat16, (rows, K), "gate")
     if M == 0:
         return (r if y is None else r_out), x_out
-    _check("w4_block_norm", load().w4_block_norm(
-        _ptr(y), r.data_ptr(), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(r_out), _ptr(x_out), M, K,
-        rows, res_scale, eps, w_offset, _stream(r, stream)))
+    rc = (_lib or load()).w4_block_norm(
+        None if y is None else y.data_ptr(), r.data_ptr(),
+        None if w_post is None else w_post.data_ptr(), None if gate is None else gate.data_ptr(),
+        None if w_pre is None else w_pre.data_ptr(), None if y is None else r_out.data_ptr(),
+        None if x_out is None else x_out.data_ptr(), M, K, rows, res_scale, eps, w_offset,
+        _stream(r, stream))
+    if rc:
+        raise W4Error("w4_block_norm", rc)
     return (r if y is None else r_out), x_out
 
 
@@ -719,15 +728,18 @@ def w4_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: t
     if pos is not None:
         _need(pos, torch.int32, (T,), "pos")
     if q_out is None:
-        q_out = q.new_empty(q.shape)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need(q_out, torch.bfloat16, (T, Hq, D), "q_out")
     if T == 0:
         return q_out
-    _check("w4_rope_append", load().w4_rope_append(
+    rc = (_lib or load()).w4_rope_append(
         kv, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-        _ptr(goff), _ptr(pos), inv_freq.data_ptr(), mscale, 2 * n,
-        1 if interleaved else 0, q_out.data_ptr(), T, Hq, _stream(q, stream)))
+        None if goff is None else goff.data_ptr(), None if pos is None else pos.data_ptr(),
+        inv_freq.data_ptr(), mscale, 2 * n, 1 if interleaved else 0, q_out.data_ptr(), T, Hq,
+        _stream(q, stream))
+    if rc:
+        raise W4Error("w4_rope_append", rc)
     return q_out
 
 
@@ -737,7 +749,7 @@ def w4_attn_decode_workspace_bytes(q_heads: int, heads: int, head_dim: int) -> i
 
 def _attn_outputs(q, out, lse):
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _need(out, torch.bfloat16, q.shape, "out")
     if lse is not None:
@@ -764,13 +776,21 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     out = _attn_outputs(q, out, lse)
     if B == 0 or Hq == 0:
         return out
-    lib = load()
-    _call_with_workspace(
-        lib.w4_attn_decode, "w4_attn_decode",
-        (kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), _ptr(lse), Hq, max_len,
-         D ** -0.5 if scale is None else scale, window, sinks),
-        (_stream(q, stream),), q.device, workspace,
-        lambda: lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D))
+    lib = _lib or load()
+    ws = workspace if workspace is not None else _ws.get(q.get_device())
+    rc = lib.w4_attn_decode(
+        kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), None if lse is None else lse.data_ptr(), Hq,
+        max_len, D ** -0.5 if scale is None else scale, window, sinks,
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(q, stream))
+    if rc == W4_ERR_WORKSPACE and workspace is None:
+        ws = _workspace(q.device, lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D))
+        rc = lib.w4_attn_decode(
+            kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), None if lse is None else lse.data_ptr(), Hq,
+            max_len, D ** -0.5 if scale is None else scale, window, sinks, ws.data_ptr(), ws.numel(),
+            _stream(q, stream))
+    if rc:
+        raise W4Error("w4_attn_decode", rc)
     return out
 
 
@@ -791,9 +811,12 @@ def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     out = _attn_outputs(q, out, lse)
     if T == 0 or Hq == 0:
         return out
-    _check("w4_attn_prefill", load().w4_attn_prefill(
-        kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(), _ptr(lse), T, Hq, max_q,
-        max_len, D ** -0.5 if scale is None else scale, window, sinks, _stream(q, stream)))
+    rc = (_lib or load()).w4_attn_prefill(
+        kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), T, Hq, max_q, max_len,
+        D ** -0.5 if scale is None else scale, window, sinks, _stream(q, stream))
+    if rc:
+        raise W4Error("w4_attn_prefill", rc)
     return out
 
 
