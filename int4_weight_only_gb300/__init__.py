@@ -1,4 +1,5 @@
-"""Python binding of libw4 (the INT4 weight-only linear layer for GB300).
+"""Python binding of libw4 (the INT4 weight-only linear layer for GB300 and the
+operators of a decoder block around it).
 
 The functions here carry the names of the C entry points in ``include/w4.h``
 and only marshal arguments: they check dtypes and shapes of torch CUDA
