@@ -41,6 +41,11 @@
 // bits of them: the second product costs nothing under the loads (8 sequences
 // of 128k keys: 331 us with it, 330 without) and brings the output's error
 // from 1.4 times that of one rounding down to it.
+//
+// Measured (28 / 4 heads of 128): 8 sequences of 128k keys 331-338 us, 0.91-0.93
+// of the measured copy rate; 64 ragged ones (1 to 8192 keys) 41 us, 0.68 (CTAs
+// finish 33 us after the start on average); one of 517 keys 7.1 us of latency
+// (lookup, first keys, join).
 #include "attn_device.cuh"
 #include "w4_internal.h"
 
@@ -49,7 +54,9 @@
 namespace w4 {
 namespace {
 
-constexpr int kItemUnits = 2;           // what starting and joining an item costs, in units
+// What starting and joining an item costs, in units: 64 ragged sequences take 55 us
+// with 0, 42 with 1, 41 with 2 and 3; uniform long ones do not depend on it.
+constexpr int kItemUnits = 2;
 constexpr float kLazy = 8.f;            // log2 units the maximum may lag behind
 
 // One CTA per SM; warps and ring depth fill its registers and shared memory.

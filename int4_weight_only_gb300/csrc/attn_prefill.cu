@@ -42,6 +42,13 @@
 //                   row at its end (attend_row)
 // Every wait is bounded (mbar_wait); copies and MMAs in flight are drained
 // before the CTA ends.
+//
+// Measured (28 / 4 heads of 128): 8192 tokens 366 us, 1314 TFLOP/s (the softmax
+// taken out: 1573); 2048 behind 14336 357 us; 2048 tokens 38.9 us.  Bound by
+// shared memory under the MMAs: a step reads 128 KB for its two score products
+// and 64 KB for its value products and takes 64 KB of copies, 2048 cycles at
+// 128 bytes, as many as its MMAs take; then by the chain from a score product
+// over its softmax to the next.
 #include "attn_device.cuh"
 #include "w4_internal.h"
 
@@ -811,8 +818,10 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     // CTAs of a cluster that share an item: the fewest with the shortest last turn,
     // from upper bounds of the items and of an item's steps.  In units of a step
     // (1.8 us for heads of 128), starting and finishing an item costs about 3, with
-    // the join of its parts 5: 2048 tokens behind 14336 take 425 us in two turns of
-    // whole items and 16 tokens behind 8176 take 132 us on one CTA each.
+    // the join of its parts 5.  On 1, 2, 4, 8 CTAs an item (28 / 4 heads of 128):
+    // 16 tokens behind 8176 take 87.5, 52.8, 31.4, 21.2 us, 2048 behind 14336 409,
+    // 357, 464, 658, twice 300 behind 3796 61, 42, 59, 107, eight prompts of 512
+    // tokens 41, 105, 206, 454; the rule takes the best of each.
     const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)a.max_len);
     long long keys = cap;
     if (a.window) keys = std::min(cap, (long long)a.window + 2 * tpt + kN + std::min<long long>(a.sinks, cap));

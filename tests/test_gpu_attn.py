@@ -205,6 +205,13 @@ def test_prefill_heads(w4, Hq, Hkv, D):
     prefill(w4, [1, 3, 17, 40, 130], [1, 70, 17, 41, 130], Hq, Hkv, D, seed=Hq)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(128, 1, 64), (64, 1, 128), (130, 2, 64), (1, 1, 128)])
+def test_wide_and_single_groups(w4, Hq, Hkv, D):
+    """Up to 128 query heads on one key-value head; a single head."""
+    decode(w4, [1, 33, 150], Hq, Hkv, D, seed=Hq)
+    prefill(w4, [3, 1, 5], [40, 1, 140], Hq, Hkv, D, seed=Hq)
+
+
 @pytest.mark.parametrize("qs,lens", [([1], [1]), ([128], [128]), ([129], [129]), ([127], [255]), ([5], [1030]),
                                      ([300], [333]), ([64, 1, 200, 0, 31], [64, 500, 201, 60, 31])])
 @pytest.mark.parametrize("D", [64, 128])
