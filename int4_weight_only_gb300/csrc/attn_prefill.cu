@@ -653,7 +653,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         mx[e] = i + 4 < kN ? fmaxf(fmaxf(mx[e], s[i + e]), s[i + 4 + e]) : fmaxf(mx[e], s[i + e]);
                 const float mn = fmaxf(fmaxf(m, mx[0]), fmaxf(fmaxf(mx[1], mx[2]), mx[3]));
                 // S complete means this tile's O of the step before is complete too
-                if (__any_sync(0xffffffffu, (mn - m) * sc > kLazy)) {
+                // rows without a query hold what was there before: they have no say, or the
+                // same inputs would not give the same bits
+                if (__any_sync(0xffffffffu, have && (mn - m) * sc > kLazy)) {
                     const float f = mn == m ? 1.f : ex2_approx((m - mn) * sc);
                     m = mn;
                     l *= f;

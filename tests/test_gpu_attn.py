@@ -336,6 +336,35 @@ def test_prefill_matches_decode(w4):
     assert (a.float() - b.float()).abs().max() < 0.05
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(14, 2, 64), (28, 4, 128), (9, 3, 64), (17, 1, 128), (16, 2, 128)])
+@pytest.mark.parametrize("qs,lens", [([50, 37], [400, 300]), ([300, 260], [300, 2000]), ([128] * 40, [128] * 40)])
+def test_prefill_same_bits(w4, Hq, Hkv, D, qs, lens):
+    """A sequence's result depends on its own inputs alone: not on the tokens that
+    follow it, nor on what earlier calls left on chip in rows that no query fills."""
+    cache = Paged(lens, Hkv, D, 16, fill=0.0)
+    cache.fill_random(2.0)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(qs)]), dtype=torch.int32, device="cuda")
+    T, sc = sum(qs), D ** -0.5
+
+    def run(q, heads):
+        return w4.w4_attn_prefill(q, cache.k[:, :heads], cache.v[:, :heads], off, cache.kv_len, cache.table, max(qs),
+                                  max(lens), sc).clone()
+
+    q = randn_bf16(T, Hq, D, seed=3, scale=2.0).cuda()
+    wide = randn_bf16(T, 16 * Hkv, D, seed=4).cuda()      # 16 heads to one: every row of a tile is a query's
+    first = None
+    for left in (1.0, 60.0, 1.0, 300.0):
+        run((wide * left).bfloat16(), Hkv)
+        y = run(q, Hkv)
+        other = q.clone()
+        other[qs[0]:] *= left
+        z = run(other, Hkv)[:qs[0]]
+        first = y if first is None else first
+        assert torch.equal(first, y), f"after queries of size {left}"
+        assert torch.equal(first[:qs[0]], z), f"before tokens of size {left}"
+    assert w4.w4_get_device_error() == 0
+
+
 def test_prefill_bad_device_data(w4):
     q = randn_bf16(60, 4, 64, seed=1).cuda()
 
