@@ -46,17 +46,4 @@ __device__ __forceinline__ int page_of(const w4_paged_kv& kv, int b, int j, int*
     return p;
 }
 
-// Rows [t0, t1) of sequence b from its token offsets; an offset outside
-// [0, T] or decreasing leaves the sequence without rows and raises the flag.
-__device__ __forceinline__ void seq_rows(const int32_t* goff, int b, int T, int* t0, int* t1,
-                                         int* err) {
-    int o0 = __ldg(goff + b), o1 = __ldg(goff + b + 1);
-    if (o0 < 0 || o1 < o0 || o1 > T) {
-        atomicCAS(err, 0, W4_ERR_GROUP_TOKENS);
-        o0 = o1 = 0;
-    }
-    *t0 = o0;
-    *t1 = o1;
-}
-
 }  // namespace w4
