@@ -504,6 +504,18 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         const uint32_t iv = 2 * step + 1, ik = 2 * step + 2;    // ring items of V c and K c + 1
                         const int sv = iv % NS, sk = ik % NS;
                         bool v_here = false, k_here = false;
+                        auto next_s = [&](int x) {        // S_x of step c + 1
+                            if (!k_here) ok = wait(&ctl->full[sk], (ik / NS) & 1);
+                            if (!ok) return;
+                            k_here = true;
+                            tc_fence_after();
+                            mma_s(x, sk);
+                            commit_elected(&ctl->sfull[x]);
+                            if (x == ntile - 1) {
+                                commit_elected(&ctl->empty[sk]);
+                                if (c + 2 == c1) commit_elected(&ctl->qempty);
+                            }
+                        };
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             if (!ok || c >= end[x]) continue;
@@ -526,16 +538,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                                 commit_elected(&ctl->ofull[x]);
                                 ++no[x];
                             } else {
-                                if (!k_here) ok = wait(&ctl->full[sk], (ik / NS) & 1);
-                                if (!ok) continue;
-                                k_here = true;
-                                tc_fence_after();
-                                mma_s(x, sk);
-                                commit_elected(&ctl->sfull[x]);
-                            }
-                            if (x == ntile - 1 && c + 1 < c1) {
-                                commit_elected(&ctl->empty[sk]);
-                                if (c + 2 == c1) commit_elected(&ctl->qempty);
+                                next_s(x);
                             }
                         }
                     }
