@@ -43,12 +43,15 @@
 // Every wait is bounded (mbar_wait); copies and MMAs in flight are drained
 // before the CTA ends.
 //
-// Measured (28 / 4 heads of 128): 8192 tokens 366 us, 1314 TFLOP/s (the softmax
-// taken out: 1573); 2048 behind 14336 357 us; 2048 tokens 38.9 us.  Bound by
-// shared memory under the MMAs: a step reads 128 KB for its two score products
-// and 64 KB for its value products and takes 64 KB of copies, 2048 cycles at
-// 128 bytes, as many as its MMAs take; then by the chain from a score product
-// over its softmax to the next.
+// Measured (28 / 4 heads of 128): 8192 tokens 355 us, 1353 TFLOP/s (347 with its
+// exponentials left out); 2048 behind 14336 345 us; 2048 tokens 38.6 us.  Bound
+// by shared memory under the MMAs: a step reads 128 KB for its two score
+// products and 64 KB for its value products and takes 64 KB of copies, 2048
+// cycles at 128 bytes, as many as its MMAs take; then by the chain from a score
+// product over its softmax to the next.  Heads of 64 are bound by that chain: a
+// step takes 1.46 us with two tiles, 1.20 with one.  P in TMEM columns of its
+// own, which they have room for, so that the next score product starts as soon
+// as S is read, took 1.63: the two tiles then run their softmax at one time.
 #include "attn_device.cuh"
 #include "w4_internal.h"
 
@@ -824,9 +827,9 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     // from upper bounds of the items and of an item's steps.  In units of a step
     // (1.8 us for heads of 128), starting and finishing an item costs about 3, with
     // the join of its parts 5.  On 1, 2, 4, 8 CTAs an item (28 / 4 heads of 128):
-    // 16 tokens behind 8176 take 87.5, 52.8, 31.4, 21.2 us, 2048 behind 14336 409,
-    // 357, 464, 658, twice 300 behind 3796 61, 42, 59, 107, eight prompts of 512
-    // tokens 41, 105, 206, 454; the rule takes the best of each.
+    // 16 tokens behind 8176 take 86.9, 52.2, 31.3, 21.0 us, 2048 behind 14336 393,
+    // 345, 453, 647, twice 300 behind 3796 59, 42, 59, 107, eight prompts of 512
+    // tokens 41, 105, 206, 452; the rule takes the best of each.
     const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)a.max_len);
     long long keys = cap;
     if (a.window) keys = std::min(cap, (long long)a.window + 2 * tpt + kN + std::min<long long>(a.sinks, cap));
