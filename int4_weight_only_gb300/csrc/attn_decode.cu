@@ -37,10 +37,11 @@
 // The running maximum is lazy: a warp keeps the maximum it scaled by until a
 // score exceeds it by 2^8, so the common step has no shuffles and no rescaling.
 // l sums the fp32 weights.  As matrix operands they are two bf16 values, the
-// rounded weight and what its rounding left, so the values' products see 16
+// weight's upper half and what that leaves, so the values' products see 15
 // bits of them: the second product costs nothing under the loads (8 sequences
 // of 128k keys: 331 us with it, 330 without) and brings the output's error
-// from 1.4 times that of one rounding down to it.
+// from 1.4 times that of one rounding down to it.  Both parts of a weight are
+// positive, so an infinite value that the token sees gives the infinity.
 //
 // Measured (28 / 4 heads of 128): 8 sequences of 128k keys 331-338 us, 0.91-0.93
 // of the measured copy rate; 64 ragged ones (1 to 8192 keys) 41 us, 0.68 (CTAs
@@ -364,7 +365,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                         for (int t = 0; t < D / 16; ++t) { o[x][t][e] *= f; o[x][t][e + 2] *= f; }
                     }
             }
-            uint32_t pb[NT][2], pl[NT][2];      // bf16 weights, and what their rounding left
+            uint32_t pb[NT][2], pl[NT][2];      // the weights' upper halves, and what they leave
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
                 float w0[4];
@@ -375,9 +376,11 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float u = w0[2 * h], v = w0[2 * h + 1];
-                    const uint32_t hi = pack_bf16x2(u, v);
+                    const uint32_t hi = prmt(__float_as_uint(u), __float_as_uint(v), 0x7632);
                     pb[x][h] = movmatrix_trans(hi);
-                    pl[x][h] = movmatrix_trans(pack_bf16x2(u - bf16x2_lo(hi), v - bf16x2_hi(hi)));
+                    // the factor keeps the rest of a bf16 weight above zero: 0 * inf is NaN
+                    constexpr float kUp = 1.f + 0x1p-23f;
+                    pl[x][h] = movmatrix_trans(pack_bf16x2(fmaf(u, kUp, -bf16x2_lo(hi)), fmaf(v, kUp, -bf16x2_hi(hi))));
                 }
             }
 #pragma unroll
