@@ -136,17 +136,25 @@ def _check(fn: str, rc: int):
 
 # ------------------------------------------------------------- workspace
 _ws = {}
+_ws_outgrown = []       # replaced buffers: graphs captured with them go on using them
 
 
 def _workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
-    """A per-device zero-filled scratch buffer (grown on demand); the kernels
-    leave its counters at zero after each call."""
+    """A per-device zero-filled scratch buffer; the kernels leave its counters
+    at zero after each call.  4 MiB hold what one-token attention needs (2.6 MB
+    on 152 SMs) and the usual split-K layers; a buffer that is too small is
+    replaced by one of at least twice its size and kept, so that graphs and
+    kernels on other streams that have its address stay valid."""
     idx = device.index if device.index is not None else torch.cuda.current_device()
     buf = _ws.get(idx)
     if nbytes == 0:
         return buf
     if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+        size = max(nbytes, 4 << 20)
+        if buf is not None:
+            size = max(size, 2 * buf.numel())
+            _ws_outgrown.append(buf)
+        buf = torch.zeros(size, dtype=torch.uint8, device=device)
         _ws[idx] = buf
     return buf
 
