@@ -144,12 +144,16 @@ def _workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
     at zero after each call.  4 MiB hold what one-token attention needs (2.6 MB
     on 152 SMs) and the usual split-K layers; a buffer that is too small is
     replaced by one of at least twice its size and kept, so that graphs and
-    kernels on other streams that have its address stay valid."""
+    kernels on other streams that have its address stay valid.  While a graph is
+    captured its memory and the zero fill are the graph's: a buffer that does
+    not exist yet is then made for the one call and not shared."""
     idx = device.index if device.index is not None else torch.cuda.current_device()
     buf = _ws.get(idx)
     if nbytes == 0:
         return buf
     if buf is None or buf.numel() < nbytes:
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(nbytes, dtype=torch.uint8, device=device)
         size = max(nbytes, 4 << 20)
         if buf is not None:
             size = max(size, 2 * buf.numel())

@@ -51,3 +51,28 @@ def test_a_graph_of_linears_outlives_the_first_attention_call(lib):
         g.replay()
         assert torch.equal(y, want)
     assert all((t == 0xA5).all() for t in taken) and lib.w4_get_device_error() == 0
+
+
+def test_a_first_call_inside_a_capture(lib):
+    """The first calls without a workspace of their own are captured; eager calls after it, before
+    the graph ever runs, find counters at zero."""
+    args, y = linear()
+    att = attention()
+    out = torch.empty_like(att[0])
+    own = torch.zeros(4 << 20, dtype=torch.uint8, device="cuda")
+    lib.w4a16_linear(*args, workspace=own)
+    lib.w4_attn_decode(*att, workspace=own)
+    assert not lib._ws
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.w4a16_linear(*args, y=y)
+        lib.w4_attn_decode(*att, out=out)
+    torch.cuda.synchronize()
+    want, want_o = lib.w4a16_linear(*args).clone(), lib.w4_attn_decode(*att).clone()
+    for _ in range(3):
+        y.fill_(0)
+        out.fill_(0)
+        g.replay()
+        assert torch.equal(y, want) and torch.equal(out, want_o)
+    assert torch.equal(lib.w4a16_linear(*args), want) and torch.equal(lib.w4_attn_decode(*att), want_o)
+    assert lib.w4_get_device_error() == 0

@@ -16,6 +16,7 @@ def lib(monkeypatch):
     zeros = torch.zeros
     monkeypatch.setattr(_lib, "_ws", {})
     monkeypatch.setattr(torch, "zeros", lambda n, dtype, device: zeros(n, dtype=dtype))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return _lib
 
 
@@ -33,3 +34,14 @@ def test_the_first_buffer_serves_attention(lib):
     """152 SMs x 2 parts x 16 heads x (128 + 2) floats behind the counters."""
     first = lib._workspace(DEV, 1000)
     assert lib._workspace(DEV, 65536 + 152 * 2 * 16 * 130 * 4) is first
+
+
+def test_a_buffer_made_during_a_capture_is_not_shared(lib, monkeypatch):
+    """Its zero fill has only been recorded, and its memory is the graph's."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    assert lib._workspace(DEV, 1000).numel() >= 1000 and not lib._ws
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    eager = lib._workspace(DEV, 1000)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    assert lib._workspace(DEV, 1000) is eager
+    assert lib._workspace(DEV, eager.numel() + 1) is not eager and lib._workspace(DEV, 1000) is eager
