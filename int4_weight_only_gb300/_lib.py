@@ -139,26 +139,28 @@ _ws = {}
 _ws_outgrown = []       # replaced buffers: graphs captured with them go on using them
 
 
-def _workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
+def _workspace(device: torch.device, nbytes: int, stream=None) -> Optional[torch.Tensor]:
     """A per-device zero-filled scratch buffer; the kernels leave its counters
     at zero after each call.  4 MiB hold what one-token attention needs (2.6 MB
     on 152 SMs) and the usual split-K layers; a buffer that is too small is
     replaced by one of at least twice its size and kept, so that graphs and
     kernels on other streams that have its address stay valid.  While a graph is
     captured its memory and the zero fill are the graph's: a buffer that does
-    not exist yet is then made for the one call and not shared."""
+    not exist yet is then made for the one call and not shared.  `stream` is the
+    call's own (None: torch's current one): the fill is ahead of the kernel there."""
     idx = device.index if device.index is not None else torch.cuda.current_device()
     buf = _ws.get(idx)
     if nbytes == 0:
         return buf
     if buf is None or buf.numel() < nbytes:
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        size = max(nbytes, 4 << 20)
-        if buf is not None:
-            size = max(size, 2 * buf.numel())
-            _ws_outgrown.append(buf)
-        buf = torch.zeros(size, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+            size = max(nbytes, 4 << 20)
+            if buf is not None:
+                size = max(size, 2 * buf.numel())
+                _ws_outgrown.append(buf)
+            buf = torch.zeros(size, dtype=torch.uint8, device=device)
         _ws[idx] = buf
     return buf
 
@@ -166,7 +168,7 @@ def _workspace(device: torch.device, nbytes: int) -> Optional[torch.Tensor]:
 W4_ERR_WORKSPACE = -6
 
 
-def _call_with_workspace(fn, name, args_before, args_after, device, workspace, need_bytes):
+def _call_with_workspace(fn, name, args_before, args_after, device, workspace, need_bytes, stream=None):
     """Call fn(*args_before, ws_ptr, ws_bytes, *args_after).  Without a caller
     workspace the cached one goes in as it is; only when the library answers
     that it is too small is the size queried and the buffer grown (so the
@@ -176,7 +178,7 @@ def _call_with_workspace(fn, name, args_before, args_after, device, workspace, n
     wsb = 0 if ws is None else ws.numel() * ws.element_size()
     rc = fn(*args_before, _ptr(ws), wsb, *args_after)
     if rc == W4_ERR_WORKSPACE and workspace is None:
-        ws = _workspace(device, need_bytes())
+        ws = _workspace(device, need_bytes(), stream)
         rc = fn(*args_before, _ptr(ws), ws.numel() * ws.element_size(), *args_after)
     _check(name, rc)
 
@@ -256,7 +258,7 @@ def w4a16_linear(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
         (_ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(y), M, N, K,
          int(group_size), 1 if zeros is None else 0),
         (_stream(x, stream),), x.device, workspace,
-        lambda: lib.w4a16_workspace_bytes(M, N, K, group_size))
+        lambda: lib.w4a16_workspace_bytes(M, N, K, group_size), stream)
     return y
 
 
@@ -284,7 +286,7 @@ def w4a16_linear_partial(x: torch.Tensor, packed: torch.Tensor, scales: torch.Te
         (_ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(y32), M, N, K,
          int(group_size), 1 if zeros is None else 0),
         (_stream(x, stream),), x.device, workspace,
-        lambda: lib.w4a16_workspace_bytes(M, N, K, group_size))
+        lambda: lib.w4a16_workspace_bytes(M, N, K, group_size), stream)
     return y32
 
 
@@ -348,7 +350,7 @@ def w4a16_linear_bf16p(x: torch.Tensor, packed: torch.Tensor, scales_b: torch.Te
         (_ptr(x), _ptr(packed), _ptr(scales_b), _ptr(offsets_b), _ptr(bias), _ptr(y), M, N, K,
          int(group_size)),
         (_stream(x, stream),), x.device, workspace,
-        lambda: lib.w4a16_workspace_bytes(M, N, K, group_size))
+        lambda: lib.w4a16_workspace_bytes(M, N, K, group_size), stream)
     return y
 
 
@@ -391,7 +393,7 @@ def w4a16_linear_swiglu(x: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
         (_ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(y), M, F, K,
          int(group_size), 1 if zeros is None else 0),
         (_stream(x, stream),), x.device, workspace,
-        lambda: lib.w4a16_workspace_bytes(M, 2 * F, K, group_size))
+        lambda: lib.w4a16_workspace_bytes(M, 2 * F, K, group_size), stream)
     return y
 
 
@@ -431,7 +433,7 @@ def w4a16_linear_swiglu_q8(x: torch.Tensor, packed: torch.Tensor, scales: torch.
         (_ptr(x), _ptr(packed), _ptr(scales), _ptr(zeros), _ptr(bias), _ptr(y), _ptr(qx),
          _ptr(sx), M, F, K, int(group_size), 1 if zeros is None else 0, int(q_group_size)),
         (_stream(x, stream),), dev, workspace,
-        lambda: max(lib.w4a16_workspace_bytes(M, 2 * F, K, group_size), 64 << 10))
+        lambda: max(lib.w4a16_workspace_bytes(M, 2 * F, K, group_size), 64 << 10), stream)
     return y, qx, sx
 
 
@@ -605,7 +607,7 @@ def w4a8_linear(qx: torch.Tensor, sx: torch.Tensor, packed: torch.Tensor,
         (_ptr(qx), _ptr(sx), _ptr(packed), _ptr(w_scales), _ptr(bias), _ptr(y), _ptr(acc_out),
          M, N, K, int(group_size)),
         (_stream(qx, stream),), qx.device, workspace,
-        lambda: lib.w4a8_workspace_bytes(M, N, K, group_size))
+        lambda: lib.w4a8_workspace_bytes(M, N, K, group_size), stream)
     return y, acc_out
 
 
@@ -796,7 +798,7 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
         _stream(q, stream))
     if rc == W4_ERR_WORKSPACE and workspace is None:
-        ws = _workspace(q.device, lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D))
+        ws = _workspace(q.device, lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D), stream)
         rc = lib.w4_attn_decode(
             kv, q.data_ptr(), qs[0], qs[1], out.data_ptr(), None if lse is None else lse.data_ptr(), Hq,
             max_len, D ** -0.5 if scale is None else scale, window, sinks, ws.data_ptr(), ws.numel(),

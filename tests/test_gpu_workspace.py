@@ -76,3 +76,29 @@ def test_a_first_call_inside_a_capture(lib):
         assert torch.equal(y, want) and torch.equal(out, want_o)
     assert torch.equal(lib.w4a16_linear(*args), want) and torch.equal(lib.w4_attn_decode(*att), want_o)
     assert lib.w4_get_device_error() == 0
+
+
+def test_a_first_call_on_another_stream(lib):
+    """The current stream is busy: the first call on another one does not wait for it, and
+    its counters are cleared all the same."""
+    args, y = linear()
+    att = attention()
+    own = torch.zeros(4 << 20, dtype=torch.uint8, device="cuda")
+    want, want_o = lib.w4a16_linear(*args, workspace=own).clone(), lib.w4_attn_decode(*att, workspace=own).clone()
+    side = torch.cuda.Stream()
+    for first in ("linear", "attention"):
+        lib._ws.clear()
+        y.fill_(0)
+        out = torch.zeros_like(want_o)
+        torch.cuda.synchronize()
+        done = torch.cuda.Event()
+        torch.cuda._sleep(200_000_000)
+        done.record()
+        if first == "linear":
+            lib.w4a16_linear(*args, y=y, stream=side)
+        lib.w4_attn_decode(*att, out=out, stream=side)
+        side.synchronize()
+        assert not done.query()
+        assert torch.equal(out, want_o) and (first != "linear" or torch.equal(y, want))
+        torch.cuda.synchronize()
+        assert not lib._ws[0][:65536].any()

@@ -1,4 +1,5 @@
 """The binding's shared workspace: who keeps it, on host buffers (no GPU)."""
+import contextlib
 import weakref
 
 import pytest
@@ -14,8 +15,22 @@ def lib(monkeypatch):
     ensure_built()
     from int4_weight_only_gb300 import _lib
     zeros = torch.zeros
+    streams = [None]                    # the current one and, innermost last, those entered
+    filled = []                    # the stream of each zero fill
+
+    @contextlib.contextmanager
+    def stream(s):
+        streams.append(s if s is not None else streams[-1])
+        yield
+        streams.pop()
+
+    def fill(n, dtype, device):
+        filled.append(streams[-1])
+        return zeros(n, dtype=dtype)
     monkeypatch.setattr(_lib, "_ws", {})
-    monkeypatch.setattr(torch, "zeros", lambda n, dtype, device: zeros(n, dtype=dtype))
+    monkeypatch.setattr(_lib, "filled", filled, raising=False)
+    monkeypatch.setattr(torch, "zeros", fill)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return _lib
 
@@ -45,3 +60,16 @@ def test_a_buffer_made_during_a_capture_is_not_shared(lib, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
     assert lib._workspace(DEV, 1000) is eager
     assert lib._workspace(DEV, eager.numel() + 1) is not eager and lib._workspace(DEV, 1000) is eager
+
+
+def test_the_fill_is_on_the_calls_own_stream(lib):
+    """Elsewhere it could come after the kernel."""
+    calls = []
+
+    def fn(ptr, nbytes, raw):
+        calls.append(nbytes)
+        return 0 if nbytes >= 1000 else lib.W4_ERR_WORKSPACE
+    lib._call_with_workspace(fn, "fn", (), (7,), DEV, None, lambda: 1000, "side")
+    assert lib.filled == ["side"] and calls[0] == 0 and calls[1] >= 1000
+    lib._workspace(DEV, 2 * calls[1])
+    assert lib.filled == ["side", None]
