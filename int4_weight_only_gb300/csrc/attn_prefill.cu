@@ -37,9 +37,10 @@
 //                   O_A += P_A V, S_A = Q_A K', O_B += P_B V, S_B = Q_B K'
 //   warps 10, 11    release V blocks to the MMAs.  In a block that not every
 //                   row sees entirely, a weight of zero does not make a NaN
-//                   harmless: slots past the end are zeroed, and if a hidden
-//                   slot holds a NaN or infinity the part is recomputed row by
-//                   row at its end (attend_row)
+//                   harmless: slots past the end are zeroed, and a NaN or
+//                   infinity in a slot that some row does not see is taken out
+//                   and added at the part's end to the rows that see it
+//                   (add_non_finite)
 // Every wait is bounded (mbar_wait); copies and MMAs in flight are drained
 // before the CTA ends.
 //
@@ -77,7 +78,7 @@ struct Ctl {
     uint32_t tmem;
     int abort;
     // by V-releasing warp and part number mod 4: a slot that some row does not see
-    // holds a non-finite value.  No warp is more than two parts ahead of another
+    // held a non-finite value.  No warp is more than two parts ahead of another
     int bad[2][4];
 };
 
@@ -146,6 +147,12 @@ __device__ __forceinline__ uint32_t cluster_nctas() {
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};"
                  :: "r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // 128 consecutive columns of this warp's 32 TMEM lanes (one lane per thread),
@@ -287,56 +294,80 @@ struct Walk {
         const int each = steps / n, rest = steps - each * n;
         return i * each + min(i, rest);
     }
-    // every row of the item sees all of block j0
-    __device__ __forceinline__ bool all_see(const AttnArgs& a, int j0) const {
-        return j0 + kN - 1 <= p0 && (a.window == 0 || p1 - j0 < a.window || j0 + kN <= a.sinks);
-    }
 };
 
-// One row of a part by itself, straight from the definition: used only when a
-// hidden value is not finite, where the matrix product would let it through.
-// Blocks c0 .. c1 - 1; a whole row goes to `out`, a part's to the join's row at
-// shared::cluster address dst_o, m and l to dst_ml.
+// Every row of the tokens at p0 .. p1 sees all of block j0.
+__device__ __forceinline__ bool all_see(const AttnArgs& a, int j0, int p0, int p1) {
+    return j0 + kN - 1 <= p0 && (a.window == 0 || p1 - j0 < a.window || j0 + kN <= a.sinks);
+}
+
+// The slots lo .. hi - 1 of such a block that no row's causal mask or window hides.
+__device__ __forceinline__ void seen_slots(const AttnArgs& a, int j0, int p0, int p1, int* lo, int* hi) {
+    *hi = min(max(p0 + 1 - j0, 0), kN);
+    *lo = a.window ? min(max(p1 - a.window + 1 - j0, 0), *hi) : 0;
+}
+
+__device__ __forceinline__ bool non_finite(uint32_t bf16_bits) { return (bf16_bits & 0x7F80u) == 0x7F80u; }
+
+// Adds to a finished row of o the values that the V release took out of blocks
+// c0 .. c1 - 1 and that the row's token, at position p, sees: a weight is positive,
+// so an infinity or NaN reaches the sum as it is.  A warp's rows have the item's
+// sequence and key-value head in common, so its lanes look through the slots together
+// (the few blocks with hidden slots, once each).  The row is out[0 .. D - 1], or, of a part
+// to be joined, fp32 at shared::cluster address dst_o.
 template <int D>
-__device__ __noinline__ void attend_row(const AttnArgs& a, int b, int hk, int head, int tok, int p, KeyBlocks kb,
-                                        int c0, int c1, uint32_t dst_o, uint32_t dst_ml) {
-    const int lg = 31 - __clz(a.kv.page_size);
-    const uint16_t* q = a.q + tok * a.q_tok + head * a.q_head;
-    const size_t row = (size_t)tok * a.Hq + head;
-    float m = kNegInf, l = 0.f;
-    for (int d0 = -32; d0 < D; d0 += 32) {          // first pass: m and l; then 32 columns a pass
-        float o[32];
-        for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        for (int c = c0 * kN; c < c1 * kN; ++c) {
-            const int j = kb(c / kN) * kN + c % kN;
-            if (!key_visible(j, p, a.window, a.sinks)) continue;
-            const int page = page_of(a.kv, b, j >> lg, a.err), at = j & (a.kv.page_size - 1);
-            const uint16_t* k = a.kv.k + page * a.kv.k_page_stride + hk * a.kv.k_head_stride + at * a.kv.k_slot_stride;
-            float s = 0.f;
-            for (int d = 0; d < D; ++d) s = fmaf(bf16_bits_to_f32(q[d]), bf16_bits_to_f32(k[d]), s);
-            if (d0 < 0) {
-                const float mn = fmaxf(m, s);
-                l = l * (mn == m ? 1.f : ex2_approx((m - mn) * a.scale)) + ex2_approx((s - mn) * a.scale);
-                m = mn;
-            } else {
-                const uint16_t* v = a.kv.v + page * a.kv.v_page_stride + hk * a.kv.v_head_stride +
-                                    at * a.kv.v_slot_stride + d0;
-                const float w = ex2_approx((s - m) * a.scale);
-                for (int i = 0; i < 32; ++i) o[i] = fmaf(w, bf16_bits_to_f32(v[i]), o[i]);
+__device__ __noinline__ void add_non_finite(const AttnArgs& a, int b, int hk, int p0, int p1, KeyBlocks kb, int c0,
+                                            int c1, int p, uint16_t* out, uint32_t dst_o) {
+    const int lane = threadIdx.x & 31, lg = 31 - __clz(a.kv.page_size), first = max(p0, 0);
+    for (int c = c0; c < c1; ++c) {
+        const int j0 = kb(c) * kN;
+        if (all_see(a, j0, p0, p1)) continue;
+        int lo, hi;
+        seen_slots(a, j0, p0, p1, &lo, &hi);
+        for (int i0 = 0; i0 < kN * (D / 8); i0 += 32) {
+            const int s = (i0 + lane) / (D / 8), j = j0 + s, d = (i0 + lane) % (D / 8) * 8;
+            // taken out, and some row sees it
+            const bool in = (s < lo || s >= hi) && j <= p1 &&
+                            (a.window == 0 || first - j < a.window || j < a.sinks);
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (in)
+                u = *reinterpret_cast<const uint4*>(
+                    a.kv.v + page_of(a.kv, b, j >> lg, a.err) * a.kv.v_page_stride + hk * a.kv.v_head_stride +
+                    (j & (a.kv.page_size - 1)) * a.kv.v_slot_stride + d);
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) any |= non_finite((&u.x)[e]) || non_finite((&u.x)[e] >> 16);
+            for (uint32_t m = __ballot_sync(0xffffffffu, any); m; m &= m - 1) {
+                const int src = __ffs(m) - 1, js = __shfl_sync(0xffffffffu, j, src),
+                          ds = __shfl_sync(0xffffffffu, d, src);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w = __shfl_sync(0xffffffffu, (&u.x)[e >> 1], src), bits = e & 1 ? w >> 16 : w & 0xFFFFu;
+                    if (!non_finite(bits) || !key_visible(js, p, a.window, a.sinks)) continue;
+                    const float x = bf16_bits_to_f32((uint16_t)bits);
+                    if (dst_o) st_shared_cluster(dst_o + (ds + e) * 4, ld_shared_cluster(dst_o + (ds + e) * 4) + x);
+                    else out[ds + e] = f32_to_bf16_bits(bf16_bits_to_f32(out[ds + e]) + x);
+                }
             }
         }
-        if (d0 < 0) continue;
-        for (int i = 0; i < 32; ++i) {
-            if (dst_o) st_shared_cluster(dst_o + (d0 + i) * 4, o[i]);
-            else a.out[row * D + d0 + i] = f32_to_bf16_bits(l == 0.f ? 0.f : o[i] / l);
-        }
     }
-    if (dst_o) {
-        st_shared_cluster(dst_ml, m);
-        st_shared_cluster(dst_ml + 4, l);
-    } else if (a.lse) {
-        a.lse[row] = l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
-    }
+}
+
+// Zeros in place of the non-finite values in slots 0 .. lo - 1 and hi .. kN - 1 of a V
+// block: 16-byte pieces t, t + 64, ...  Within the check that finds them it costs
+// every call 1.2 us, inlined behind it 0.8 (2048 tokens).
+template <int D>
+__device__ __noinline__ void take_out(uint8_t* v, int t, int lo, int hi) {
+    for (int panel = 0; panel < D / 64; ++panel)
+        for (int s = 0; s < 2; ++s)
+            for (int i = 8 * (s ? hi : 0) + t; i < 8 * (s ? kN : lo); i += 64) {
+                uint4* p = reinterpret_cast<uint4*>(v + panel * kN * 128) + i;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t& z = (&p->x)[e];
+                    z &= (non_finite(z) ? 0xFFFF0000u : ~0u) & (non_finite(z >> 16) ? 0x0000FFFFu : ~0u);
+                }
+            }
 }
 
 // SPLIT: the CTAs of a cluster share the steps of one item.
@@ -566,12 +597,14 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     const int st = iv % NS, j0 = w.kb(c) * kN;
                     ok = __all_sync(0xffffffffu, mbar_wait(&ctl->full[st], (iv / NS) & 1, abort, a.err));
                     if (!ok) break;
-                    if (!w.all_see(a, j0)) {
+                    if (!all_see(a, j0, w.p0, w.p1)) {
                         uint8_t* v = ring + st * SB;
-                        // rows that some query does not see: past the first token, or out of
+                        // slots that some query does not see: past the first token, or out of
                         // the last one's window
-                        const int hi = max(w.p0 + 1 - j0, 0), lo = a.window ? min(max(w.p1 - a.window + 1 - j0, 0), hi) : 0;
+                        int lo, hi;
+                        seen_slots(a, j0, w.p0, w.p1, &lo, &hi);
                         // 16-byte pieces of 128-byte rows (the swizzle only permutes a row's pieces)
+                        bool found = false;
                         auto check = [&](int r0, int r1) {
                             for (int panel = 0; panel < D / 64; ++panel)
                                 for (int i = 8 * r0 + (warp - 10) * 32 + lane; i < 8 * r1; i += 64) {
@@ -584,16 +617,19 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) {
                                         const uint32_t z = (&u.x)[e];
-                                        bad |= (z & 0x7F80u) == 0x7F80u || (z & 0x7F800000u) == 0x7F800000u;
+                                        found |= non_finite(z) || (z & 0x7F800000u) == 0x7F800000u;
                                     }
                                 }
                         };
-                        check(0, min(lo, kN));
-                        check(min(hi, kN), kN);
+                        check(0, lo);
+                        check(hi, kN);
+                        if (__any_sync(0xffffffffu, found)) {
+                            take_out<D>(v, (warp - 10) * 32 + lane, lo, hi);
+                            bad = true;
+                        }
                         fence_proxy_async_smem();
                     }
-                    const bool any = __any_sync(0xffffffffu, bad);
-                    if (lane == 0 && (c == c0 || any)) *(volatile int*)&ctl->bad[warp - 10][part & 3] = any;
+                    if (lane == 0 && (c == c0 || bad)) *(volatile int*)&ctl->bad[warp - 10][part & 3] = bad;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->vready[st]);
                 }
@@ -639,7 +675,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 tmem_ld_x128(s_addr, su);
                 float* s = reinterpret_cast<float*>(su);
                 const int j0 = w.kb(c) * kN;
-                if (!w.all_see(a, j0)) {
+                if (!all_see(a, j0, w.p0, w.p1)) {
                     // bit i of a word: key 32 z + i of the block is seen
                     const int hi = p - j0, lo = a.window ? hi - a.window + 1 : 0, sk = a.sinks - j0;
                     auto below = [](int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; };
@@ -718,7 +754,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 cluster_sync();             // every CTA is done with its Q and its ring
             }
             if (act && ok) {
-                const bool bad = ((volatile int*)ctl->bad[0])[bad_at] | ((volatile int*)ctl->bad[1])[bad_at];
+                const bool bad = __any_sync(
+                    0xffffffffu, ((volatile int*)ctl->bad[0])[bad_at] | ((volatile int*)ctl->bad[1])[bad_at]);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 // rows lie apart, so a store is one sector a lane: whole sectors where `out` allows
                 const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
@@ -726,7 +763,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(o_addr + 32 * i, o);
-                    if (bad || !have) continue;
+                    if (!have) continue;
                     if (SPLIT) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -751,9 +788,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->oempty[tile]);      // O may be overwritten
-                if (bad) {
-                    if (have) attend_row<D>(a, w.b, w.hk, head, tok, p, w.kb, c0, end, dst_o, dst_ml);
-                } else if (SPLIT) {
+                if (bad)
+                    add_non_finite<D>(a, w.b, w.hk, w.p0, w.p1, w.kb, c0, end, p, a.out + row * D, dst_o);
+                if (SPLIT) {
                     st_shared_cluster(dst_ml, m);
                     st_shared_cluster(dst_ml + 4, l);
                 } else if (have && a.lse) {
