@@ -77,9 +77,12 @@ struct Ctl {
     uint64_t drain;
     uint32_t tmem;
     int abort;
-    // by V-releasing warp and part number mod 4: a slot that some row does not see
-    // held a non-finite value.  No warp is more than two parts ahead of another
-    int bad[2][4];
+    // by V-releasing warp: the last part (counted from 1) with a slot that some row does not
+    // see and that held a non-finite value.  Written before the V block is released, so a
+    // tile that has its O finds its part's number here, or a later part's (a tile may
+    // be any number of parts behind: those of one tile do not wait for the other):
+    // looking through its slots then adds nothing
+    int bad[2];
 };
 
 // The join of an item's parts, over the space of Q and the ring: rows of o by
@@ -401,7 +404,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_init(&ctl->oempty[i], 4);
         }
         mbar_init(&ctl->drain, 1);
-        ctl->abort = 0;
+        ctl->abort = ctl->bad[0] = ctl->bad[1] = 0;
         fence_mbar_init();
     }
     if (warp == 8 && lane == 0) { tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV); }
@@ -629,7 +632,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         }
                         fence_proxy_async_smem();
                     }
-                    if (lane == 0 && (c == c0 || bad)) *(volatile int*)&ctl->bad[warp - 10][part & 3] = bad;
+                    if (lane == 0 && bad) *(volatile int*)&ctl->bad[warp - 10] = (int)part + 1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->vready[st]);
                 }
@@ -649,7 +652,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         Walk w = w0;
         for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
             const int c0 = w.c0, c1 = w.c1;
-            const uint32_t bad_at = part & 3;
+            const int bad_at = (int)part;
             if (w.kb.n > 0 && c0 < c1) ++part;
             // row r of tile x: token i0 + x tpt + r / g, query head hk g + r % g
             const int tok_in = tile * tpt + rt;
@@ -755,7 +758,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             if (act && ok) {
                 const bool bad = __any_sync(
-                    0xffffffffu, ((volatile int*)ctl->bad[0])[bad_at] | ((volatile int*)ctl->bad[1])[bad_at]);
+                    0xffffffffu, max(((volatile int*)ctl->bad)[0], ((volatile int*)ctl->bad)[1]) > bad_at);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 // rows lie apart, so a store is one sector a lane: whole sectors where `out` allows
                 const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;

@@ -85,3 +85,23 @@ def test_slots_around_every_edge(w4, Hq, Hkv, D, window, sinks, bad):
         o, off = run(w4, cache, q, qs, lens, window=window, sinks=sinks)
         for b in (0, 1, 2, 3 * copies - 1):
             compare(o, q, kv, off, qs, lens, b, [0, 1, 4, 8, 34, 35, 36, 63, 64, 69, 149, 150, 299][: qs[b]], window, sinks)
+
+
+def test_two_tile_and_one_tile_items_on_one_cta(w4):
+    """Uneven sequences, so that CTAs go from items of two tiles to several of one; every other
+    sequence ends in a value that is not finite.  The same bits at every call."""
+    r = np.random.default_rng(5)
+    qs = [int(x) for x in r.choice([1, 5, 18, 19, 36, 130, 700], 90)]
+    lens = [n + int(x) for n, x in zip(qs, r.integers(0, 40, 90))]
+    H, D = 4, 128
+    cache = Paged(lens, H, D, 16)
+    kv = cache.fill_random()
+    for b in range(0, 90, 2):
+        poison(cache, kv, b, [lens[b] - 1], float("nan"), b % H)
+    q = randn_bf16(sum(qs), 28, D, seed=1).cuda()
+    o, off = run(w4, cache, q, qs, lens)
+    for b in range(0, 90, 5):
+        compare(o, q, kv, off, qs, lens, b, [0, -1, qs[b] // 2])
+    first = o.view(torch.int16).clone()
+    for _ in range(20):
+        assert torch.equal(run(w4, cache, q, qs, lens)[0].view(torch.int16), first)
