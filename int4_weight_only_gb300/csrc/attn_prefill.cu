@@ -30,9 +30,9 @@
 //   warps 0-3, 4-7  softmax of tile A, B (one row per thread), O to memory
 //   warp 8          TMA: Q of an item, then K and V blocks into a ring of slots
 //                   (K in even, V in odd slots), one box per page and 64
-//                   columns; pages past the sequence's end are read out of
-//                   bounds of the tensor map, which fills them with zeros.  It
-//                   runs ahead into the next item
+//                   columns; pages that hold no key a row sees are read out
+//                   of bounds of the tensor map, which fills them with zeros.
+//                   It runs ahead into the next item
 //   warp 9          TMEM allocation; issues the MMAs, for each step
 //                   O_A += P_A V, S_A = Q_A K', O_B += P_B V, S_B = Q_B K'
 //   warps 10, 11    release V blocks to the MMAs.  In a block that not every
@@ -469,10 +469,13 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 ++part;
                 for (int c = c0; c < c1 && ok; ++c) {
                     const int j0 = w.kb(c) * kN;
-                    // lane: page pg of the block, 64-column panel pn; a page past the end is out of bounds
+                    // lane: page pg of the block, 64-column panel pn; a page of which no row sees a
+                    // key is not looked up (it may be gone) and loaded from out of bounds, as zeros
                     const int pg = lane % npg, pn = lane / npg, jp = j0 + pg * R;
+                    const bool seen = jp <= w.p1 && (a.window == 0 || max(w.p0, 0) - (jp + R - 1) < a.window ||
+                                                     jp < a.sinks);
                     int page = a.kv.pages;
-                    if (pn < D / 64 && jp < w.len) page = page_of(a.kv, w.b, jp >> lg, a.err);
+                    if (pn < D / 64 && seen) page = page_of(a.kv, w.b, jp >> lg, a.err);
                     for (int kv = 0; kv < 2 && ok; ++kv, ++it) {
                         const int st = it % NS;
                         if (it >= (uint32_t)NS)
