@@ -60,6 +60,8 @@ __device__ __forceinline__ RowPlace place_of(const RopeArgs& a, int t) {
         for (int b0 = 0; b0 < a.kv.batch; b0 += 32) {
             const int i = min(b0 + lane, a.kv.batch - 1);
             const int s0 = __ldg(a.goff + i), s1 = __ldg(a.goff + i + 1), len = __ldg(a.kv.kv_len + i);
+            // whether or not a row belongs to the sequence
+            if (s0 < 0 || s1 < s0 || s1 > a.T) atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
             const uint32_t m = __ballot_sync(0xffffffffu, b0 + lane < a.kv.batch && s0 <= t);
             if (m) {
                 const int f = 31 - __clz(m);
@@ -69,14 +71,9 @@ __device__ __forceinline__ RowPlace place_of(const RopeArgs& a, int t) {
                 o1 = __shfl_sync(0xffffffffu, s1, f);
                 n = __shfl_sync(0xffffffffu, len, f);
             }
-            if (!(m >> 31)) break;
+            if (!(m >> 31) && t < a.T - 1) break;         // the last row sees all offsets
         }
-        if (!found) return w;
-        if (o0 < 0 || o1 < o0 || o1 > a.T) {
-            atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
-            return w;
-        }
-        if (t >= o1) return w;
+        if (!found || o0 < 0 || o1 > a.T || t >= o1) return w;
         ahead = o1 - 1 - t;
     } else {
         n = __ldg(a.kv.kv_len + b);
