@@ -688,6 +688,8 @@ def w4_block_norm(y: Optional[torch.Tensor], r: torch.Tensor, w_pre: Optional[to
     if gate is not None:
         rows = gate.shape[0]
         _need(gate, torch.bfloat16, (rows, K), "gate")
+        if rows == 0 and M > 0:
+            raise ValueError(f"gate must have at least one row for {M} tokens")
     if M == 0:
         return (r if y is None else r_out), x_out
     rc = (_lib or load()).w4_block_norm(

@@ -136,3 +136,13 @@ def test_binding_refusals(w4):
         w4.w4_block_norm(r, r, w, gate=r[:3].contiguous())
     e = r[:0]
     assert w4.w4_block_norm(e, e, w)[1].shape == (0, 64)
+
+
+def test_a_gate_without_rows_is_refused(w4):
+    """Its pointer is null, which means no gate: it must not be taken for one."""
+    r = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        w4.w4_block_norm(r, r, w, gate=r[:0])
+    e = r[:0]
+    assert w4.w4_block_norm(e, e, w, gate=e)[1].shape == (0, 64)
