@@ -763,6 +763,11 @@ def w4_attn_decode_workspace_bytes(q_heads: int, heads: int, head_dim: int) -> i
     return int(load().w4_attn_decode_workspace_bytes(q_heads, heads, head_dim))
 
 
+def _past_32_bits(**args):
+    """ctypes would cut them to their lower 32 bits."""
+    raise ValueError(", ".join(f"{k}={v}" for k, v in args.items()) + ": more than a 32-bit integer holds")
+
+
 def _attn_outputs(q, out, lse):
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -792,6 +797,8 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     out = _attn_outputs(q, out, lse)
     if B == 0 or Hq == 0:
         return out
+    if (max_len | window | sinks) > 0x7FFFFFFF:
+        _past_32_bits(max_len=max_len, window=window, sinks=sinks)
     lib = _lib or load()
     ws = workspace if workspace is not None else _ws.get(q.get_device())
     rc = lib.w4_attn_decode(
@@ -827,6 +834,8 @@ def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     out = _attn_outputs(q, out, lse)
     if T == 0 or Hq == 0:
         return out
+    if (max_q | max_len | window | sinks) > 0x7FFFFFFF:
+        _past_32_bits(max_q=max_q, max_len=max_len, window=window, sinks=sinks)
     rc = (_lib or load()).w4_attn_prefill(
         kv, q.data_ptr(), qs[0], qs[1], goff.data_ptr(), out.data_ptr(),
         None if lse is None else lse.data_ptr(), T, Hq, max_q, max_len,

@@ -456,3 +456,19 @@ def test_binding_refusals(w4):
         w4.w4_attn_prefill(**dec, goff=goff[:2], max_q=1)
     e = q[:0]
     assert w4.w4_attn_prefill(e, c.k, c.v, goff * 0, c.kv_len, c.table, 1, 4).shape == e.shape
+
+
+def test_integers_past_32_bits_are_refused(w4):
+    """They must not be cut to their lower bits (a window of 2^32 to none)."""
+    c = Paged([3, 4], 2, 64, 16, fill=0.0)
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    goff = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    args = dict(q=q, k_cache=c.k, v_cache=c.v, kv_len=c.kv_len, table=c.table, max_len=4)
+    for big in (1 << 31, 1 << 32, (1 << 32) + 4):
+        for name in ("window", "sinks", "max_len"):
+            with pytest.raises((ValueError, w4.W4Error)):
+                w4.w4_attn_decode(**dict(args, **{name: big}))
+            with pytest.raises((ValueError, w4.W4Error)):
+                w4.w4_attn_prefill(**dict(args, **{name: big}), goff=goff, max_q=1)
+        with pytest.raises((ValueError, w4.W4Error)):
+            w4.w4_attn_prefill(**args, goff=goff, max_q=big)
