@@ -594,7 +594,8 @@ W4_API int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_
  *    are the last tokens of sequence b (a prompt, or a chunk behind a cached
  *    prefix), placed as in w4_rope_append; goff as there.
  *  q     bf16, 16-byte aligned; token and head strides in elements,
- *        multiples of 8, D contiguous.
+ *        multiples of 8 (positive for w4_attn_prefill; the stride of a
+ *        dimension of extent 1 is ignored), D contiguous.
  *  out   bf16 contiguous, 16-byte aligned.
  *  lse   [rows, q_heads] fp32 out or NULL: log sum exp(scale q . k).
  *  max_len, max_q   host upper bounds of kv_len and of a sequence's rows: they

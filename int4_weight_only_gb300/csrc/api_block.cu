@@ -33,15 +33,18 @@ int check_kv(const w4_paged_kv* in, w4_paged_kv* kv) {
     return W4_OK;
 }
 
-// The part of the attention calls' checks that does not depend on the form.
+// The part of the attention calls' checks that does not depend on the form.  As for
+// the cache, strides of extent 1 (of `tokens` and q_heads) are replaced by valid ones.
 int check_attn(const w4_paged_kv* in, const uint16_t* q, long long q_tok, long long q_head,
-               uint16_t* out, float* lse, int q_heads, int max_len, float scale, int window,
+               uint16_t* out, float* lse, int tokens, int q_heads, int max_len, float scale, int window,
                int sinks, AttnArgs* a) {
     w4_paged_kv* kv = &a->kv;
     const int rc = check_kv(in, kv);
     if (rc) return rc;
     if (!q || !out) return W4_ERR_NULL_PTR;
     if (kv->head_dim != 64 && kv->head_dim != 128) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (tokens == 1) q_tok = 8;
+    if (q_heads == 1) q_head = 8;
     if (q_heads < 1 || q_heads % kv->heads || max_len < 0 || window < 0 || sinks < 0 || q_tok < 0 || q_head < 0 ||
         !(scale > 0.f) || !std::isfinite(scale))
         return W4_ERR_INVALID_ARG;
@@ -174,7 +177,8 @@ int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
                    uint16_t* out, float* lse, int q_heads, int max_len, float scale, int window, int sinks,
                    void* workspace, size_t workspace_bytes, void* stream) {
     AttnArgs a{};
-    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
+    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, kv ? kv->batch : 0, q_heads, max_len, scale,
+                        window, sinks, &a);
     if (rc) return rc;
     if (kv->batch == 0) return W4_OK;
     // the list of units is counted in 32 bits
@@ -193,7 +197,8 @@ int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_
                     const int32_t* goff, uint16_t* out, float* lse, int T, int q_heads, int max_q, int max_len,
                     float scale, int window, int sinks, void* stream) {
     AttnArgs a{};
-    const int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, q_heads, max_len, scale, window, sinks, &a);
+    const int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, T, q_heads, max_len, scale, window, sinks,
+                              &a);
     if (rc) return rc;
     if (!goff) return W4_ERR_NULL_PTR;
     if (T < 0 || max_q < 0) return W4_ERR_INVALID_ARG;
@@ -201,9 +206,6 @@ int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_
     if (kv->batch == 0 || T == 0 || max_q == 0) return W4_OK;
     a.err = device_error_flag();
     if (!a.err) return W4_ERR_CUDA;
-    // strides of extent 1 are never used, but the tensor map wants valid ones
-    if (q_heads == 1) a.q_head = 8;
-    if (T == 1) a.q_tok = 8;
     if (a.q_head == 0 || a.q_tok == 0) return W4_ERR_INVALID_ARG;
     a.goff = goff;
     a.T = T;

@@ -163,3 +163,17 @@ def test_norm_refusals(w4):
                      (dict(a=float("inf")), "INVALID_ARG"), (dict(y=ODD), "MISALIGNED"), (dict(xout=ODD), "MISALIGNED")):
         assert call(**kw) == c["W4_ERR_" + code], kw
     assert call(M=0) == c["W4_OK"]
+
+
+def test_query_strides_of_extent_one_are_ignored(w4):
+    """As those of the cache are: one token, or one head, may have any."""
+    lib, c = w4.load(), _codes()
+    refused, fine = c["W4_ERR_MISALIGNED"], c["W4_ERR_WORKSPACE"]
+    one = _kv(heads=1, batch=1)
+    assert _decode(lib, _kv(batch=1), qt=4, ws=None) == fine and _decode(lib, qt=4, ws=None) == refused
+    assert _decode(lib, one, hq=1, qh=3, qt=-1, ws=None) == fine and _decode(lib, one, hq=2, qh=3, ws=None) == refused
+
+    def chunk(T, hq, qt, qh):
+        return lib.w4_attn_prefill(_kv(heads=1), OK16, qt, qh, OK16, OK16, None, T, hq, 0, 64, 0.1, 0, 0, None)
+    assert chunk(1, 1, 3, 0) == c["W4_OK"] and chunk(1, 2, 4, 128) == c["W4_OK"] and chunk(2, 1, 128, 5) == c["W4_OK"]
+    assert chunk(2, 1, 4, 128) == refused and chunk(1, 2, 128, 5) == refused
