@@ -472,3 +472,20 @@ def test_integers_past_32_bits_are_refused(w4):
                 w4.w4_attn_prefill(**dict(args, **{name: big}), goff=goff, max_q=1)
         with pytest.raises((ValueError, w4.W4Error)):
             w4.w4_attn_prefill(**args, goff=goff, max_q=big)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(17, 1, 128), (40, 1, 64), (24, 1, 64), (128, 1, 128), (66, 2, 64)])
+def test_decode_wide_groups_over_long_sequences(w4, Hq, Hkv, D):
+    """Several items of 16 heads read the same keys, each cut over CTAs."""
+    for lens in ([9000], [1, 700, 3001, 250], [400 + 37 * i for i in range(20)]):
+        decode(w4, lens, Hq, Hkv, D, 32, seed=Hq)
+    decode(w4, [5000, 90], Hq, Hkv, D, 32, 1000, 33, seed=Hq)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(28, 4, 128), (16, 8, 64)])
+def test_prefill_uneven_batches(w4, Hq, Hkv, D):
+    """One long prompt, or one chunk behind a long prefix, among sequences of a few tokens."""
+    rows = [0, 1, 15, 700, 1499]
+    prefill(w4, [1500] + [16] * 37, [1500] + [16] * 37, Hq, Hkv, D, 64, rows=rows)
+    prefill(w4, [1] * 20 + [700] + [1] * 20, [300] * 20 + [900] + [7] * 20, Hq, Hkv, D, 64, rows=rows)
+    prefill(w4, [300] + [1] * 7, [12000] + [90] * 7, Hq, Hkv, D, 64, rows=[0, 299])
