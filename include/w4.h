@@ -584,9 +584,17 @@ W4_API int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_
  * position p sees key j when
  *  j <= p  and  (window == 0  or  p - j < window  or  j < sinks):
  * a causal mask, optionally a sliding window of the last `window` keys
- * (itself included) with the first `sinks` keys kept visible.  Keys that no
- * token sees are not read and have no influence, whatever they hold.  A token
- * that sees nothing gets o = 0 and lse = -inf.
+ * (itself included) with the first `sinks` keys kept visible.  Keys that a
+ * token does not see have no influence on it, whatever they hold, and pages
+ * without a key that a token of the call sees need no valid table entry.  A
+ * token that sees nothing, or only scores of -inf, gets o = 0 and lse = -inf.
+ * An infinite or NaN value that a token sees reaches its o as the sum says.
+ *
+ * Range: values are summed before the division by the sum of the weights, and
+ * a weight is at most 2^8 there, so |v| times the visible keys has to stay
+ * below 2^120 (1.3e36).  Exactness: w4_attn_prefill rounds a weight to bf16
+ * for its product (outputs 0.0021 to 0.0023 from 64 bits in the relative
+ * norm), w4_attn_decode keeps 15 bits of it (0.0016, one bf16 rounding).
  *
  *  w4_attn_decode: one token a sequence, p = kv_len[b] - 1 (its key already
  *    written); q, out [batch, q_heads, D].
@@ -606,7 +614,8 @@ W4_API int w4_rope_append(const w4_paged_kv* kv, const uint16_t* q, long long q_
  *  workspace (decode): at least w4_attn_decode_workspace_bytes(...) bytes,
  *        zero-filled once (it starts with W4_WORKSPACE_COUNTER_BYTES of arrival
  *        counters that every call leaves at zero; it can be the linear layers'
- *        workspace).  Calls that share one must not overlap on the GPU.
+ *        workspace).  Calls that share one must not overlap on the GPU, and a
+ *        captured graph keeps its address: it has to outlive the graph.
  * ------------------------------------------------------------------------- */
 W4_API size_t w4_attn_decode_workspace_bytes(int q_heads, int heads, int head_dim);
 W4_API int w4_attn_decode(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,

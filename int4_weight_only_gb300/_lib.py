@@ -786,9 +786,10 @@ def w4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     D], position kv_len - 1) over the paged cache; scale defaults to D**-0.5.
     Key j is visible when j <= p and (window == 0 or p - j < window or
     j < sinks).  max_len bounds kv_len; lse [B, Hq] fp32 receives the
-    log-sum-exp when given.  Without `workspace` the device's shared one is used:
-    calls on several streams that can overlap need one each
-    (w4_attn_decode_workspace_bytes, zero-filled)."""
+    log-sum-exp when given.  Without `workspace` the device's shared one is used
+    (it is never freed, so graphs may be captured with it): calls on several
+    streams that can overlap need one each (w4_attn_decode_workspace_bytes,
+    zero-filled)."""
     kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
     qs = _need_view(q, torch.bfloat16, 3, "q")
     B, Hq, D = q.shape

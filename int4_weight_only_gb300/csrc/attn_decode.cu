@@ -46,7 +46,9 @@
 // Measured (28 / 4 heads of 128): 8 sequences of 128k keys 331-338 us, 0.91-0.93
 // of the measured copy rate; 64 ragged ones (1 to 8192 keys) 41 us, 0.68 (CTAs
 // finish 33 us after the start on average); one of 517 keys 7.1 us of latency
-// (lookup, first keys, join).
+// (lookup, first keys, join).  More than 16 heads to one key-value head are items of
+// their own that read the keys again: 8 sequences of 32768 keys take 32 us for 16
+// heads, 84 for 64 and 157 for 128.
 #include "attn_device.cuh"
 #include "w4_internal.h"
 
@@ -161,6 +163,10 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     Part cur, nxt;
     cur.b = cur.base = 0;
     int part = 0;                           // > 0: units of a part, items cut one by one
+    // Equal parts win for equal lengths (28 / 4 heads, 4 sequences of 1000 keys: 8.0 us
+    // against 8.8 by the list, 12 of 8000 37.8 against 39.0) and cost up to 0.3 us for
+    // ragged ones.  Of 17 to 32 sequences the limit leaves equal ones to the list (24 of
+    // 1000: 16.9 us, cut 14.6), since ragged ones lose there (20 up to 8000: 21.4, cut 22.9).
     if (B <= 16 && B * items <= G) {
         // each lane tries a size of part, from an equal share up; the smallest whose
         // parts are no more than the CTAs wins

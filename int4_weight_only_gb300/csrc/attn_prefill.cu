@@ -24,7 +24,10 @@
 // The running maximum m is lazy: a row keeps the maximum it scaled by until a
 // step exceeds it by more than 2^8, so O is rescaled in the first steps and
 // then hardly ever; P stays below 2^8, which costs bf16 nothing.  The sums use
-// the fp32 weights, before they are rounded to bf16 as matrix operands.
+// the fp32 weights, before they are rounded to bf16 as matrix operands: one word,
+// because a second one for the rounding's rest, as in attn_decode.cu, is another
+// value product where the tensor cores are the scarce part (the output is 0.0022
+// from 64 bits, against 0.0016 of one rounding of the result).
 //
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of tile A, B (one row per thread), O to memory
@@ -44,15 +47,20 @@
 // Every wait is bounded (mbar_wait); copies and MMAs in flight are drained
 // before the CTA ends.
 //
-// Measured (28 / 4 heads of 128): 8192 tokens 355 us, 1353 TFLOP/s (347 with its
-// exponentials left out); 2048 behind 14336 345 us; 2048 tokens 38.6 us.  Bound
-// by shared memory under the MMAs: a step reads 128 KB for its two score
-// products and 64 KB for its value products and takes 64 KB of copies, 2048
-// cycles at 128 bytes, as many as its MMAs take; then by the chain from a score
-// product over its softmax to the next.  Heads of 64 are bound by that chain: a
+// Measured (28 / 4 heads of 128, in a graph): 8192 tokens 352-358 us, 1345-1368
+// TFLOP/s (347 with its exponentials left out); 2048 behind 14336 345 us; 2048
+// tokens 38.2-38.6 us.  A step of two tiles takes 3330 cycles.  Its MMAs need 2048,
+// and shared memory as many (128 KB for the score products' operands, 64 KB for the
+// value products', 64 KB of copies, at 128 bytes a cycle): by the counters both
+// are busy for 61 % of the time, and neither is the limit.  The other 1300 cycles
+// are waits between a tile's score product, its softmax and its value product that
+// the other tile's work does not fill.  Heads of 64 are bound by that chain alone: a
 // step takes 1.46 us with two tiles, 1.20 with one.  P in TMEM columns of its
 // own, which they have room for, so that the next score product starts as soon
 // as S is read, took 1.63: the two tiles then run their softmax at one time.
+// Uneven batches are far slower than their work: items are dealt out by position, as if
+// every sequence were as long as the longest (28 / 4 heads: one prompt of 8192 tokens
+// with 37 of 16 takes 6.2 ms, with 255 single tokens 1.5 ms, alone 0.35).
 #include "attn_device.cuh"
 #include "w4_internal.h"
 

@@ -10,7 +10,10 @@
 // else; everything a row needs is loaded before its first sum, so that a row
 // waits for memory once.  Sums and norms are fp32.  Bound by HBM: 8192 rows of
 // 3840 take 38.0 us without the norm after the block (0.98 of the measured copy
-// rate) and 42.9 us with it (a second row sum), one row 1.7 us of latency.
+// rate) and 42.9 us with it (a second row sum), one row 1.7 us of latency.  Rows of
+// more than 16384 columns take 1024 threads of 64 registers, which do not hold a
+// row's loads (168 bytes spilled): 2048 rows of 16384 take 47.6 / 57.0 us (0.83 /
+// 0.69), 1024 of 32768 57.1 / 68.4 (0.69 / 0.58).
 #include "block_device.cuh"
 #include "w4_internal.h"
 

@@ -72,3 +72,26 @@ def test_prefill(w4, Hq, Hkv, D, where):
     for b, (n, m) in enumerate(zip(qs, lens)):
         t = slice(int(off[b]), int(off[b + 1]))
         same(o[t], BO.attention(to64(q[t]), *kv[b], m - n + np.arange(n), D ** -0.5), f"{where} {n} of {m}")
+
+
+def test_scores_of_minus_infinity(w4):
+    """They weigh nothing; a token that sees no other score gets zeros, as one that sees no key."""
+    n, D = 300, 64
+    cache = Paged([n, n], 1, D, 16)
+    kv = cache.fill_random()
+    for b, hidden in ((0, slice(0, 290)), (1, slice(0, n))):
+        k, v = kv[b]
+        k[hidden, :, 0] = -INF
+        cache.put(b, torch.tensor(k).bfloat16(), torch.tensor(v).bfloat16())
+    q = randn_bf16(80, 4, D, seed=1).abs().cuda()
+    off = torch.tensor([0, 40, 80], dtype=torch.int32, device="cuda")
+    lse = torch.zeros(80, 4, device="cuda")
+    o = w4.w4_attn_prefill(q, cache.k, cache.v, off, cache.kv_len, cache.table, 40, n, lse=lse)
+    lse1 = torch.zeros(2, 4, device="cuda")
+    o1 = w4.w4_attn_decode(q[[39, 79]], cache.k, cache.v, cache.kv_len, cache.table, n, lse=lse1)
+    assert w4.w4_get_device_error() == 0
+    for y, z in ((o[:30], lse[:30]), (o[40:], lse[40:]), (o1[1:], lse1[1:])):
+        assert not y.any() and (z == -INF).all()
+    k, v = kv[0][0][290:], kv[0][1][290:]
+    check(o[30:40], lse[30:40], BO.attention(to64(q[30:40]), k, v, np.arange(10), D ** -0.5), "prompt")
+    check(o1[:1], lse1[:1], BO.attention(to64(q[39:40]), k, v, [9], D ** -0.5), "one token")
