@@ -86,6 +86,10 @@ extern "C" {
                                           [0, pages), or a kv_len that is
                                           negative or past the table or max_len */
 
+#define W4_ERR_NO_PAGES           -14  /* device flag: w4_kv_plan ran out of free
+                                          pages; the requests without one are not
+                                          in the step                          */
+
 /* Size of the library's built-in split-K scratch used by
  * w4a16_linear_noalloc (4 MiB, held by every GPU that loads the library).  */
 #define W4_NOALLOC_SCRATCH_BYTES (4 << 20)
@@ -626,6 +630,146 @@ W4_API int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q
                            long long q_head_stride, const int32_t* goff, uint16_t* out,
                            float* lse, int T, int q_heads, int max_q, int max_len, float scale,
                            int window, int sinks, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * w4_attn_shared - w4_attn_decode without a window, for batches in which groups
+ * of sequences have their first tokens in common: the keys and values that a
+ * group shares are read once for all its sequences.  o and lse are those of
+ * w4_attn_decode on the same cache, up to rounding (the weights of the shared
+ * keys are rounded to bf16, as in w4_attn_prefill).
+ *
+ *  group   [groups + 1] int32 on the device: sequences group[i] .. group[i+1] - 1
+ *          are group i (non-decreasing, within [0, batch]; sequences outside
+ *          every group share nothing).
+ *  shared  [groups] int32 on the device: the first shared[i] tokens are the same
+ *          for all of group i.  They are read through the page table of the
+ *          group's first sequence (also when that one is an unused row); the
+ *          others' entries for whole pages of them are not looked at.  An
+ *          empty group's number is not looked at.  Any number of tokens, page ends or not; 0 for a
+ *          group that shares nothing.
+ *  Every sequence has kv_len[b] >= shared[i], or 0 (an unused row, o = 0).  A
+ *  shorter one, and a shared[i] that is negative or past the table or max_len,
+ *  raise W4_ERR_PAGE_TABLE; offsets outside [0, batch] or decreasing raise
+ *  W4_ERR_GROUP_TOKENS.  The outputs concerned are then unspecified.
+ *  q       strides positive multiples of 8 (of extent 1: ignored); the other
+ *          arguments are w4_attn_decode's, the workspace included.
+ *  scratch at least w4_attn_shared_scratch_bytes(...) bytes, 16-byte aligned,
+ *          need not be initialised: the shared parts' results between the two
+ *          kernels of a call.  Calls that can overlap need one each.
+ *  groups >= 1; head counts and head_dim as in w4_attn_decode.
+ * ------------------------------------------------------------------------- */
+W4_API size_t w4_attn_shared_scratch_bytes(int batch, int q_heads, int heads, int head_dim);
+W4_API int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
+                          long long q_head_stride, const int32_t* group, const int32_t* shared,
+                          int groups, uint16_t* out, float* lse, int q_heads, int max_len,
+                          float scale, void* workspace, size_t workspace_bytes, void* scratch,
+                          size_t scratch_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * w4_kv_plan - one step's page table entries, lengths, offsets and slots from
+ * the requests' lengths, on the device, so that a captured step follows them.
+ * Request b has lens[b] tokens in the cache and gets new_tokens[b] more (NULL:
+ * one each; 0: it is not in this step).  It needs the pages ceil(lens / page_size)
+ * .. ceil((lens + new) / page_size) - 1 of its row of the table; they are taken
+ * from the free list in the order of the requests.  With them
+ *  kv_len[b]   = lens + new, or 0 when the request is not in the step;
+ *  goff[b]     = the sum of the new tokens before request b (goff[batch]: all);
+ *  and for row t = goff[b] + i of the step's tokens, i < new:
+ *  pos[t]      = lens[b] + i;
+ *  slots[t]    = its place in the pool, page * page_size + pos % page_size;
+ *  rows from goff[batch] to T - 1 get pos = slots = -1.
+ *  kv_len, goff and table are what w4_rope_append and the attention calls take.
+ *
+ *  lens, new_tokens  [batch] int32.  free_pages  [n_free] int32, page numbers;
+ *  used        [1] int32: how many of them are given out already.
+ *  table       [batch, max_pages] int32, row stride table_stride: only the
+ *              entries of new pages are written.
+ *  lens_out    [batch] int32 or NULL: the lengths after the step (may be lens).
+ *  used_out    [1] int32 or NULL: used after the step (may be used).
+ *  Not in the step, with kv_len 0, lens_out = lens and pos = slots = -1 in its
+ *  rows, is also a request whose pages the free list no longer holds
+ *  (W4_ERR_NO_PAGES; of the requests that need pages it is the first such and all
+ *  behind it), whose lengths are negative or past the table (W4_ERR_PAGE_TABLE)
+ *  or whose rows do not fit in T (W4_ERR_GROUP_TOKENS); goff stays within T.
+ *  new_tokens < 0 counts as 0 rows.  A page number outside [0, pages) raises
+ *  W4_ERR_PAGE_TABLE and gives slot -1, used outside [0, n_free] is clamped with
+ *  the same flag.
+ *  page_size a power of two, 16 .. 4096; batch <= W4_KV_PLAN_MAX_BATCH;
+ *  T, n_free, max_pages * page_size <= 2^30.  Outputs other than the two
+ *  in-place pairs must not overlap inputs.
+ * ------------------------------------------------------------------------- */
+#define W4_KV_PLAN_MAX_BATCH 8192
+W4_API int w4_kv_plan(const int32_t* lens, const int32_t* new_tokens, const int32_t* free_pages,
+                      int n_free, const int32_t* used, int32_t* table, long long table_stride,
+                      int batch, int max_pages, int page_size, int pages, int T, int32_t* kv_len,
+                      int32_t* goff, int32_t* pos, int64_t* slots, int32_t* lens_out,
+                      int32_t* used_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * w4_moe_route - the experts of every token and the order in which the grouped
+ * linear takes them:
+ *  p = softmax(logits) or sigmoid(logits);  s = p + bias (s = p without one)
+ *  groups > 1: the experts fall into `groups` equal runs; a run is ranked by the
+ *    sum of its group_best (1 or 2) largest s and only the top_groups best runs
+ *    are kept (without a bias and with group_best 1: by its largest logit);
+ *  the k largest s of what is left are the token's experts, in that order;
+ *  weights = p of the chosen experts (the bias only chooses), divided by their
+ *    sum when renorm != 0, times scale.
+ *  Scores are compared as in exact arithmetic, equal ones by the lower index
+ *  (without a bias the logits are compared): where fp32 cannot tell two apart
+ *  the token is chosen again in 64 bits.  The bias does not enter the weights.
+ *
+ *  logits   [T, E] bf16 (logits_bf16 != 0) or fp32, row stride in elements, E
+ *           contiguous.  -inf or NaN: the expert is not offered to the token;
+ *           +inf: softmax gives the infinite ones equal shares.
+ *  bias     [E] fp32 or NULL; an expert whose s is -inf or NaN is not offered.
+ *  count    [1] int32 on the device or NULL: tokens from *count on are padding
+ *           and get no expert.
+ *  weights  [T, k] fp32, ids [T, k] int32 out.  Where fewer than k experts are
+ *           offered the rest is id -1, weight 0.
+ *  row      [T, k] int32 out: the place of (token, j) among all choices sorted by
+ *           expert, then token; -1 for id -1.  goff [E + 1] int32 out: expert e's
+ *           rows are goff[e] .. goff[e+1] - 1 (w4a16_grouped_linear's goff; rows
+ *           from goff[E] to T k - 1 belong to nobody and are left alone there).
+ *  1 <= k <= 32, E <= 1024, groups <= 32 divides E, 1 <= top_groups <= groups,
+ *  k <= top_groups * E / groups, T * k < 2^31, T <= 2^22.
+ *  workspace  at least w4_moe_route_workspace_bytes(T, E) bytes (0 for few
+ *           tokens), 16-byte aligned, need not be initialised; calls that can
+ *           overlap need one each.
+ * ------------------------------------------------------------------------- */
+#define W4_MOE_SOFTMAX 0
+#define W4_MOE_SIGMOID 1
+#define W4_MOE_MAX_EXPERTS 1024
+#define W4_MOE_MAX_TOPK 32
+W4_API size_t w4_moe_route_workspace_bytes(int T, int E);
+W4_API int w4_moe_route(const void* logits, int logits_bf16, long long logits_stride,
+                        const float* bias, const int32_t* count, int T, int E, int k, int score,
+                        int groups, int top_groups, int group_best, int renorm, float scale,
+                        float* weights, int32_t* ids, int32_t* row, int32_t* goff, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * w4_moe_gather - tokens copied to their experts' rows:
+ *  out[row[t, j]] = x[t]  for every row[t, j] in [0, R);  other rows of out are
+ *  left as they were.
+ * w4_moe_combine - the experts' rows weighted and summed back to tokens:
+ *  out[t] = sum_j weights[t, j] * y[row[t, j]] (+ shared[t]), summed in fp32 in
+ *  the order of j, then the shared row, rounded to bf16 once.
+ *
+ *  x [T, K] bf16, row stride in elements; y [R, N], shared [T, N] or NULL, out
+ *  bf16 contiguous; row [T, k] int32, weights [T, k] fp32 (w4_moe_route's).
+ *  row -1 is skipped (a weight there is not read into the sum); any other value
+ *  outside [0, R) is skipped and raises W4_ERR_GROUP_TOKENS.  No two places of
+ *  `row` may name the same row of a gather's out.  out must not overlap x or y;
+ *  it may be `shared`.
+ *  k <= W4_MOE_MAX_TOPK, K, N <= 2^22; buffers need 2-byte alignment (rows that are multiples
+ *  of 16 bytes, 16-byte aligned, run fastest).
+ * ------------------------------------------------------------------------- */
+W4_API int w4_moe_gather(const uint16_t* x, long long x_stride, const int32_t* row, uint16_t* out,
+                         int T, int k, int K, int R, void* stream);
+W4_API int w4_moe_combine(const uint16_t* y, const int32_t* row, const float* weights,
+                          const uint16_t* shared, uint16_t* out, int T, int k, int N, int R,
+                          void* stream);
 
 /* ---------------------------------------------------------------------------
  * w4_get_device_error - synchronizes `stream`, then returns and clears the

@@ -17,7 +17,8 @@ from ._lib import (W4Error, lib_path, load, w4_pack_rtn, w4a16_workspace_bytes,
                    w4a8_quantize_act_smooth, w4_smooth, w4_gptq,
                    w4_get_device_error, w4_set_wait_limit, w4_set_fault_injection,
                    w4_block_norm, w4_rope_freqs, w4_rope_append, w4_attn_decode_workspace_bytes,
-                   w4_attn_decode, w4_attn_prefill,
+                   w4_attn_decode, w4_attn_prefill, w4_attn_shared_scratch_bytes, w4_attn_shared,
+                   w4_kv_plan, w4_moe_route_workspace_bytes, w4_moe_route, w4_moe_gather, w4_moe_combine,
                    w4_error_string, padded_k,
                    EXPORTED)
 
@@ -31,4 +32,6 @@ __all__ = ["W4Error", "lib_path", "load", "w4_pack_rtn", "w4a16_workspace_bytes"
            "w4a8_quantize_act_smooth", "w4_smooth", "w4_gptq",
            "w4_get_device_error", "w4_set_wait_limit", "w4_set_fault_injection", "w4_error_string", "padded_k",
            "w4_block_norm", "w4_rope_freqs", "w4_rope_append", "w4_attn_decode_workspace_bytes",
-           "w4_attn_decode", "w4_attn_prefill", "EXPORTED"]
+           "w4_attn_decode", "w4_attn_prefill", "w4_attn_shared_scratch_bytes", "w4_attn_shared",
+           "w4_kv_plan", "w4_moe_route_workspace_bytes", "w4_moe_route", "w4_moe_gather", "w4_moe_combine",
+           "EXPORTED"]

@@ -54,6 +54,15 @@ _SIGS = {
                                 _c_int, _c_int, _vp, _c_size, _vp]),
     "w4_attn_prefill": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _vp] + [_c_int] * 4
                         + [ctypes.c_float, _c_int, _c_int, _vp]),
+    "w4_attn_shared_scratch_bytes": (_c_size, [_c_int] * 4),
+    "w4_attn_shared": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int,
+                                ctypes.c_float, _vp, _c_size, _vp, _c_size, _vp]),
+    "w4_kv_plan": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_ll] + [_c_int] * 5 + [_vp] * 7),
+    "w4_moe_route_workspace_bytes": (_c_size, [_c_int] * 2),
+    "w4_moe_route": (_c_int, [_vp, _c_int, _c_ll, _vp, _vp] + [_c_int] * 8 + [ctypes.c_float]
+                     + [_vp] * 5 + [_c_size, _vp]),
+    "w4_moe_gather": (_c_int, [_vp, _c_ll, _vp, _vp] + [_c_int] * 4 + [_vp]),
+    "w4_moe_combine": (_c_int, [_vp] * 5 + [_c_int] * 4 + [_vp]),
     "w4_get_device_error": (_c_int, [_vp]),
     "w4_set_wait_limit": (_c_int, [ctypes.c_longlong, _vp]),
     "w4_set_fault_injection": (_c_int, [_c_int, _vp]),
@@ -843,6 +852,223 @@ def w4_attn_prefill(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         D ** -0.5 if scale is None else scale, window, sinks, _stream(q, stream))
     if rc:
         raise W4Error("w4_attn_prefill", rc)
+    return out
+
+
+_scratch_sizes = {}
+
+
+def _scratch(nbytes, device, stream):
+    """Uninitialised bytes for one call: memory of the call's stream, so that it can be
+    taken again as soon as the call is enqueued."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def w4_attn_shared_scratch_bytes(batch: int, q_heads: int, heads: int, head_dim: int) -> int:
+    return int(load().w4_attn_shared_scratch_bytes(batch, q_heads, heads, head_dim))
+
+
+def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_len: torch.Tensor,
+                   table: torch.Tensor, group: torch.Tensor, shared: torch.Tensor, max_len: int,
+                   scale: Optional[float] = None, out=None, lse=None, workspace=None, scratch=None,
+                   stream=None) -> torch.Tensor:
+    """w4_attn_decode (without a window) where groups of sequences share their
+    first tokens: sequences group[i] .. group[i + 1] - 1 (group [G + 1] int32) have
+    their first shared[i] tokens (shared [G] int32) in common, in the pages that
+    the first one's row of the table names; those are read once for the group.
+    kv_len counts them; a sequence has at least shared[i] tokens, or 0.  workspace
+    is w4_attn_decode's; scratch (w4_attn_shared_scratch_bytes, uninitialised) is
+    allocated for the call when not given."""
+    kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
+    qs = _need_view(q, torch.bfloat16, 3, "q")
+    B, Hq, D = q.shape
+    if B != batch or D != pool[3]:
+        raise ValueError(f"q must have shape [{batch}, heads, {pool[3]}], got {tuple(q.shape)}")
+    G = shared.numel()
+    _need(shared, torch.int32, (G,), "shared")
+    _need(group, torch.int32, (G + 1,), "group")
+    if G == 0:
+        raise ValueError("there must be at least one group")
+    out = _attn_outputs(q, out, lse)
+    if B == 0 or Hq == 0:
+        return out
+    if max_len > 0x7FFFFFFF:
+        _past_32_bits(max_len=max_len)
+    lib = _lib or load()
+    key = (B, Hq, pool[1], D, q.get_device())
+    need = _scratch_sizes.get(key)
+    if need is None:
+        need = _scratch_sizes[key] = lib.w4_attn_shared_scratch_bytes(B, Hq, pool[1], D)
+    if scratch is None:
+        scratch = _scratch(max(need, 16), q.device, stream)
+    ws = workspace if workspace is not None else _ws.get(q.get_device())
+
+    def call(ws):
+        return lib.w4_attn_shared(
+            kv, q.data_ptr(), qs[0], qs[1], group.data_ptr(), shared.data_ptr(), G, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), Hq, max_len, D ** -0.5 if scale is None else scale,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+            scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(q, stream))
+    rc = call(ws)
+    if rc == W4_ERR_WORKSPACE and workspace is None:
+        rc = call(_workspace(q.device, lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D), stream))
+    if rc:
+        raise W4Error("w4_attn_shared", rc)
+    return out
+
+
+# ------------------------------------------------------------- a serving step
+def _i32(t, shape, name):
+    if (type(t) is not torch.Tensor or t.dtype is not torch.int32 or not t.is_cuda or t.shape != shape
+            or not t.is_contiguous()):
+        _need(t, torch.int32, shape, name)
+
+
+def w4_kv_plan(lens: torch.Tensor, new_tokens: Optional[torch.Tensor], free_pages: torch.Tensor,
+               used: torch.Tensor, table: torch.Tensor, page_size: int, pages: int, T: int,
+               lens_out=None, used_out=None, stream=None):
+    """(kv_len [B], goff [B + 1], pos [T] int32, slots [T] int64) of a step, and the new
+    pages written into `table` [B, columns]: request b has lens[b] tokens and gets
+    new_tokens[b] more (None: one each; 0: not in the step), in pages taken from
+    free_pages [F] behind the first used[0] of them.  T: rows of the step; those behind
+    its last token get pos = slots = -1.  lens_out [B] and used_out [1] receive lens and
+    used after the step when given (they may be lens and used themselves).  A request
+    that finds no page, or does not fit the table or T, gets kv_len 0 and raises the
+    device flag (see include/w4.h)."""
+    B = lens.numel()
+    _i32(lens, (B,), "lens")
+    if new_tokens is not None:
+        _i32(new_tokens, (B,), "new_tokens")
+    _i32(free_pages, (free_pages.numel(),), "free_pages")
+    _i32(used, (1,), "used")
+    ts = _need_view(table, torch.int32, 2, "table")
+    if table.shape[0] != B:
+        raise ValueError(f"table must have {B} rows, got {table.shape[0]}")
+    if lens_out is not None:
+        _i32(lens_out, (B,), "lens_out")
+    if used_out is not None:
+        _i32(used_out, (1,), "used_out")
+    if T < 0 or (T | pages | page_size) > 0x7FFFFFFF:
+        raise ValueError(f"T={T}, pages={pages}, page_size={page_size}: out of range")
+    kv_len = lens.new_empty(B)
+    goff = lens.new_empty(B + 1)
+    pos = lens.new_empty(T)
+    slots = lens.new_empty(T, dtype=torch.int64)
+    rc = (_lib or load()).w4_kv_plan(
+        lens.data_ptr(), None if new_tokens is None else new_tokens.data_ptr(), free_pages.data_ptr(),
+        free_pages.numel(), used.data_ptr(), table.data_ptr(), ts[0], B, table.shape[1], page_size, pages, T,
+        kv_len.data_ptr(), goff.data_ptr(), pos.data_ptr(), slots.data_ptr(),
+        None if lens_out is None else lens_out.data_ptr(), None if used_out is None else used_out.data_ptr(),
+        _stream(lens, stream))
+    if rc:
+        raise W4Error("w4_kv_plan", rc)
+    return kv_len, goff, pos, slots
+
+
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def w4_moe_route_workspace_bytes(T: int, E: int) -> int:
+    return int(load().w4_moe_route_workspace_bytes(T, E))
+
+
+def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+                 groups: int = 1, top_groups: int = 1, group_best: int = 1, renorm: bool = True,
+                 scale: float = 1.0, count: Optional[torch.Tensor] = None, workspace=None, stream=None):
+    """(weights [T, k] fp32, ids [T, k], row [T, k], goff [E + 1] int32): the k experts of
+    every token of logits [T, E] (bf16 or fp32) by score + bias ("softmax" or "sigmoid"),
+    among the top_groups best of `groups` equal runs of experts (ranked by the sum of
+    their group_best largest), the weights (scores without the bias, over their sum when
+    renorm, times scale), each choice's place in the order of the experts, and the
+    experts' first rows there (w4a16_grouped_linear's goff).  Equal scores go to the
+    lower index; logits of -inf or NaN are never chosen: id -1, weight 0, row -1 where
+    fewer than k are left.  count [1] int32: tokens from count on get no expert.
+    workspace (w4_moe_route_workspace_bytes, uninitialised) is allocated when not given."""
+    T, E = logits.shape
+    if logits.dtype is torch.bfloat16:
+        ls = _need_view(logits, torch.bfloat16, 2, "logits")
+        half = 1
+    else:
+        ls = _need_view(logits, torch.float32, 2, "logits")
+        half = 0
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {tuple(MOE_SCORES)}, got {score!r}")
+    if bias is not None:
+        _need(bias, torch.float32, (E,), "bias")
+    if count is not None:
+        _i32(count, (1,), "count")
+    if not 1 <= k <= 0x7FFFFFFF or (groups | top_groups | group_best) > 0x7FFFFFFF:
+        raise ValueError(f"k={k}, groups={groups}, top_groups={top_groups}, group_best={group_best}: out of range")
+    lib = _lib or load()
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    row = torch.empty_like(ids)
+    goff = ids.new_empty(E + 1)
+    need = 0
+    if workspace is None:
+        if T > 64:
+            need = lib.w4_moe_route_workspace_bytes(T, E)
+            if need:
+                workspace = _scratch(need, logits.device, stream)
+    else:
+        need = workspace.numel() * workspace.element_size()
+    rc = lib.w4_moe_route(
+        logits.data_ptr(), half, ls[0], None if bias is None else bias.data_ptr(),
+        None if count is None else count.data_ptr(), T, E, k, MOE_SCORES[score], groups, top_groups, group_best,
+        1 if renorm else 0, scale, weights.data_ptr(), ids.data_ptr(), row.data_ptr(), goff.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), need, _stream(logits, stream))
+    if rc:
+        raise W4Error("w4_moe_route", rc)
+    return weights, ids, row, goff
+
+
+def w4_moe_gather(x: torch.Tensor, row: torch.Tensor, out=None, stream=None) -> torch.Tensor:
+    """out [T * k, K] bf16 (or any [R, K] given): out[row[t, j]] = x[t] for x [T, K] and
+    w4_moe_route's row [T, k]; rows that nothing names are left as they were (a new out
+    is not initialised).  -1 is skipped."""
+    xs = _need_view(x, torch.bfloat16, 2, "x")
+    T, K = x.shape
+    k = row.shape[1] if row.dim() == 2 else 0
+    _i32(row, (T, k), "row")
+    if out is None:
+        out = x.new_empty((T * k, K))
+    else:
+        _need(out, torch.bfloat16, (out.shape[0], K), "out")
+    if T == 0 or K == 0:
+        return out
+    rc = (_lib or load()).w4_moe_gather(x.data_ptr(), xs[0], row.data_ptr(), out.data_ptr(), T, k, K,
+                                        out.shape[0], _stream(x, stream))
+    if rc:
+        raise W4Error("w4_moe_gather", rc)
+    return out
+
+
+def w4_moe_combine(y: torch.Tensor, row: torch.Tensor, weights: torch.Tensor,
+                   shared: Optional[torch.Tensor] = None, out=None, stream=None) -> torch.Tensor:
+    """out [T, N] bf16 = sum_j weights[t, j] * y[row[t, j]] (+ shared[t]), summed in fp32,
+    for y [R, N] bf16 and w4_moe_route's row and weights [T, k]; -1 is skipped.  out may
+    be `shared`."""
+    R, N = y.shape
+    _need(y, torch.bfloat16, (R, N), "y")
+    T, k = row.shape
+    _i32(row, (T, k), "row")
+    _need(weights, torch.float32, (T, k), "weights")
+    if shared is not None:
+        _need(shared, torch.bfloat16, (T, N), "shared")
+    if out is None:
+        out = y.new_empty((T, N))
+    else:
+        _need(out, torch.bfloat16, (T, N), "out")
+    if T == 0 or N == 0:
+        return out
+    rc = (_lib or load()).w4_moe_combine(y.data_ptr(), row.data_ptr(), weights.data_ptr(),
+                                         None if shared is None else shared.data_ptr(), out.data_ptr(), T, k, N, R,
+                                         _stream(y, stream))
+    if rc:
+        raise W4Error("w4_moe_combine", rc)
     return out
 
 

@@ -692,6 +692,8 @@ const char* w4_error_string(int code) {
             return "a group's token offsets were invalid (outside [0, T] or decreasing)";
         case W4_ERR_PAGE_TABLE:
             return "a page number or a cached length was out of range";
+        case W4_ERR_NO_PAGES:
+            return "the free list ran out of pages";
         default: return "unknown error code";
     }
 }

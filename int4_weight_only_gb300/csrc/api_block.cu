@@ -69,6 +69,25 @@ int attn_workspace(AttnArgs* a, size_t need, void* ws, size_t ws_bytes) {
     return a->err ? W4_OK : W4_ERR_CUDA;
 }
 
+// The scratch of w4_attn_shared, from its first 32-byte boundary on; returns its bytes.
+size_t shared_scratch(AttnShared* s, void* base, int batch, int q_heads, int head_dim, int sms) {
+    char* p = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(base) + 31) & ~(uintptr_t)31);
+    char* const p0 = p;
+    auto take = [&](size_t bytes) {
+        char* at = p;
+        p += (bytes + 31) & ~(size_t)31;
+        return at;
+    };
+    const size_t rows = (size_t)batch * q_heads, slots = (size_t)2 * sms * kSharedRows;
+    s->share = reinterpret_cast<int*>(take(sizeof(int)));
+    s->info = reinterpret_cast<int4*>(take(batch * sizeof(int4)));
+    s->row_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
+    s->slot_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
+    s->row_o = reinterpret_cast<float*>(take(rows * head_dim * sizeof(float)));
+    s->slot_o = reinterpret_cast<float*>(take(slots * head_dim * sizeof(float)));
+    return (size_t)(p - p0) + 32;
+}
+
 }  // namespace
 }  // namespace w4
 
@@ -211,6 +230,42 @@ int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q_token_
     a.T = T;
     a.max_q = std::min(max_q, T);
     return launch_attn_prefill(a, current_sm_count(), static_cast<cudaStream_t>(stream));
+}
+
+size_t w4_attn_shared_scratch_bytes(int batch, int q_heads, int heads, int head_dim) {
+    if (batch < 0 || q_heads < 1 || heads < 1 || q_heads % heads || head_dim < 1) return 0;
+    const int sms = current_sm_count();
+    AttnShared sh;
+    return sms < 1 ? 0 : shared_scratch(&sh, nullptr, batch, q_heads, head_dim, sms);
+}
+
+int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
+                   const int32_t* group, const int32_t* shared, int groups, uint16_t* out, float* lse, int q_heads,
+                   int max_len, float scale, void* workspace, size_t workspace_bytes, void* scratch,
+                   size_t scratch_bytes, void* stream) {
+    AttnArgs a{};
+    int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, kv ? kv->batch : 0, q_heads, max_len, scale, 0,
+                        0, &a);
+    if (rc) return rc;
+    if (!group || !shared) return W4_ERR_NULL_PTR;
+    if (groups < 1) return W4_ERR_INVALID_ARG;
+    if (!aligned(group, 4) || !aligned(shared, 4)) return W4_ERR_MISALIGNED;
+    if (kv->batch == 0) return W4_OK;
+    if (a.q_head == 0 || a.q_tok == 0) return W4_ERR_INVALID_ARG;
+    // the lists of units, steps of 128 keys and of 16, are counted in 32 bits
+    const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)max_len);
+    if ((cap / 64 + 8) * q_heads * kv->batch > (1LL << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
+    if (!scratch) return W4_ERR_WORKSPACE;
+    if (!aligned(scratch, 16)) return W4_ERR_MISALIGNED;
+    const int sms = current_sm_count();
+    rc = attn_workspace(&a, attn_decode_ws_bytes(q_heads, kv->heads, kv->head_dim, sms), workspace, workspace_bytes);
+    if (rc) return rc;
+    if (scratch_bytes < shared_scratch(&a.sh, scratch, kv->batch, q_heads, kv->head_dim, sms)) return W4_ERR_WORKSPACE;
+    a.sh.group = group; a.sh.shared = shared; a.sh.groups = groups;
+    a.T = kv->batch;
+    a.max_q = 1;
+    rc = launch_attn_shared_prefix(a, sms, static_cast<cudaStream_t>(stream));
+    return rc ? rc : launch_attn_shared_own(a, sms, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -94,16 +94,68 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
 // The part of an item that a CTA works on, as one of its warps sees it.
 struct Part {
     KeyBlocks kb;           // the sequence's visible 16-key blocks
-    int b, it, len;         // sequence, item of it, clamped length
+    int b, it, len, lo;     // sequence, item of it, clamped length, first key of its own
     int units;              // of each of its items: kItemUnits without keys, then a block per warp each
     int base;               // first unit of the sequence in the list
     int first_unit, end;    // of the item; end of the part (in the list)
-    int len_after;          // length of the sequence after b (loaded ahead)
+    int len_after, lo_after;    // of the sequence after b (loaded ahead)
     int first, n;           // the CTAs that hold parts of the item: the first, how many
     int c0, nb;             // this warp's first block, number of blocks
     int issued;             // blocks whose copies are on their way
     int page;               // page of the next one
 };
+
+// Adds to a row over a sequence's own keys (four columns, with its maximum and sum) the parts
+// of its shared prefix, in the order of the keys; hin: the head's number in its group of q_heads /
+// heads.  What the list of parts says is kept inside the workspace, whatever it holds.
+template <int D>
+__device__ __forceinline__ void add_shared(const AttnArgs& a, int b, int hk, int hin, int d, float4* o, float* m,
+                                           float* l) {
+    const int4 s = __ldg(a.sh.info + b);
+    if (s.z <= kSharedItemUnits) return;                // no shared keys
+    const int g = a.Hq / a.kv.heads, tpt = kSharedRows / 2 / g, share = max(__ldg(a.sh.share), 1), G = (int)gridDim.x;
+    const int u = s.y + hk * s.z, first = min(max((u + kSharedItemUnits) / share, 0), G - 1);
+    const int n = min(max((u + s.z - 1) / share - first + 1, 1), G - first);
+    const int tile = s.w >= tpt ? 1 : 0, r = min(max(tile * (kSharedRows / 2) + (s.w - tile * tpt) * g + hin, 0), kSharedRows - 1);
+    const float *po, *pml;                              // part 0, and from part to part
+    size_t step = 0;
+    if (n == 1) {
+        const size_t row = (size_t)b * a.Hq + hk * g + hin;
+        po = a.sh.row_o + row * D;
+        pml = a.sh.row_ml + row * 2;
+    } else {
+        po = a.sh.slot_o + ((size_t)2 * first * kSharedRows + r) * D;
+        pml = a.sh.slot_ml + ((size_t)2 * first * kSharedRows + r) * 2;
+        step = kSharedRows;                             // slots 2 c + 1 of the first CTA, then 2 c
+    }
+    auto at = [&](int x) { return x == 0 ? step : 2 * x * step; };
+    const float sc = a.scale;
+    constexpr int U = 8;                                // parts whose loads are in flight together
+    for (int x0 = 0; x0 < n; x0 += U) {
+        float2 ml[U];
+        float4 t[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const size_t p = at(min(x0 + i, n - 1));
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(pml + p * 2));
+            t[i] = __ldcg(reinterpret_cast<const float4*>(po + p * D + d));
+        }
+        float mx = *m;
+#pragma unroll
+        for (int i = 0; i < U; ++i) mx = x0 + i < n ? fmaxf(mx, ml[i].x) : mx;
+        const float f0 = *m == mx ? 1.f : ex2_approx((*m - mx) * sc);
+        o->x *= f0; o->y *= f0; o->z *= f0; o->w *= f0;
+        *l *= f0;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (x0 + i >= n) break;
+            const float f = ml[i].x == mx ? 1.f : ex2_approx((ml[i].x - mx) * sc);
+            *l += f * ml[i].y;
+            o->x += f * t[i].x; o->y += f * t[i].y; o->z += f * t[i].z; o->w += f * t[i].w;
+        }
+        *m = mx;
+    }
+}
 
 // A finished head's output row (four columns) and log-sum-exp.
 template <int D>
@@ -114,7 +166,9 @@ __device__ __forceinline__ void put_out(const AttnArgs& a, size_t row, int d, fl
     if (a.lse && d == 0) a.lse[row] = l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int NT>
+// SHARED: of each sequence the keys behind its shared prefix (none where it has no more), to
+// which the prefix's parts are added.
+template <int D, int NT, bool SHARED>
 __global__ void __launch_bounds__(Shape<D, NT>::threads, 1)
 k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
     using S = Shape<D, NT>;
@@ -141,10 +195,18 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 
     // ---- this CTA's work (every warp finds it by itself)
     const int G = (int)gridDim.x;
-    auto blocks_of = [&](int len) { return key_blocks<16>(len - 1, len - 1, a.window, a.sinks); };
+    auto blocks_of = [&](int len, int lo) {
+        if constexpr (SHARED) {
+            const int b0 = lo / 16;
+            return KeyBlocks{0, b0, len > lo ? (len - 1) / 16 + 1 - b0 : 0};
+        }
+        return key_blocks<16>(len - 1, len - 1, a.window, a.sinks);
+    };
     auto len_of = [&](int b) { return b < B ? kv_length(a.kv, b, a.max_len, a.err) : 0; };
+    // the first key that is the sequence's own
+    auto lo_of = [&](int b) { return SHARED && b < B ? max(__ldg(&a.sh.info[b].x), 0) : 0; };
     // 0 keys: a unit that writes o = 0
-    auto units_of = [&](int len) { return max(1, (blocks_of(len).n + W - 1) / W); };
+    auto units_of = [&](int len, int lo) { return max(1, (blocks_of(len, lo).n + W - 1) / W); };
     auto warp_scan = [&](int v) {           // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -153,9 +215,9 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         }
         return v;
     };
-    const int len0 = len_of(lane), real0 = lane < B ? units_of(len0) : 0;
+    const int len0 = len_of(lane), lo0 = lo_of(lane), real0 = lane < B ? units_of(len0, lo0) : 0;
     int total = lane < B ? items * (real0 + kItemUnits) : 0;
-    for (int b = lane + 32; b < B; b += 32) total += items * (units_of(len_of(b)) + kItemUnits);
+    for (int b = lane + 32; b < B; b += 32) total += items * (units_of(len_of(b), lo_of(b)) + kItemUnits);
     total = __reduce_add_sync(0xffffffffu, total);
     // consecutive shares of the list
     const int share = (total + G - 1) / G;
@@ -184,17 +246,19 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         cur.b = __ffs(past) - 1;
         u0 = (int)blockIdx.x - __shfl_sync(0xffffffffu, v - mine, cur.b);      // part of the sequence
         cur.len = __shfl_sync(0xffffffffu, len0, cur.b);
+        cur.lo = __shfl_sync(0xffffffffu, lo0, cur.b);
     } else {
         if (u0 >= total) return;
         for (int b0 = 0;; b0 += 32) {
-            const int len = b0 ? len_of(b0 + lane) : len0;
-            const int n = b0 + lane < B ? items * (units_of(len) + kItemUnits) : 0, v = warp_scan(n);
+            const int len = b0 ? len_of(b0 + lane) : len0, lo = b0 ? lo_of(b0 + lane) : lo0;
+            const int n = b0 + lane < B ? items * (units_of(len, lo) + kItemUnits) : 0, v = warp_scan(n);
             const uint32_t past = __ballot_sync(0xffffffffu, cur.base + v > u0);
             if (past) {
                 const int f = __ffs(past) - 1;
                 cur.b = b0 + f;
                 cur.base += __shfl_sync(0xffffffffu, v - n, f);
                 cur.len = __shfl_sync(0xffffffffu, len, f);
+                cur.lo = __shfl_sync(0xffffffffu, lo, f);
                 break;
             }
             cur.base += __shfl_sync(0xffffffffu, v, 31);
@@ -235,15 +299,17 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             n.b = s.b + 1;
             n.base = s.end;
             n.len = s.len_after;
-            n.kb = blocks_of(n.len);
-            n.units = units_of(n.len) + kItemUnits;
+            n.lo = s.lo_after;
+            n.kb = blocks_of(n.len, n.lo);
+            n.units = units_of(n.len, n.lo) + kItemUnits;
             n.len_after = len_of(n.b + 1);
+            n.lo_after = lo_of(n.b + 1);
         }
         start(n, s.end);
         return n;
     };
-    cur.kb = blocks_of(cur.len);
-    cur.units = units_of(cur.len) + kItemUnits;
+    cur.kb = blocks_of(cur.len, cur.lo);
+    cur.units = units_of(cur.len, cur.lo) + kItemUnits;
     if (part) {
         // the item's units in n runs equal to one, on CTAs first .. first + n - 1
         const int real = cur.units - kItemUnits;
@@ -257,6 +323,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         take(cur, s0, s0 + each + (x < rest ? 1 : 0));
     } else {
         cur.len_after = len_of(cur.b + 1);
+        cur.lo_after = lo_of(cur.b + 1);
         start(cur, u0);
     }
     uint32_t put = 0, got = 0;              // blocks issued and consumed by this warp
@@ -295,7 +362,8 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const int hk = cur.it / ngrp, h0 = hk * g + (cur.it - hk * ngrp) * HP;
         const int rows = min(HP, (hk + 1) * g - h0);
         const int p = cur.len - 1;
-        auto seen = [&](int j) { return key_visible(j, p, a.window, a.sinks); };
+        const int lo = cur.lo;
+        auto seen = [&](int j) { return SHARED ? j <= p && j >= lo : key_visible(j, p, a.window, a.sinks); };
 
         // ---- query pieces: head 8 x + lane / 4
         uint4 qf[NT][D / 32];
@@ -322,7 +390,8 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             if (!ok) break;
             const uint8_t* st = ring + (got % NS) * S::stage_bytes;
             const int j0 = cur.kb(cur.c0 + i * W) * 16;
-            const bool all = j0 + 15 <= p && (a.window == 0 || p - j0 < a.window || j0 + 16 <= a.sinks);
+            const bool all = j0 + 15 <= p &&
+                             (SHARED ? j0 >= lo : a.window == 0 || p - j0 < a.window || j0 + 16 <= a.sinks);
             float s[NT][2][4];
 #pragma unroll
             for (int x = 0; x < NT; ++x)
@@ -492,6 +561,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 v.x += f * t.x; v.y += f * t.y; v.z += f * t.z; v.w += f * t.w;
             }
             if (n == 1) {
+                if (SHARED && cur.len > 0) add_shared<D>(a, cur.b, hk, h0 - hk * g + r, d, &v, &mr, &lr);
                 put_out<D>(a, row0 + r, d, v, mr, lr);
             } else {
                 *reinterpret_cast<float4*>(mine + r * D + d) = v;
@@ -571,7 +641,9 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                         const float4 t = *reinterpret_cast<const float4*>(so + (x * HP + r) * D + d);
                         v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
                     }
-                    put_out<D>(a, row0 + r, d, v, s_m[0][r], s_l[0][r]);
+                    float mr = s_m[0][r], lr = s_l[0][r];
+                    if (SHARED) add_shared<D>(a, cur.b, hk, h0 - hk * g + r, d, &v, &mr, &lr);
+                    put_out<D>(a, row0 + r, d, v, mr, lr);
                 }
             }
         }
@@ -584,7 +656,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         for (; got != put; ++got) mbar_wait_drain(&full[warp][got % NS], (got / NS) & 1, a.err);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SHARED>
 int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     using S = Shape<D, NT>;
     CUtensorMap tmK, tmV;
@@ -599,7 +671,7 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
         return W4_ERR_CUDA;
     const int grid = sm_count, bytes = (int)S::smem;
     static SmemLimit limit;
-    if (!limit.raise(k_attn_decode<D, NT>, bytes)) return W4_ERR_CUDA;
+    if (!limit.raise(k_attn_decode<D, NT, SHARED>, bytes)) return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(S::threads);
@@ -610,7 +682,7 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_decode<D, NT>, tmK, tmV, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k_attn_decode<D, NT, SHARED>, tmK, tmV, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 // Two tiles of 8 heads share the keys and values that one would read twice.
@@ -622,10 +694,22 @@ size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count) {
     return (size_t)sm_count * 2 * 8 * head_tiles(Hq, Hkv) * (D + 2) * sizeof(float);
 }
 
-int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+namespace {
+template <bool SHARED>
+int launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     const int nt = head_tiles(a.Hq, a.kv.heads);
-    if (a.kv.head_dim == 128) return nt == 1 ? go<128, 1>(a, sm_count, stream) : go<128, 2>(a, sm_count, stream);
-    return nt == 1 ? go<64, 1>(a, sm_count, stream) : go<64, 2>(a, sm_count, stream);
+    if (a.kv.head_dim == 128)
+        return nt == 1 ? go<128, 1, SHARED>(a, sm_count, stream) : go<128, 2, SHARED>(a, sm_count, stream);
+    return nt == 1 ? go<64, 1, SHARED>(a, sm_count, stream) : go<64, 2, SHARED>(a, sm_count, stream);
+}
+}  // namespace
+
+int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+    return launch<false>(a, sm_count, stream);
+}
+
+int launch_attn_shared_own(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+    return launch<true>(a, sm_count, stream);
 }
 
 }  // namespace w4

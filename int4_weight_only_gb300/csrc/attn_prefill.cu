@@ -66,6 +66,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 namespace w4 {
 namespace {
@@ -307,6 +308,157 @@ struct Walk {
     }
 };
 
+// Groups of sequences that share their first tokens (w4_attn_shared), one new token a
+// sequence: the same tiles, "tokens" being the sequences of a group, and every row sees the
+// same keys, the shared ones.  An item is a pair of tiles and a key-value head; the items of
+// all groups form one list of units, a step each and kSharedUnits for what starting and
+// finishing an item costs, cut into equal consecutive shares, one per CTA.
+constexpr int kSharedUnits = kSharedItemUnits;
+
+// What the list needs to know of a group.
+struct SharedGroup {
+    int t0, nq, len;            // first sequence, sequences, shared keys
+    int steps, w, items;        // steps and units of an item, items
+
+    __device__ __forceinline__ int units() const { return w * items; }
+};
+__device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int tpt, int i) {
+    SharedGroup s{0, 0, 0, 0, 0, 0};
+    if (i >= a.sh.groups) return s;
+    const int o0 = __ldg(a.sh.group + i), o1 = __ldg(a.sh.group + i + 1), n = __ldg(a.sh.shared + i);
+    if (o0 < 0 || o1 < o0 || o1 > a.kv.batch) {
+        atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
+        return s;
+    }
+    if (o0 == o1) return s;
+    const long long cap = min((long long)a.kv.max_pages * a.kv.page_size, (long long)a.max_len);
+    s.len = (int)min(max((long long)n, 0LL), cap);
+    if (s.len != n) atomicCAS(a.err, 0, W4_ERR_PAGE_TABLE);
+    s.t0 = o0;
+    s.nq = o1 - o0;
+    s.steps = (s.len + kN - 1) / kN;
+    if (s.steps > 0) {
+        s.w = s.steps + kSharedUnits;
+        s.items = (s.nq + 2 * tpt - 1) / (2 * tpt) * a.kv.heads;
+    }
+    return s;
+}
+__device__ __forceinline__ int warp_scan_sum(int v) {       // inclusive
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    return v;
+}
+// Units of all groups, by a whole warp.
+__device__ __forceinline__ int shared_total(const AttnArgs& a, int tpt) {
+    int v = 0;
+    for (int i = threadIdx.x & 31; i < a.sh.groups; i += 32) v += shared_group(a, tpt, i).units();
+    return __reduce_add_sync(0xffffffffu, v);
+}
+__device__ __forceinline__ int shared_share(int total) { return max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1); }
+
+// A CTA's walk through its share, with the names that the kernel knows from Walk.
+struct SharedWalk {
+    int b, hk;                  // the group's first sequence, key-value head
+    int x, n, c0, c1;           // the part: number x of n, steps c0 .. c1 - 1
+    int t0, len, i0, n_tok, ntile, p0, p1;
+    KeyBlocks kb;
+    int grp, idx, U, u1, share; // group, item of it, the item's first unit, end of the share
+    SharedGroup g;
+
+    __device__ __forceinline__ bool begin(const AttnArgs& a, int tpt) {
+        const int lane = threadIdx.x & 31, total = shared_total(a, tpt);
+        share = shared_share(total);
+        const int u0 = share * (int)blockIdx.x;
+        u1 = min(u0 + share, total);
+        if (u0 >= u1) return false;
+        int base = 0;
+        for (int i0 = 0;; i0 += 32) {
+            const int units = shared_group(a, tpt, i0 + lane).units(), v = warp_scan_sum(units);
+            const uint32_t past = __ballot_sync(0xffffffffu, base + v > u0);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                grp = i0 + f;
+                base += __shfl_sync(0xffffffffu, v - units, f);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, v, 31);
+        }
+        g = shared_group(a, tpt, grp);
+        idx = (u0 - base) / g.w;
+        U = base + idx * g.w;
+        item(a, tpt);
+        return c0 < c1 || next<false>(a, tpt);
+    }
+    __device__ __forceinline__ void item(const AttnArgs& a, int tpt) {
+        const int y = idx / a.kv.heads, u0 = share * (int)blockIdx.x;
+        hk = idx - y * a.kv.heads;
+        b = t0 = g.t0;
+        len = g.len;
+        i0 = y * 2 * tpt;
+        n_tok = min(g.nq - i0, 2 * tpt);
+        ntile = n_tok > tpt ? 2 : 1;
+        p0 = p1 = g.len - 1;
+        kb = KeyBlocks{0, 0, g.steps};
+        c0 = min(max(u0 - U - kSharedUnits, 0), g.steps);
+        c1 = min(max(u1 - U - kSharedUnits, 0), g.steps);
+        const int first = (U + kSharedUnits) / share;
+        n = (U + g.w - 1) / share - first + 1;
+        x = (int)blockIdx.x - first;
+    }
+    template <bool>
+    __device__ __forceinline__ bool next(const AttnArgs& a, int tpt) {
+        for (;;) {
+            U += g.w;
+            if (U >= u1) return false;
+            if (++idx == g.items) {
+                do {                                    // units are left, so a group with items follows
+                    if (++grp >= a.sh.groups) return false;
+                    g = shared_group(a, tpt, grp);
+                } while (g.items == 0);
+                idx = 0;
+            }
+            item(a, tpt);
+            if (c0 < c1) return true;
+        }
+    }
+    __device__ __forceinline__ int tile_steps(int, int) const { return kb.n; }
+};
+
+// For the kernel that joins the parts: the list's shares, and each sequence's shared length,
+// first unit (of key-value head 0), units of an item and place in its pair of tiles.  Groups are
+// dealt out over the CTAs; a whole warp.  Sequences outside every group share nothing.
+__device__ __noinline__ void publish_shared(const AttnArgs& a, int tpt) {
+    const int lane = threadIdx.x & 31, G = (int)gridDim.x;
+    if (blockIdx.x == 0) {
+        const int total = shared_total(a, tpt);
+        if (lane == 0) *a.sh.share = shared_share(total);
+        const int lo = min(max(__ldg(a.sh.group), 0), a.kv.batch), hi = min(max(__ldg(a.sh.group + a.sh.groups), 0), a.kv.batch);
+        for (int b = lane; b < lo; b += 32) a.sh.info[b] = make_int4(0, 0, 0, 0);
+        for (int b = hi + lane; b < a.kv.batch; b += 32) a.sh.info[b] = make_int4(0, 0, 0, 0);
+    }
+    int base = 0;
+    for (int i0 = 0; i0 < a.sh.groups; i0 += 32) {
+        const SharedGroup g = shared_group(a, tpt, i0 + lane);
+        const int v = warp_scan_sum(g.units()), at = base + v - g.units();
+        for (uint32_t m = __ballot_sync(0xffffffffu, g.nq > 0 && (i0 + lane) % G == (int)blockIdx.x); m; m &= m - 1) {
+            const int f = __ffs(m) - 1, t0 = __shfl_sync(0xffffffffu, g.t0, f), nq = __shfl_sync(0xffffffffu, g.nq, f);
+            const int w = __shfl_sync(0xffffffffu, g.w, f), len = __shfl_sync(0xffffffffu, g.len, f);
+            const int u = __shfl_sync(0xffffffffu, at, f);
+            for (int t = lane; t < nq; t += 32) {
+                const int y = t / (2 * tpt), n = __ldg(a.kv.kv_len + t0 + t);
+                // a sequence is unused or has its group's keys
+                if (n != 0 && n < len) atomicCAS(a.err, 0, W4_ERR_PAGE_TABLE);
+                a.sh.info[t0 + t] = make_int4(len, u + y * a.kv.heads * w, w, t - y * 2 * tpt);
+            }
+        }
+        base += __shfl_sync(0xffffffffu, v, 31);
+    }
+}
+
 // Every row of the tokens at p0 .. p1 sees all of block j0.
 __device__ __forceinline__ bool all_see(const AttnArgs& a, int j0, int p0, int p1) {
     return j0 + kN - 1 <= p0 && (a.window == 0 || p1 - j0 < a.window || j0 + kN <= a.sinks);
@@ -381,11 +533,16 @@ __device__ __noinline__ void take_out(uint8_t* v, int t, int lo, int hi) {
             }
 }
 
-// SPLIT: the CTAs of a cluster share the steps of one item.
-template <int D, bool SPLIT>
+// Whole items; the CTAs of a cluster share the steps of one item; parts of the items of
+// groups with a shared prefix, to be joined by another kernel.
+enum Mode { kWhole, kSplit, kShared };
+
+template <int D, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const int tpt) {
+    constexpr bool SPLIT = MODE == kSplit;
+    using WalkT = std::conditional_t<MODE == kShared, SharedWalk, Walk>;
     constexpr int NS = slots<D>(), SB = slot_bytes<D>();
     constexpr uint32_t IDESC_S = idesc_bf16_f32(kTile, kN);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(kTile, D) | (1u << 16);      // B is MN major
@@ -422,9 +579,11 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
     // ---- this CTA's work (every thread finds it by itself)
     const int Hkv = a.kv.heads, nc = SPLIT ? (int)cluster_nctas() : 1;
-    Walk w0;
+    WalkT w0;
     bool mine;
-    if constexpr (SPLIT) {
+    if constexpr (MODE == kShared) {
+        mine = w0.begin(a, tpt);
+    } else if constexpr (SPLIT) {
         mine = w0.pick(a, tpt, (int)blockIdx.x / nc);
         w0.x = (int)cluster_ctarank();
         w0.n = nc;
@@ -459,8 +618,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int R = min(a.kv.page_size, kN), npg = kN / R, g = a.Hq / Hkv;
             uint32_t it = 0, part = 0;
             bool ok = true;
-            Walk w = w0;
-            for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+            WalkT w = w0;
+            for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                 if (w.kb.n == 0 || w.c0 == w.c1) continue;
                 const int c0 = w.c0, c1 = w.c1;
                 // Q of the part before is no longer read
@@ -528,8 +687,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 uint32_t step = 0, part = 0;              // steps and parts of this CTA so far
                 uint32_t np[2] = {0, 0}, no[2] = {0, 0};  // steps, parts by tile
                 bool ok = true;
-                Walk w = w0;
-                for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+                WalkT w = w0;
+                for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                     if (w.kb.n == 0 || w.c0 == w.c1) continue;
                     const int c0 = w.c0, c1 = w.c1;
                     int end[2];
@@ -601,8 +760,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             // -------------------------------------------------------- V release
             uint32_t step = 0, part = 0;
             bool ok = true;
-            Walk w = w0;
-            for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+            WalkT w = w0;
+            for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                 if (w.kb.n == 0 || w.c0 == w.c1) continue;
                 const int c0 = w.c0, c1 = w.c1;
                 bool bad = false;
@@ -649,6 +808,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 }
                 ++part;
             }
+            if constexpr (MODE == kShared) {
+                if (warp == 11) publish_shared(a, tpt);
+            }
         }
         if (joins) { cluster_sync(); cluster_sync(); }
     } else {
@@ -660,8 +822,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const float sc = a.scale;
         uint32_t ns = 0, no = 0, part = 0;                // steps and parts of this tile, parts of the CTA
         bool ok = true;
-        Walk w = w0;
-        for (bool go = mine; go && ok; go = w.next<SPLIT>(a, tpt)) {
+        WalkT w = w0;
+        for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
             const int c0 = w.c0, c1 = w.c1;
             const int bad_at = (int)part;
             if (w.kb.n > 0 && c0 < c1) ++part;
@@ -669,7 +831,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int tok_in = tile * tpt + rt;
             const bool have = rt < tpt && tok_in < w.n_tok;
             const int tok = w.t0 + w.i0 + tok_in, head = w.hk * g + (r - rt * g);
-            const int p = have ? w.p0 + tok_in : -1;
+            const int p = !have ? -1 : MODE == kShared ? w.p1 : w.p0 + tok_in;
             const size_t row = (size_t)tok * a.Hq + head;
             const int n_steps = tile < w.ntile ? w.tile_steps(tile, tpt) : 0, end = min(n_steps, c1);
             if (!joins && end <= c0) {
@@ -771,6 +933,18 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 const bool bad = __any_sync(
                     0xffffffffu, max(((volatile int*)ctl->bad)[0], ((volatile int*)ctl->bad)[1]) > bad_at);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                // a part of a shared prefix: the row as it is, for the join
+                float *part_o = nullptr, *part_ml = nullptr;
+                if constexpr (MODE == kShared) {
+                    if (w.n == 1) {
+                        part_o = a.sh.row_o + row * D;
+                        part_ml = a.sh.row_ml + row * 2;
+                    } else {
+                        const size_t slot = 2 * blockIdx.x + (w.x ? 0 : 1);
+                        part_o = a.sh.slot_o + (slot * 2 * kTile + tile * kTile + r) * D;
+                        part_ml = a.sh.slot_ml + (slot * 2 * kTile + tile * kTile + r) * 2;
+                    }
+                }
                 // rows lie apart, so a store is one sector a lane: whole sectors where `out` allows
                 const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll
@@ -778,7 +952,10 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(o_addr + 32 * i, o);
                     if (!have) continue;
-                    if (SPLIT) {
+                    if constexpr (MODE == kShared) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) st_global_v8(part_o + 32 * i + e, o + e);
+                    } else if (SPLIT) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             st_cluster_v4(dst_o + (32 * i + e) * 4, o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -802,16 +979,18 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->oempty[tile]);      // O may be overwritten
-                if (bad)
+                if (MODE != kShared && bad)
                     add_non_finite<D>(a, w.b, w.hk, w.p0, w.p1, w.kb, c0, end, p, a.out + row * D, dst_o);
-                if (SPLIT) {
+                if constexpr (MODE == kShared) {
+                    if (have) *reinterpret_cast<float2*>(part_ml) = make_float2(m, l);
+                } else if (SPLIT) {
                     st_shared_cluster(dst_ml, m);
                     st_shared_cluster(dst_ml + 4, l);
                 } else if (have && a.lse) {
                     a.lse[row] = l == 0.f ? kNegInf : (m * sc + log2f(l)) * 0.6931471805599453f;
                 }
             }
-            if (joins) {
+            if constexpr (SPLIT) if (joins) {
                 cluster_sync();             // every part's rows have arrived
                 // eight threads a row of this CTA's share
                 constexpr int C = D / 8;
@@ -850,11 +1029,11 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
+// The tensor maps of a launch: Q by tiles of whole tokens, K and V by pages.
 template <int D>
-int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-    const int g = a.Hq / a.kv.heads, tpt = kTile / g;
+bool encode_maps(const AttnArgs& a, int tpt, CUtensorMap* tmQ, CUtensorMap* tmK, CUtensorMap* tmV) {
+    const int g = a.Hq / a.kv.heads;
     const uint32_t R = (uint32_t)std::min(a.kv.page_size, kN);
-    CUtensorMap tmQ, tmK, tmV;
     const uint64_t qd[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.T};
     const uint64_t qst[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_tok * 2};
     const uint32_t qb[3] = {64, (uint32_t)g, (uint32_t)tpt};
@@ -869,9 +1048,15 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
         return encode_tmap_nd(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box,
                               CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    if (!encode(&tmQ, a.q, 3, qd, qst, qb) || !encode(&tmK, a.kv.k, 4, kd, ks, kbx) ||
-        !encode(&tmV, a.kv.v, 4, kd, vs, kbx))
-        return W4_ERR_CUDA;
+    return encode(tmQ, a.q, 3, qd, qst, qb) && encode(tmK, a.kv.k, 4, kd, ks, kbx) &&
+           encode(tmV, a.kv.v, 4, kd, vs, kbx);
+}
+
+template <int D>
+int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+    const int tpt = kTile / (a.Hq / a.kv.heads);
+    CUtensorMap tmQ, tmK, tmV;
+    if (!encode_maps<D>(a, tpt, &tmQ, &tmK, &tmV)) return W4_ERR_CUDA;
     const long long items = ((long long)a.max_q + 2 * tpt - 1) / (2 * tpt) * a.kv.heads * a.kv.batch;
     if (items > (1LL << 26)) return W4_ERR_UNSUPPORTED_SHAPE;
     // CTAs of a cluster that share an item: the fewest with the shortest last turn,
@@ -892,7 +1077,7 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
         if (cost < best) { best = cost; nc = c; }
     }
     constexpr size_t bytes = smem_total<D>();
-    auto kern = nc > 1 ? k_attn_prefill<D, true> : k_attn_prefill<D, false>;
+    auto kern = nc > 1 ? k_attn_prefill<D, kSplit> : k_attn_prefill<D, kWhole>;
     static SmemLimit limit[2];
     if (!limit[nc > 1].raise(kern, (int)bytes)) return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -911,7 +1096,35 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, a, tpt) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
+template <int D>
+int go_shared(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+    const int tpt = kTile / (a.Hq / a.kv.heads);
+    CUtensorMap tmQ, tmK, tmV;
+    if (!encode_maps<D>(a, tpt, &tmQ, &tmK, &tmV)) return W4_ERR_CUDA;
+    constexpr size_t bytes = smem_total<D>();
+    auto kern = k_attn_prefill<D, kShared>;
+    static SmemLimit limit;
+    if (!limit.raise(kern, (int)bytes)) return W4_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sm_count);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, a, tpt) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
 }  // namespace
+
+static_assert(kSharedRows == 2 * kTile, "as the join reads them");
+
+int launch_attn_shared_prefix(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+    return a.kv.head_dim == 128 ? go_shared<128>(a, sm_count, stream) : go_shared<64>(a, sm_count, stream);
+}
 
 int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     return a.kv.head_dim == 128 ? go<128>(a, sm_count, stream) : go<64>(a, sm_count, stream);

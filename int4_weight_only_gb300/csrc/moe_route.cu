@@ -1,0 +1,529 @@
+// moe_route.cu - the experts of every token, and the order in which the grouped
+// linears take them.
+//
+//   p = softmax(z) or sigmoid(z),  s = p + bias,  the k largest s among the kept groups
+//   w = p of the chosen, over their sum;  row = place in the order (expert, token)
+//
+// A warp takes a token: logit e of it sits in lane e % 32, register e / 32.  Scores become
+// integer keys of the same order, so that a round of the selection is one maximum over the
+// lane's registers and two warp reductions (the largest key, the lowest index that has it).
+//
+// Scores closer than their fp32 errors could come out in the wrong order, and another expert
+// would be chosen than the definition says.  Without a bias nothing is at stake: the logits
+// have the order of the scores.  With one, or with groups ranked by two scores, the warp looks
+// at every comparison that decided something; where one was closer than kClose allows (and
+// the two experts do not have the same logit and bias, which is a true tie), it chooses again
+// in 64 bits.  With 256 experts that is one token in some thousand.
+//
+// The order is a counting sort without atomics on results: in a run of 32 tokens, bit t of an
+// expert's word says that token t chose it, so a choice's rank among the run's is a population
+// count.  Up to kRouteOne tokens one CTA does all; above, each CTA leaves its counts by
+// expert, and a second kernel's CTAs add those of all the CTAs (and of those before them).
+#include "block_device.cuh"
+#include "w4_internal.h"
+
+#include <algorithm>
+
+namespace w4 {
+namespace {
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr uint32_t kAll = 0xffffffffu;
+
+// Scores differ by the errors of the exponential (its argument's rounding, 2^-24 |x - m|
+// e^-|x - m| < 2^-25 of the largest p, and 2^-22 of p), of the sum (at most E / 32 + 5
+// roundings, 2^-18.8 of p) and of the quotient; two of them by less than 2^-18 of the largest
+// p.  The rounding of p + bias adds 2^-24 of it each.
+constexpr float kClose = 0x1p-18f, kCloseSum = 0x1p-22f;
+
+// Order-preserving key of a float that is not NaN; 0 is below every key of a value over -inf.
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+__device__ __forceinline__ float warp_max(float v) {
+    return value_of(__reduce_max_sync(kAll, key_of(v)));
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// Logit e of token t: NaN as -inf, -0 as +0 (equal values have equal bits).
+__device__ __forceinline__ float logit_of(const RouteArgs& a, int t, int e) {
+    const long long at = t * a.stride + e;
+    const float v = a.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at])
+                           : static_cast<const float*>(a.logits)[at];
+    return v != v ? -kInf : v + 0.f;
+}
+
+// p of logit x, given the row's largest logit and sum of exponentials over it.
+__device__ __forceinline__ float soft_num(float x, float m) { return m == kInf ? (x == kInf ? 1.f : 0.f) : expf(x - m); }
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+__device__ __forceinline__ double soft_num(double x, double m) { return isinf(m) && m > 0 ? (x == m ? 1. : 0.) : exp(x - m); }
+__device__ __forceinline__ double sigmoid(double x) { return 1. / (1. + exp(-x)); }
+
+// The two largest of what two lanes have, largest first.
+template <typename F> __device__ __forceinline__ void top_two(F& a, F& b, F c, F d) {
+    const F hi = a > c ? a : c, lo = a > c ? c : a;
+    const F other = b > d ? b : d;
+    a = hi;
+    b = lo > other ? lo : other;
+}
+template <typename F> __device__ __forceinline__ F group_rank(F a, F b, int best) {
+    return best == 2 && b > -kInf ? a + b : a;
+}
+
+// The same choice in 64 bits: lane j's expert, or -1.
+template <int V>
+__device__ __noinline__ int choose_wide(const RouteArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
+    double x[V], m = -kInf, sum = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = i * 32 + lane < a.E ? (double)logit_of(a, t, i * 32 + lane) : -kInf;
+        m = x[i] > m ? x[i] : m;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const double v = __shfl_xor_sync(kAll, m, o);
+        m = v > m ? v : m;
+    }
+    if (!a.sigmoid) {
+        for (int i = 0; i < V; ++i) sum += x[i] > -kInf ? soft_num(x[i], m) : 0.;
+        sum = warp_sum(sum);
+    }
+    // what groups are ranked by; without a bias experts are chosen by their logits
+    double s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane;
+        double p = -kInf;
+        if (x[i] > -kInf) {
+            p = a.sigmoid ? sigmoid(x[i]) : soft_num(x[i], m) / sum;
+            if (a.bias) p += (double)__ldg(a.bias + e);
+            if (!(p > -kInf)) p = -kInf;
+        }
+        s[i] = p;
+    }
+    if (a.groups > 1) {
+        double mine = -kInf;
+        for (int g = 0; g < a.groups; ++g) {
+            double b1 = -kInf, b2 = -kInf;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if ((i * 32 + lane) / a.gsize == g) top_two<double>(b1, b2, s[i], -kInf);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const double c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+                top_two(b1, b2, c1, c2);
+            }
+            if (lane == g) mine = group_rank(b1, b2, a.best);
+        }
+        int above = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const double v = __shfl_sync(kAll, mine, g);
+            above += v > mine || (v == mine && g < lane);
+        }
+        const uint32_t keep = __ballot_sync(kAll, lane < a.groups && above < a.top_groups);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 32 + lane < a.E && !(keep >> ((i * 32 + lane) / a.gsize) & 1)) s[i] = -kInf;
+    }
+    if (!a.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = s[i] > -kInf ? x[i] : -kInf;
+    }
+    int id = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double best = -kInf;
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (s[i] > best) { best = s[i]; at = i * 32 + lane; }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const double v = __shfl_xor_sync(kAll, best, o);
+            const int w = __shfl_xor_sync(kAll, at, o);
+            if (v > best || (v == best && w < at)) { best = v; at = w; }
+        }
+        if (at == 0x7fffffff) break;
+        if (lane == j) id = at;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (at == i * 32 + lane) s[i] = -kInf;
+    }
+    return id;
+}
+
+// The experts of token t: lane j gets the j-th (or -1) and its weight.  buf: E floats of the
+// warp's own (groups).
+template <int V>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, float* buf, int* id_out, float* w_out) {
+    const int lane = threadIdx.x & 31;
+    float x[V], m = -kInf, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = i * 32 + lane < a.E ? logit_of(a, t, i * 32 + lane) : -kInf;
+        m = fmaxf(m, x[i]);
+    }
+    const bool two = a.groups > 1 && a.best == 2;
+    const bool scored = a.bias || two;              // the choice goes by scores
+    m = warp_max(m);
+    if (!a.sigmoid && (scored || !a.renorm)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += x[i] > -kInf ? soft_num(x[i], m) : 0.f;
+        sum = warp_sum(sum);
+    }
+    auto prob = [&](float v) { return a.sigmoid ? sigmoid(v) : soft_num(v, m) / sum; };
+    uint32_t key[V];
+    bool close = false;
+    if (scored) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float s = -kInf;
+            if (x[i] > -kInf) {
+                s = prob(x[i]);
+                if (a.bias) s += __ldg(a.bias + i * 32 + lane);
+            }
+            key[i] = s > -kInf ? key_of(s) : 0u;
+        }
+        if (a.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i * 32 + lane < a.E) buf[i * 32 + lane] = key[i] ? value_of(key[i]) : -kInf;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = x[i] > -kInf ? key_of(x[i]) : 0u;
+        if (a.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i * 32 + lane < a.E) buf[i * 32 + lane] = x[i];
+        }
+    }
+    __syncwarp();
+    const float err = scored && m > -kInf ? kClose * prob(m) : 0.f;
+    if (a.groups > 1) {
+        // L lanes a group, each with every L-th of its scores; groups start at different ones,
+        // so that the lanes' words lie in different banks
+        int L = 32;
+        while (L > 1 && L * a.groups > 32) L >>= 1;
+        const int g = lane / L, sub = lane % L, steps = (a.gsize + L - 1) / L;
+        float b1 = -kInf, b2 = -kInf;
+        if (g < a.groups) {
+            int at = g % steps;
+            for (int i = 0; i < steps; ++i) {
+                if (at * L + sub < a.gsize) top_two<float>(b1, b2, buf[g * a.gsize + at * L + sub], -kInf);
+                if (++at == steps) at = 0;
+            }
+        }
+        for (int o = L / 2; o; o >>= 1) {
+            const float c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
+            top_two(b1, b2, c1, c2);
+        }
+        const float mine = group_rank(b1, b2, a.best);
+        int above = 0;
+        for (int i = 0; i < a.groups; ++i) {
+            const float v = __shfl_sync(kAll, mine, i * L);
+            above += v > mine || (v == mine && i < g);
+        }
+        const bool in = g < a.groups && above < a.top_groups;
+        if (scored) {
+            const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
+            close |= hi > -kInf && lo - hi <= 2.f * err + 2.f * kCloseSum * (fabsf(lo) + fabsf(hi));
+        }
+        const uint32_t keep = __ballot_sync(kAll, in && sub == 0);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * 32 + lane < a.E && !(keep >> ((i * 32 + lane) / a.gsize * L) & 1)) key[i] = 0;
+        __syncwarp();                               // buf is read
+    }
+    if (scored && !a.bias) {                        // inside the groups the logits have the scores' order
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i]) key[i] = key_of(x[i]);
+    }
+    int id = -1;
+    uint32_t mine = 0;
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) best = max(best, key[i]);
+        best = __reduce_max_sync(kAll, best);
+        if (best == 0) break;
+        uint32_t at = ~0u;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+            if (key[i] == best) at = i * 32 + lane;
+        at = __reduce_min_sync(kAll, at);
+        if (lane == j) { id = (int)at; mine = best; }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (at == (uint32_t)(i * 32 + lane)) key[i] = 0;
+    }
+    if (a.bias) {
+        // each chosen one against the next, then the last against all that is left
+        const float sx = id >= 0 ? logit_of(a, t, id) : 0.f, sb = id >= 0 ? __ldg(a.bias + id) : 0.f;
+        const float s = value_of(mine), s1 = __shfl_up_sync(kAll, s, 1);
+        const float x1 = __shfl_up_sync(kAll, sx, 1), c1 = __shfl_up_sync(kAll, sb, 1);
+        close |= lane > 0 && id >= 0 && s1 - s <= err + kCloseSum * fmaxf(fabsf(s1), fabsf(s)) && !(x1 == sx && c1 == sb);
+        const float last = __shfl_sync(kAll, s, a.k - 1), lx = __shfl_sync(kAll, sx, a.k - 1),
+                    lb = __shfl_sync(kAll, sb, a.k - 1);
+        if (__shfl_sync(kAll, id, a.k - 1) >= 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float v = value_of(key[i]);
+                if (key[i] && last - v <= err + kCloseSum * fmaxf(fabsf(last), fabsf(v)))
+                    close |= !(x[i] == lx && __ldg(a.bias + i * 32 + lane) == lb);
+            }
+        }
+    }
+    if (__any_sync(kAll, close)) id = choose_wide<V>(a, t);
+    // ---- weights of the chosen
+    const bool have = id >= 0;
+    const float z = have ? logit_of(a, t, id) : -kInf;
+    float w = 0.f;
+    if (a.renorm) {
+        // over the largest chosen logit (sigmoid: only if all are negative), so that weights
+        // that underflow together keep their ratios
+        const float c = warp_max(z);
+        if (have) {
+            if (!a.sigmoid) w = soft_num(z, c);
+            else w = c >= 0.f ? sigmoid(z) : expf(z - c) / (1.f + expf(z));
+        }
+        const float total = warp_sum(w);
+        w = have && total > 0.f ? w / total * a.scale : 0.f;
+    } else if (have) {
+        w = prob(z) * a.scale;
+    }
+    *id_out = id;
+    *w_out = w;
+}
+
+template <int V> constexpr int route_threads() { return V <= 8 ? 1024 : 512; }
+
+// Inclusive sum over a CTA's threads; part: a word per warp.
+__device__ __forceinline__ int block_scan(int v, int* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kAll, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) part[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int u = lane < warps ? part[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int q = __shfl_up_sync(kAll, u, o);
+            if (lane >= o) u += q;
+        }
+        part[lane] = u;
+    }
+    __syncthreads();
+    if (warp) v += part[warp - 1];
+    __syncthreads();
+    return v;
+}
+
+// ONE: all tokens, and their order; else the CTA's tokens and its counts.
+template <int V, bool ONE>
+__global__ void __launch_bounds__(route_threads<V>(), 1) k_moe_route(const RouteArgs a) {
+    extern __shared__ float group_buf[];
+    __shared__ uint32_t bits[ONE ? kRouteOne / 32 : 1][V * 32];       // ONE: who chose; else counts
+    __shared__ int base[V * 32];
+    __shared__ int part[32];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+    for (int i = tid; i < (ONE ? kRouteOne / 32 : 1) * V * 32; i += blockDim.x) (&bits[0][0])[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch();
+    const int t0 = ONE ? 0 : (int)blockIdx.x * a.per, t1 = min(a.T, t0 + (ONE ? a.T : a.per));
+    const int real = a.count ? min(max(__ldg(a.count), 0), a.T) : a.T;
+    for (int t = t0 + warp; t < t1; t += warps) {
+        int id = -1;
+        float w = 0.f;
+        if (t < real) choose<V>(a, t, group_buf + warp * a.E, &id, &w);
+        if (lane < a.k) {
+            a.ids[(size_t)t * a.k + lane] = id;
+            a.weights[(size_t)t * a.k + lane] = w;
+            if (id >= 0) {
+                if (ONE) atomicOr(&bits[t >> 5][id], 1u << (t & 31));
+                else atomicAdd(&bits[0][id], 1u);
+            }
+        }
+    }
+    __syncthreads();
+    if (!ONE) {
+        for (int e = tid; e < a.pitch; e += blockDim.x)
+            a.hist[(size_t)blockIdx.x * a.pitch + e] = e < a.E ? (uint16_t)bits[0][e] : (uint16_t)0;
+        return;
+    }
+    // first rows of the experts
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
+        const int e = e0 + tid;
+        int c = 0;
+        if (e < a.E)
+#pragma unroll
+            for (int i = 0; i < kRouteOne / 32; ++i) c += __popc(bits[i][e]);
+        const int v = block_scan(c, part);
+        if (e < a.E) {
+            base[e] = carry + v - c;
+            a.goff[e] = carry + v - c;
+            if (e == a.E - 1) a.goff[a.E] = carry + v;
+        }
+        carry += part[warps - 1];
+        __syncthreads();
+    }
+    for (int i = tid; i < a.T * a.k; i += blockDim.x) {
+        const int t = i / a.k, id = a.ids[i];
+        int r = -1;
+        if (id >= 0) {
+            r = base[id];
+#pragma unroll
+            for (int j = 0; j < kRouteOne / 32; ++j) {
+                const int d = t - 32 * j;
+                if (d > 0) r += __popc(d >= 32 ? bits[j][id] : bits[j][id] & ((1u << d) - 1u));
+            }
+        }
+        a.row[i] = r;
+    }
+}
+
+// The rows of a CTA's tokens: counts of all CTAs and of those before it, then ranks in runs of
+// 128 tokens.
+constexpr int kOrderThreads = 512, kOrderRun = 128;
+__global__ void __launch_bounds__(kOrderThreads, 1) k_moe_order(const RouteArgs a) {
+    extern __shared__ int order_smem[];             // base [pitch], total [pitch], bits [run / 32][pitch]
+    __shared__ int part[32];
+    int *base = order_smem, *total = base + a.pitch;
+    uint32_t* bits = reinterpret_cast<uint32_t*>(total + a.pitch);
+    const int tid = threadIdx.x, me = blockIdx.x, B = gridDim.x;
+    for (int i = tid; i < (2 + kOrderRun / 32) * a.pitch; i += blockDim.x) order_smem[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch();
+    {
+        // a thread: eight experts of every `rows`-th CTA
+        const int cols = a.pitch / 8, rows = blockDim.x / cols, c = tid % cols, r = tid / cols;
+        int all[8], before[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all[i] = before[i] = 0;
+        if (r < rows) {
+#pragma unroll 4
+            for (int b = r; b < B; b += rows) {
+                const uint4 u = *reinterpret_cast<const uint4*>(a.hist + (size_t)b * a.pitch + c * 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int n = (int)((&u.x)[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
+                    all[i] += n;
+                    if (b < me) before[i] += n;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (all[i]) atomicAdd(total + c * 8 + i, all[i]);
+                if (before[i]) atomicAdd(base + c * 8 + i, before[i]);
+            }
+        }
+    }
+    __syncthreads();
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
+        const int e = e0 + tid, c = e < a.E ? total[e] : 0, v = block_scan(c, part);
+        if (e < a.E) {
+            base[e] += carry + v - c;
+            if (me == 0) {
+                a.goff[e] = carry + v - c;
+                if (e == a.E - 1) a.goff[a.E] = carry + v;
+            }
+        }
+        carry += part[(blockDim.x >> 5) - 1];
+        __syncthreads();
+    }
+    const int t1 = min(a.T, (me + 1) * a.per);
+    for (int t0 = me * a.per; t0 < t1; t0 += kOrderRun) {
+        const int n = min(kOrderRun, t1 - t0) * a.k;
+        const int32_t* ids = a.ids + (size_t)t0 * a.k;
+        for (int i = tid; i < n; i += blockDim.x) {
+            const int t = i / a.k, id = ids[i];
+            if (id >= 0) atomicOr(bits + (t >> 5) * a.pitch + id, 1u << (t & 31));
+        }
+        __syncthreads();
+        for (int i = tid; i < n; i += blockDim.x) {
+            const int t = i / a.k, id = ids[i];
+            int r = -1;
+            if (id >= 0) {
+                r = base[id];
+#pragma unroll
+                for (int j = 0; j < kOrderRun / 32; ++j) {
+                    const int d = t - 32 * j;
+                    const uint32_t word = bits[j * a.pitch + id];
+                    if (d > 0) r += __popc(d >= 32 ? word : word & ((1u << d) - 1u));
+                }
+            }
+            a.row[(size_t)t0 * a.k + i] = r;
+        }
+        if (t0 + kOrderRun >= t1) break;
+        __syncthreads();
+        for (int e = tid; e < a.E; e += blockDim.x)
+#pragma unroll
+            for (int j = 0; j < kOrderRun / 32; ++j) {
+                base[e] += __popc(bits[j * a.pitch + e]);
+                bits[j * a.pitch + e] = 0;
+            }
+        __syncthreads();
+    }
+}
+
+template <typename... A>
+bool launch(void (*kern)(A...), int grid, int threads, size_t smem, cudaStream_t stream, const RouteArgs& a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess;
+}
+
+template <int V>
+int go(const RouteArgs& a, cudaStream_t stream) {
+    const bool one = a.T <= kRouteOne;
+    // no more warps than tokens
+    const int tokens = one ? a.T : a.per, threads = std::min(route_threads<V>(), std::max(128, (tokens * 32 + 127) / 128 * 128));
+    const size_t smem = a.groups > 1 ? (size_t)threads / 32 * a.E * sizeof(float) : 0;
+    static SmemLimit limit[2];
+    constexpr int most = route_threads<V>() / 32 * V * 32 * (int)sizeof(float);
+    if (one) {
+        if (!limit[0].raise(k_moe_route<V, true>, most)) return W4_ERR_CUDA;
+        return launch(k_moe_route<V, true>, 1, threads, smem, stream, a) ? W4_OK : W4_ERR_CUDA;
+    }
+    if (!limit[1].raise(k_moe_route<V, false>, most)) return W4_ERR_CUDA;
+    const int grid = (a.T + a.per - 1) / a.per;
+    if (!launch(k_moe_route<V, false>, grid, threads, smem, stream, a)) return W4_ERR_CUDA;
+    return launch(k_moe_order, grid, kOrderThreads, (2 + kOrderRun / 32) * a.pitch * sizeof(int), stream, a)
+               ? W4_OK : W4_ERR_CUDA;
+}
+
+}  // namespace
+
+int route_blocks(int T) { return std::min(kRouteBlocks, (T + 31) / 32); }
+
+int launch_moe_route(const RouteArgs& a, cudaStream_t stream) {
+    return a.E <= 64 ? go<2>(a, stream) : a.E <= 128 ? go<4>(a, stream) : a.E <= 256 ? go<8>(a, stream)
+         : a.E <= 512 ? go<16>(a, stream) : go<32>(a, stream);
+}
+
+}  // namespace w4

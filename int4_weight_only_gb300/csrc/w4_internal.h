@@ -251,6 +251,19 @@ struct RopeArgs {
 };
 int launch_rope_append(const RopeArgs& a, cudaStream_t stream);
 
+// Prefixes shared by groups of sequences, and the results of their parts on the way from the
+// kernel that computes them to the one that joins them.
+constexpr int kSharedRows = 256;           // rows of a part
+constexpr int kSharedItemUnits = 2;        // units of an item besides its steps
+struct AttnShared {
+    const int32_t *group, *shared;         // [groups + 1] first sequences, [groups] lengths
+    int groups;
+    int* share;                            // units of a CTA
+    int4* info;                            // [batch]: see publish_shared
+    float *row_o, *row_ml;                 // items of one part: [batch, Hq, D], [batch, Hq, 2]
+    float *slot_o, *slot_ml;               // others: [2 CTAs][kSharedRows][D], [2]
+};
+
 // Attention over the paged cache (attn_decode.cu, attn_prefill.cu).
 struct AttnArgs {
     w4_paged_kv kv;
@@ -265,9 +278,60 @@ struct AttnArgs {
     int* tickets;                  // decode: arrival counters and partial results
     float* partial;
     int* err;
+    AttnShared sh;
 };
 size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count);   // of partial results
 int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream);
 int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream);
+// The shared prefixes' parts, then every sequence's own keys and the join.
+int launch_attn_shared_prefix(const AttnArgs& a, int sm_count, cudaStream_t stream);
+int launch_attn_shared_own(const AttnArgs& a, int sm_count, cudaStream_t stream);
+
+
+// ---------------------------------------------------------------- experts
+// Routing (moe_route.cu).  Up to kRouteOne tokens one CTA does everything; more go to
+// kRouteBlocks CTAs at most, whose counts by expert a second kernel adds up.
+constexpr int kRouteOne = 64;
+constexpr int kRouteBlocks = 152;
+struct RouteArgs {
+    const void* logits;
+    long long stride;
+    const float* bias;
+    const int32_t* count;
+    int bf16, T, E, k, sigmoid, groups, gsize, top_groups, best, renorm;
+    float scale;
+    float* weights;
+    int32_t *ids, *row, *goff;
+    uint16_t* hist;                // [CTAs][pitch]
+    int pitch, per;                // tokens of a CTA
+};
+inline int route_pitch(int E) { return (E + 7) / 8 * 8; }
+int route_blocks(int T);           // CTAs of the larger form
+int launch_moe_route(const RouteArgs& a, cudaStream_t stream);
+
+// Tokens to experts' rows and back (moe_move.cu).
+struct MoveArgs {
+    const uint16_t *x, *shared;    // gather: x; combine: y
+    long long stride;              // of x
+    const int32_t* row;
+    const float* weights;
+    uint16_t* out;
+    int T, k, K, R;
+    int* err;
+};
+int launch_moe_gather(const MoveArgs& a, cudaStream_t stream);
+int launch_moe_combine(const MoveArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- page plans
+struct PlanArgs {
+    const int32_t *lens, *fresh, *free_pages, *used;
+    int32_t* table;
+    long long table_stride;
+    int n_free, batch, max_pages, page_size, pages, T;
+    int32_t *kv_len, *goff, *pos, *lens_out, *used_out;
+    int64_t* slots;
+    int* err;
+};
+int launch_kv_plan(const PlanArgs& a, cudaStream_t stream);
 
 }  // namespace w4
