@@ -82,11 +82,14 @@ int w4_moe_route(const void* logits, int logits_bf16, long long logits_stride, c
     a.T = T; a.E = E; a.k = k; a.sigmoid = score == W4_MOE_SIGMOID;
     a.groups = groups; a.gsize = E / groups; a.top_groups = top_groups; a.best = group_best;
     a.renorm = renorm ? 1 : 0; a.scale = scale;
+    a.lanes = 32;
+    while (a.lanes * groups > 32) a.lanes /= 2;
+    a.group_inv = ((1 << 20) + a.gsize - 1) / a.gsize;
     a.weights = weights; a.ids = ids; a.row = row; a.goff = goff;
     a.hist = static_cast<uint16_t*>(workspace);
     a.pitch = route_pitch(E);
     const int blocks = std::max(route_blocks(T), 1);
-    a.per = ((T + blocks - 1) / blocks + 31) / 32 * 32;
+    a.per = std::max((T + blocks - 1) / blocks, 1);
     return launch_moe_route(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -4,16 +4,18 @@
 //   p = softmax(z) or sigmoid(z),  s = p + bias,  the k largest s among the kept groups
 //   w = p of the chosen, over their sum;  row = place in the order (expert, token)
 //
-// A warp takes a token: logit e of it sits in lane e % 32, register e / 32.  Scores become
-// integer keys of the same order, so that a round of the selection is one maximum over the
-// lane's registers and two warp reductions (the largest key, the lowest index that has it).
+// A warp takes a token: logit e of it sits in lane e % 32, register e / 32; the next token's
+// logits are on their way meanwhile.  Each lane keeps its two best, so that a round of the
+// selection is one warp reduction over the lanes' heads, and only a lane that has given
+// both looks through its registers again (with 256 experts and k = 8, one token in 20).
 //
 // Scores closer than their fp32 errors could come out in the wrong order, and another expert
 // would be chosen than the definition says.  Without a bias nothing is at stake: the logits
-// have the order of the scores.  With one, or with groups ranked by two scores, the warp looks
-// at every comparison that decided something; where one was closer than kClose allows (and
-// the two experts do not have the same logit and bias, which is a true tie), it chooses again
-// in 64 bits.  With 256 experts that is one token in some thousand.
+// have the order of the scores.  With one, the warp looks at the gaps between the chosen and
+// to what is left.  Where one is closer than the errors allow (and the two experts do not have
+// the same logit and bias, which is a true tie), the chosen and those as close are ranked by
+// their scores in 64 bits, one candidate a lane (settle).  Where groups ranked by scores are
+// that close, the token is chosen again in 64 bits (choose_wide).
 //
 // The order is a counting sort without atomics on results: in a run of 32 tokens, bit t of an
 // expert's word says that token t chose it, so a choice's rank among the run's is a population
@@ -30,11 +32,15 @@ namespace {
 constexpr float kInf = __builtin_huge_valf();
 constexpr uint32_t kAll = 0xffffffffu;
 
-// Scores differ by the errors of the exponential (its argument's rounding, 2^-24 |x - m|
-// e^-|x - m| < 2^-25 of the largest p, and 2^-22 of p), of the sum (at most E / 32 + 5
-// roundings, 2^-18.8 of p) and of the quotient; two of them by less than 2^-18 of the largest
-// p.  The rounding of p + bias adds 2^-24 of it each.
-constexpr float kClose = 0x1p-18f, kCloseSum = 0x1p-22f;
+// How far two scores of a row can be off against each other, over its largest p.  Each is off by
+// the exponential's 2^-22 of p (a sigmoid: of p (1 - p) <= 1/4) and the quotient's 2^-22, a softmax
+// also by its argument's rounding, 2^-24 |x - m| e^-|x - m| < 2^-25; the roundings of a softmax's
+// sum, over V registers and 5 steps, and of its reciprocal are the same for both.  The
+// rounding of p + bias adds kCloseSum of the score.
+template <int V> __device__ __forceinline__ float close_of(bool sigmoid) {
+    return sigmoid ? 0x1p-20f : 0x1p-20f + (V + 7) * 0x1p-24f;
+}
+constexpr float kCloseSum = 0x1p-22f;
 
 // Order-preserving key of a float that is not NaN; 0 is below every key of a value over -inf.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -47,23 +53,36 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ float warp_max(float v) {
     return value_of(__reduce_max_sync(kAll, key_of(v)));
 }
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ double warp_sum_wide(double v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 
 // Logit e of token t: NaN as -inf, -0 as +0 (equal values have equal bits).
+__device__ __forceinline__ float clean(float v) { return v != v ? -kInf : v + 0.f; }
 __device__ __forceinline__ float logit_of(const RouteArgs& a, int t, int e) {
     const long long at = t * a.stride + e;
-    const float v = a.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at])
-                           : static_cast<const float*>(a.logits)[at];
-    return v != v ? -kInf : v + 0.f;
+    return clean(a.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at])
+                        : static_cast<const float*>(a.logits)[at]);
+}
+// A lane's logits as they are, -inf past the last expert.
+template <int V> __device__ __forceinline__ void load_logits(const RouteArgs& a, int t, float* x) {
+    const int lane = threadIdx.x & 31;
+    if (a.bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.logits) + t * a.stride + lane;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i * 32 + lane < a.E ? bf16_bits_to_f32(__ldg(p + i * 32)) : -kInf;
+    } else {
+        const float* p = static_cast<const float*>(a.logits) + t * a.stride + lane;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i * 32 + lane < a.E ? __ldg(p + i * 32) : -kInf;
+    }
 }
 
 // p of logit x, given the row's largest logit and sum of exponentials over it.
 __device__ __forceinline__ float soft_num(float x, float m) { return m == kInf ? (x == kInf ? 1.f : 0.f) : expf(x - m); }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
 __device__ __forceinline__ double soft_num(double x, double m) { return isinf(m) && m > 0 ? (x == m ? 1. : 0.) : exp(x - m); }
 __device__ __forceinline__ double sigmoid(double x) { return 1. / (1. + exp(-x)); }
 
@@ -95,7 +114,7 @@ __device__ __noinline__ int choose_wide(const RouteArgs& a, int t) {
     }
     if (!a.sigmoid) {
         for (int i = 0; i < V; ++i) sum += x[i] > -kInf ? soft_num(x[i], m) : 0.;
-        sum = warp_sum(sum);
+        sum = warp_sum_wide(sum);
     }
     // what groups are ranked by; without a bias experts are chosen by their logits
     double s[V];
@@ -160,74 +179,141 @@ __device__ __noinline__ int choose_wide(const RouteArgs& a, int t) {
     return id;
 }
 
-// The experts of token t: lane j gets the j-th (or -1) and its weight.  buf: E floats of the
-// warp's own (groups).
+// Ranks up to 32 candidates of token t, one a lane (e < 0: none), by their scores in 64 bits; returns
+// the one of rank `lane`.  m: the row's largest logit.
 template <int V>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, float* buf, int* id_out, float* w_out) {
+__device__ __noinline__ int settle(const RouteArgs& a, int t, int e, float m) {
     const int lane = threadIdx.x & 31;
-    float x[V], m = -kInf, sum = 0.f;
+    double s = -kInf, sum = 1.;
+    if (!a.sigmoid) {
+        sum = 0.;
+#pragma unroll 1
+        for (int i = lane; i < a.E; i += 32) {
+            const float x = logit_of(a, t, i);
+            sum += x > -kInf ? soft_num((double)x, (double)m) : 0.;
+        }
+        sum = warp_sum_wide(sum);
+    }
+    if (e >= 0) {
+        const double x = logit_of(a, t, e);
+        s = (a.sigmoid ? sigmoid(x) : soft_num(x, (double)m) / sum) + (double)__ldg(a.bias + e);
+    }
+    int rank = 0, got = -1;
+#pragma unroll 1
+    for (int o = 0; o < 32; ++o) {
+        const double v = __shfl_sync(kAll, s, o);
+        const int w = __shfl_sync(kAll, e, o);
+        rank += w >= 0 && (v > s || (v == s && w < e));
+    }
+#pragma unroll 1
+    for (int o = 0; o < 32; ++o) {
+        const int w = __shfl_sync(kAll, e, o), r = __shfl_sync(kAll, rank, o);
+        if (w >= 0 && r == lane) got = w;
+    }
+    return got;
+}
+
+// The best two of a lane's values behind (v0, i0) in the order of falling values and rising
+// registers.
+template <int V>
+__device__ __forceinline__ void best_two(const float* s, float v0, int i0, float* b1, int* i1, float* b2, int* i2) {
+    *b1 = *b2 = -kInf;
+    *i1 = *i2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        x[i] = i * 32 + lane < a.E ? logit_of(a, t, i * 32 + lane) : -kInf;
+        const float v = s[i] < v0 || (s[i] == v0 && i > i0) ? s[i] : -kInf;
+        if (v > *b1) { *b2 = *b1; *i2 = *i1; *b1 = v; *i1 = i; }
+        else if (v > *b2) { *b2 = v; *i2 = i; }
+    }
+}
+
+// The experts of token t, whose logits a lane has in x: lane j gets the j-th (or -1) and its
+// weight.  buf: E floats of the warp's own (groups).
+template <int V>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, float* buf, int* id_out, float* w_out) {
+    const int lane = threadIdx.x & 31;
+    const bool two = a.groups > 1 && a.best == 2;   // groups ranked by sums of scores
+    const bool scored = a.bias || two;
+    float m = -kInf, inv = 1.f;                     // softmax: largest logit, reciprocal sum
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = clean(x[i]);
         m = fmaxf(m, x[i]);
     }
-    const bool two = a.groups > 1 && a.best == 2;
-    const bool scored = a.bias || two;              // the choice goes by scores
-    m = warp_max(m);
-    if (!a.sigmoid && (scored || !a.renorm)) {
+    if (scored || !a.renorm) {
+        m = warp_max(m);
+        if (!a.sigmoid) {
+            float sum = 0.f;
+            if (fabsf(m) == kInf) {                 // infinite logits, or none
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum += x[i] > -kInf ? soft_num(x[i], m) : 0.f;
-        sum = warp_sum(sum);
-    }
-    auto prob = [&](float v) { return a.sigmoid ? sigmoid(v) : soft_num(v, m) / sum; };
-    uint32_t key[V];
-    bool close = false;
-    if (scored) {
+                for (int i = 0; i < V; ++i) sum += x[i] == kInf ? 1.f : 0.f;
+            } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float s = -kInf;
-            if (x[i] > -kInf) {
-                s = prob(x[i]);
-                if (a.bias) s += __ldg(a.bias + i * 32 + lane);
+                for (int i = 0; i < V; ++i) sum += expf(x[i] - m);
             }
-            key[i] = s > -kInf ? key_of(s) : 0u;
+            inv = __fdividef(1.f, warp_sum(sum));
         }
-        if (a.groups > 1) {
+    }
+    auto prob = [&](float v) { return a.sigmoid ? sigmoid(v) : soft_num(v, m) * inv; };
+    // what groups are ranked by two scores of, and experts are chosen by when there is a bias
+    // (s may be x)
+    auto scores = [&](float* s) {
+        auto put = [&](int i, float p) {
+            if (a.bias) p += __ldg(a.bias + min(i * 32 + lane, a.E - 1));
+            s[i] = x[i] > -kInf && p > -kInf ? p : -kInf;
+        };
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) put(i, sigmoid(x[i]));
+        } else if (fabsf(m) == kInf) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) put(i, x[i] == kInf ? inv : 0.f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) put(i, expf(x[i] - m) * inv);
+        }
+    };
+    // from here x is what experts are chosen by, -inf where they are not offered
+    if (a.bias) scores(x);
+    const float err = scored && m > -kInf ? close_of<V>(a.sigmoid) * prob(m) : 0.f;
+    bool again = false;
+    if (a.groups > 1) {
+        if (two && !a.bias) {
+            float s[V];
+            scores(s);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (i * 32 + lane < a.E) buf[i * 32 + lane] = key[i] ? value_of(key[i]) : -kInf;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = x[i] > -kInf ? key_of(x[i]) : 0u;
-        if (a.groups > 1) {
+                if (i * 32 + lane < a.E) buf[i * 32 + lane] = s[i];
+        } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (i * 32 + lane < a.E) buf[i * 32 + lane] = x[i];
         }
-    }
-    __syncwarp();
-    const float err = scored && m > -kInf ? kClose * prob(m) : 0.f;
-    if (a.groups > 1) {
+        __syncwarp();
         // L lanes a group, each with every L-th of its scores; groups start at different ones,
         // so that the lanes' words lie in different banks
-        int L = 32;
-        while (L > 1 && L * a.groups > 32) L >>= 1;
-        const int g = lane / L, sub = lane % L, steps = (a.gsize + L - 1) / L;
+        const int L = a.lanes, g = lane / L, sub = lane - g * L;
         float b1 = -kInf, b2 = -kInf;
         if (g < a.groups) {
-            int at = g % steps;
-            for (int i = 0; i < steps; ++i) {
-                if (at * L + sub < a.gsize) top_two<float>(b1, b2, buf[g * a.gsize + at * L + sub], -kInf);
-                if (++at == steps) at = 0;
+            const float* mine = buf + g * a.gsize;
+            int at = g * L % a.gsize / L * L + sub;  // L divides neither gsize nor this in general
+#pragma unroll 4
+            for (int i = sub; i < a.gsize; i += L) {
+                if (at >= a.gsize) at = sub;
+                const float v = mine[at];
+                b2 = fmaxf(b2, fminf(b1, v));
+                b1 = fmaxf(b1, v);
+                at += L;
             }
         }
         for (int o = L / 2; o; o >>= 1) {
             const float c1 = __shfl_xor_sync(kAll, b1, o), c2 = __shfl_xor_sync(kAll, b2, o);
-            top_two(b1, b2, c1, c2);
+            b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+            b1 = fmaxf(b1, c1);
         }
         const float mine = group_rank(b1, b2, a.best);
         int above = 0;
+#pragma unroll 4
         for (int i = 0; i < a.groups; ++i) {
             const float v = __shfl_sync(kAll, mine, i * L);
             above += v > mine || (v == mine && i < g);
@@ -235,55 +321,71 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* buf, in
         const bool in = g < a.groups && above < a.top_groups;
         if (scored) {
             const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
-            close |= hi > -kInf && lo - hi <= 2.f * err + 2.f * kCloseSum * (fabsf(lo) + fabsf(hi));
+            again = hi > -kInf && lo - hi <= 2.f * err + 2.f * kCloseSum * (fabsf(lo) + fabsf(hi));
         }
         const uint32_t keep = __ballot_sync(kAll, in && sub == 0);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i * 32 + lane < a.E && !(keep >> ((i * 32 + lane) / a.gsize * L) & 1)) key[i] = 0;
+        for (int i = 0; i < V; ++i)                 // (i * 32 + lane) / gsize, exact below 1024
+            if (!(keep >> (((i * 32 + lane) * a.group_inv >> 20) * L) & 1)) x[i] = -kInf;
         __syncwarp();                               // buf is read
     }
-    if (scored && !a.bias) {                        // inside the groups the logits have the scores' order
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i]) key[i] = key_of(x[i]);
-    }
     int id = -1;
-    uint32_t mine = 0;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
+    float mine = -kInf;                             // what it was chosen by
+    if (!__any_sync(kAll, again)) {
+        float b1, b2, out = kInf;
+        int i1, i2, known = 2, at_out = -1;
+        best_two<V>(x, kInf, -1, &b1, &i1, &b2, &i2);
+        int chosen = 0;
+        for (; chosen < a.k; ++chosen) {
+            const uint32_t head = b1 > -kInf ? key_of(b1) : 0u, best = __reduce_max_sync(kAll, head);
+            if (best == 0) break;
+            const uint32_t who = __ballot_sync(kAll, head == best);
+            int from = __ffs(who) - 1;
+            if (who & (who - 1)) {                  // equal ones: the lowest expert
+                const uint32_t e = __reduce_min_sync(kAll, head == best ? (uint32_t)(i1 * 32 + lane) : ~0u);
+                from = (int)(e & 31);
+            }
+            const int e = __shfl_sync(kAll, i1, from) * 32 + from;
+            if (lane == chosen) { id = e; mine = value_of(best); }
+            if (lane == from) { out = b1; at_out = i1; b1 = b2; i1 = i2; --known; }
+            if (__any_sync(kAll, known == 0)) {
+                if (known == 0) { best_two<V>(x, out, at_out, &b1, &i1, &b2, &i2); known = 2; }
+            }
+        }
+        if (a.bias && chosen > 0) {
+            // each chosen one against the one before, then what is left against the last
+            const float s1 = __shfl_up_sync(kAll, mine, 1), last = __shfl_sync(kAll, mine, chosen - 1);
+            const int e1 = __shfl_up_sync(kAll, id, 1), e_last = __shfl_sync(kAll, id, chosen - 1);
+            bool close = lane > 0 && id >= 0 && s1 - mine <= err + kCloseSum * fmaxf(fabsf(s1), fabsf(mine));
+            const float reach = err + kCloseSum * (fabsf(last) + err);
+            uint32_t left = 0;                      // registers with an expert as good as the last
 #pragma unroll
-        for (int i = 0; i < V; ++i) best = max(best, key[i]);
-        best = __reduce_max_sync(kAll, best);
-        if (best == 0) break;
-        uint32_t at = ~0u;
-#pragma unroll
-        for (int i = V - 1; i >= 0; --i)
-            if (key[i] == best) at = i * 32 + lane;
-        at = __reduce_min_sync(kAll, at);
-        if (lane == j) { id = (int)at; mine = best; }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (at == (uint32_t)(i * 32 + lane)) key[i] = 0;
-    }
-    if (a.bias) {
-        // each chosen one against the next, then the last against all that is left
-        const float sx = id >= 0 ? logit_of(a, t, id) : 0.f, sb = id >= 0 ? __ldg(a.bias + id) : 0.f;
-        const float s = value_of(mine), s1 = __shfl_up_sync(kAll, s, 1);
-        const float x1 = __shfl_up_sync(kAll, sx, 1), c1 = __shfl_up_sync(kAll, sb, 1);
-        close |= lane > 0 && id >= 0 && s1 - s <= err + kCloseSum * fmaxf(fabsf(s1), fabsf(s)) && !(x1 == sx && c1 == sb);
-        const float last = __shfl_sync(kAll, s, a.k - 1), lx = __shfl_sync(kAll, sx, a.k - 1),
-                    lb = __shfl_sync(kAll, sb, a.k - 1);
-        if (__shfl_sync(kAll, id, a.k - 1) >= 0) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float v = value_of(key[i]);
-                if (key[i] && last - v <= err + kCloseSum * fmaxf(fabsf(last), fabsf(v)))
-                    close |= !(x[i] == lx && __ldg(a.bias + i * 32 + lane) == lb);
+            for (int i = 0; i < V; ++i)
+                if (x[i] > -kInf && (x[i] < last || (x[i] == last && i * 32 + lane > e_last)) && last - x[i] <= reach)
+                    left |= 1u << i;
+            if (__any_sync(kAll, close || left)) {
+                auto same = [&](int e, int f) {
+                    return logit_of(a, t, e) == logit_of(a, t, f) && __ldg(a.bias + e) == __ldg(a.bias + f);
+                };
+                if (close && same(id, e1)) close = false;
+                bool open = close;
+                int n = chosen, cand = id;
+#pragma unroll 1
+                for (int i = 0; i < V; ++i) {
+                    bool in = left >> i & 1;
+                    if (in && !same(i * 32 + lane, e_last)) open = true;
+                    for (uint32_t b = __ballot_sync(kAll, in); b; b &= b - 1, ++n)
+                        if (lane == n) cand = i * 32 + __ffs(b) - 1;
+                }
+                if (__any_sync(kAll, open)) {
+                    if (n > 32) again = true;
+                    else id = settle<V>(a, t, cand, m);
+                    if (lane >= a.k) id = -1;
+                }
             }
         }
     }
-    if (__any_sync(kAll, close)) id = choose_wide<V>(a, t);
+    if (__any_sync(kAll, again)) id = choose_wide<V>(a, t);
     // ---- weights of the chosen
     const bool have = id >= 0;
     const float z = have ? logit_of(a, t, id) : -kInf;
@@ -294,7 +396,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* buf, in
         const float c = warp_max(z);
         if (have) {
             if (!a.sigmoid) w = soft_num(z, c);
-            else w = c >= 0.f ? sigmoid(z) : expf(z - c) / (1.f + expf(z));
+            else w = c >= 0.f ? sigmoid(z) : __fdividef(expf(z - c), 1.f + expf(z));
         }
         const float total = warp_sum(w);
         w = have && total > 0.f ? w / total * a.scale : 0.f;
@@ -305,7 +407,10 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* buf, in
     *w_out = w;
 }
 
-template <int V> constexpr int route_threads() { return V <= 8 ? 1024 : 512; }
+#ifndef RT
+#define RT 1024
+#endif
+template <int V> constexpr int route_threads() { return V <= 8 ? RT : 512; }
 
 // Inclusive sum over a CTA's threads; part: a word per warp.
 __device__ __forceinline__ int block_scan(int v, int* part) {
@@ -346,10 +451,17 @@ __global__ void __launch_bounds__(route_threads<V>(), 1) k_moe_route(const Route
     pdl_launch();
     const int t0 = ONE ? 0 : (int)blockIdx.x * a.per, t1 = min(a.T, t0 + (ONE ? a.T : a.per));
     const int real = a.count ? min(max(__ldg(a.count), 0), a.T) : a.T;
+    float x[V], nx[V];
+    if (t0 + warp < min(t1, real)) load_logits<V>(a, t0 + warp, nx);
     for (int t = t0 + warp; t < t1; t += warps) {
         int id = -1;
         float w = 0.f;
-        if (t < real) choose<V>(a, t, group_buf + warp * a.E, &id, &w);
+        if (t < real) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = nx[i];
+            if (t + warps < min(t1, real)) load_logits<V>(a, t + warps, nx);
+            choose<V>(a, t, x, group_buf + warp * a.E, &id, &w);
+        }
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = id;
             a.weights[(size_t)t * a.k + lane] = w;

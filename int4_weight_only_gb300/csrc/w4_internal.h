@@ -251,8 +251,8 @@ struct RopeArgs {
 };
 int launch_rope_append(const RopeArgs& a, cudaStream_t stream);
 
-// Prefixes shared by groups of sequences, and the results of their parts on the way from the
-// kernel that computes them to the one that joins them.
+// Prefixes shared by groups of sequences, and the results of parts (of the prefixes and of the
+// sequences' own keys) on the way from the kernels that compute them to the one that joins them.
 constexpr int kSharedRows = 256;           // rows of a part
 constexpr int kSharedItemUnits = 2;        // units of an item besides its steps
 struct AttnShared {
@@ -262,6 +262,10 @@ struct AttnShared {
     int4* info;                            // [batch]: see publish_shared
     float *row_o, *row_ml;                 // items of one part: [batch, Hq, D], [batch, Hq, 2]
     float *slot_o, *slot_ml;               // others: [2 CTAs][kSharedRows][D], [2]
+    int* own_share;                        // own keys: units of a worker, and of each sequence its
+    int2* own_info;                        // first unit and the units of an item
+    float *own_row_o, *own_row_ml;         // as above; slots: [2 workers][heads of an item]
+    float *own_slot_o, *own_slot_ml;
 };
 
 // Attention over the paged cache (attn_decode.cu, attn_prefill.cu).
@@ -283,7 +287,8 @@ struct AttnArgs {
 size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count);   // of partial results
 int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream);
 int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream);
-// The shared prefixes' parts, then every sequence's own keys and the join.
+// The shared prefixes' parts, then (attn_shared.cu) every sequence's own keys and the join.
+int shared_own_slots(int Hq, int Hkv, int D, int sm_count);      // rows of own_slot_o
 int launch_attn_shared_prefix(const AttnArgs& a, int sm_count, cudaStream_t stream);
 int launch_attn_shared_own(const AttnArgs& a, int sm_count, cudaStream_t stream);
 
@@ -299,6 +304,7 @@ struct RouteArgs {
     const float* bias;
     const int32_t* count;
     int bf16, T, E, k, sigmoid, groups, gsize, top_groups, best, renorm;
+    int lanes, group_inv;          // lanes of a warp that rank a group; ceil(2^20 / gsize)
     float scale;
     float* weights;
     int32_t *ids, *row, *goff;
