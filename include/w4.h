@@ -652,18 +652,17 @@ W4_API int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q
  *  raise W4_ERR_PAGE_TABLE; offsets outside [0, batch] or decreasing raise
  *  W4_ERR_GROUP_TOKENS.  The outputs concerned are then unspecified.
  *  q       strides positive multiples of 8 (of extent 1: ignored); the other
- *          arguments are w4_attn_decode's, the workspace included.
+ *          arguments are w4_attn_decode's.
  *  scratch at least w4_attn_shared_scratch_bytes(...) bytes, 16-byte aligned,
- *          need not be initialised: the shared parts' results between the two
- *          kernels of a call.  Calls that can overlap need one each.
+ *          need not be initialised: results of parts between the kernels of a
+ *          call.  Calls that can overlap need one each.
  *  groups >= 1; head counts and head_dim as in w4_attn_decode.
  * ------------------------------------------------------------------------- */
 W4_API size_t w4_attn_shared_scratch_bytes(int batch, int q_heads, int heads, int head_dim);
 W4_API int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,
                           long long q_head_stride, const int32_t* group, const int32_t* shared,
                           int groups, uint16_t* out, float* lse, int q_heads, int max_len,
-                          float scale, void* workspace, size_t workspace_bytes, void* scratch,
-                          size_t scratch_bytes, void* stream);
+                          float scale, void* scratch, size_t scratch_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * w4_kv_plan - one step's page table entries, lengths, offsets and slots from

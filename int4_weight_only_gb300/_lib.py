@@ -56,7 +56,7 @@ _SIGS = {
                         + [ctypes.c_float, _c_int, _c_int, _vp]),
     "w4_attn_shared_scratch_bytes": (_c_size, [_c_int] * 4),
     "w4_attn_shared": (_c_int, [_vp, _vp, _c_ll, _c_ll, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int,
-                                ctypes.c_float, _vp, _c_size, _vp, _c_size, _vp]),
+                                ctypes.c_float, _vp, _c_size, _vp]),
     "w4_kv_plan": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _c_ll] + [_c_int] * 5 + [_vp] * 7),
     "w4_moe_route_workspace_bytes": (_c_size, [_c_int] * 2),
     "w4_moe_route": (_c_int, [_vp, _c_int, _c_ll, _vp, _vp] + [_c_int] * 8 + [ctypes.c_float]
@@ -873,15 +873,14 @@ def w4_attn_shared_scratch_bytes(batch: int, q_heads: int, heads: int, head_dim:
 
 def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_len: torch.Tensor,
                    table: torch.Tensor, group: torch.Tensor, shared: torch.Tensor, max_len: int,
-                   scale: Optional[float] = None, out=None, lse=None, workspace=None, scratch=None,
-                   stream=None) -> torch.Tensor:
+                   scale: Optional[float] = None, out=None, lse=None, scratch=None, stream=None) -> torch.Tensor:
     """w4_attn_decode (without a window) where groups of sequences share their
     first tokens: sequences group[i] .. group[i + 1] - 1 (group [G + 1] int32) have
     their first shared[i] tokens (shared [G] int32) in common, in the pages that
     the first one's row of the table names; those are read once for the group.
-    kv_len counts them; a sequence has at least shared[i] tokens, or 0.  workspace
-    is w4_attn_decode's; scratch (w4_attn_shared_scratch_bytes, uninitialised) is
-    allocated for the call when not given."""
+    kv_len counts them; a sequence has at least shared[i] tokens, or 0.  scratch
+    (w4_attn_shared_scratch_bytes, uninitialised) is allocated for the call when
+    not given."""
     kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
     qs = _need_view(q, torch.bfloat16, 3, "q")
     B, Hq, D = q.shape
@@ -904,17 +903,10 @@ def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         need = _scratch_sizes[key] = lib.w4_attn_shared_scratch_bytes(B, Hq, pool[1], D)
     if scratch is None:
         scratch = _scratch(max(need, 16), q.device, stream)
-    ws = workspace if workspace is not None else _ws.get(q.get_device())
-
-    def call(ws):
-        return lib.w4_attn_shared(
-            kv, q.data_ptr(), qs[0], qs[1], group.data_ptr(), shared.data_ptr(), G, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), Hq, max_len, D ** -0.5 if scale is None else scale,
-            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
-            scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(q, stream))
-    rc = call(ws)
-    if rc == W4_ERR_WORKSPACE and workspace is None:
-        rc = call(_workspace(q.device, lib.w4_attn_decode_workspace_bytes(Hq, pool[1], D), stream))
+    rc = lib.w4_attn_shared(
+        kv, q.data_ptr(), qs[0], qs[1], group.data_ptr(), shared.data_ptr(), G, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), Hq, max_len, D ** -0.5 if scale is None else scale,
+        scratch.data_ptr(), scratch.numel() * scratch.element_size(), _stream(q, stream))
     if rc:
         raise W4Error("w4_attn_shared", rc)
     return out
@@ -953,10 +945,11 @@ def w4_kv_plan(lens: torch.Tensor, new_tokens: Optional[torch.Tensor], free_page
         _i32(used_out, (1,), "used_out")
     if T < 0 or (T | pages | page_size) > 0x7FFFFFFF:
         raise ValueError(f"T={T}, pages={pages}, page_size={page_size}: out of range")
-    kv_len = lens.new_empty(B)
-    goff = lens.new_empty(B + 1)
-    pos = lens.new_empty(T)
-    slots = lens.new_empty(T, dtype=torch.int64)
+    dev, i32 = lens.device, torch.int32
+    kv_len = torch.empty_like(lens)
+    goff = torch.empty(B + 1, dtype=i32, device=dev)
+    pos = torch.empty(T, dtype=i32, device=dev)
+    slots = torch.empty(T, dtype=torch.int64, device=dev)
     rc = (_lib or load()).w4_kv_plan(
         lens.data_ptr(), None if new_tokens is None else new_tokens.data_ptr(), free_pages.data_ptr(),
         free_pages.numel(), used.data_ptr(), table.data_ptr(), ts[0], B, table.shape[1], page_size, pages, T,
@@ -1003,16 +996,17 @@ def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
     if not 1 <= k <= 0x7FFFFFFF or (groups | top_groups | group_best) > 0x7FFFFFFF:
         raise ValueError(f"k={k}, groups={groups}, top_groups={top_groups}, group_best={group_best}: out of range")
     lib = _lib or load()
-    weights = logits.new_empty((T, k), dtype=torch.float32)
-    ids = logits.new_empty((T, k), dtype=torch.int32)
+    dev = logits.device
+    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     row = torch.empty_like(ids)
-    goff = ids.new_empty(E + 1)
+    goff = torch.empty(E + 1, dtype=torch.int32, device=dev)
     need = 0
     if workspace is None:
         if T > 64:
             need = lib.w4_moe_route_workspace_bytes(T, E)
             if need:
-                workspace = _scratch(need, logits.device, stream)
+                workspace = _scratch(need, dev, stream)
     else:
         need = workspace.numel() * workspace.element_size()
     rc = lib.w4_moe_route(
@@ -1034,7 +1028,7 @@ def w4_moe_gather(x: torch.Tensor, row: torch.Tensor, out=None, stream=None) -> 
     k = row.shape[1] if row.dim() == 2 else 0
     _i32(row, (T, k), "row")
     if out is None:
-        out = x.new_empty((T * k, K))
+        out = torch.empty((T * k, K), dtype=torch.bfloat16, device=x.device)
     else:
         _need(out, torch.bfloat16, (out.shape[0], K), "out")
     if T == 0 or K == 0:
@@ -1059,7 +1053,7 @@ def w4_moe_combine(y: torch.Tensor, row: torch.Tensor, weights: torch.Tensor,
     if shared is not None:
         _need(shared, torch.bfloat16, (T, N), "shared")
     if out is None:
-        out = y.new_empty((T, N))
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=y.device)
     else:
         _need(out, torch.bfloat16, (T, N), "out")
     if T == 0 or N == 0:

@@ -70,7 +70,7 @@ int attn_workspace(AttnArgs* a, size_t need, void* ws, size_t ws_bytes) {
 }
 
 // The scratch of w4_attn_shared, from its first 32-byte boundary on; returns its bytes.
-size_t shared_scratch(AttnShared* s, void* base, int batch, int q_heads, int head_dim, int sms) {
+size_t shared_scratch(AttnShared* s, void* base, int batch, int q_heads, int heads, int head_dim, int sms) {
     char* p = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(base) + 31) & ~(uintptr_t)31);
     char* const p0 = p;
     auto take = [&](size_t bytes) {
@@ -85,6 +85,13 @@ size_t shared_scratch(AttnShared* s, void* base, int batch, int q_heads, int hea
     s->slot_ml = reinterpret_cast<float*>(take(slots * 2 * sizeof(float)));
     s->row_o = reinterpret_cast<float*>(take(rows * head_dim * sizeof(float)));
     s->slot_o = reinterpret_cast<float*>(take(slots * head_dim * sizeof(float)));
+    const size_t own = shared_own_slots(q_heads, heads, head_dim, sms);
+    s->own_share = reinterpret_cast<int*>(take(sizeof(int)));
+    s->own_info = reinterpret_cast<int2*>(take(batch * sizeof(int2)));
+    s->own_row_ml = reinterpret_cast<float*>(take(rows * 2 * sizeof(float)));
+    s->own_slot_ml = reinterpret_cast<float*>(take(own * 2 * sizeof(float)));
+    s->own_row_o = reinterpret_cast<float*>(take(rows * head_dim * sizeof(float)));
+    s->own_slot_o = reinterpret_cast<float*>(take(own * head_dim * sizeof(float)));
     return (size_t)(p - p0) + 32;
 }
 
@@ -236,13 +243,12 @@ size_t w4_attn_shared_scratch_bytes(int batch, int q_heads, int heads, int head_
     if (batch < 0 || q_heads < 1 || heads < 1 || q_heads % heads || head_dim < 1) return 0;
     const int sms = current_sm_count();
     AttnShared sh;
-    return sms < 1 ? 0 : shared_scratch(&sh, nullptr, batch, q_heads, head_dim, sms);
+    return sms < 1 ? 0 : shared_scratch(&sh, nullptr, batch, q_heads, heads, head_dim, sms);
 }
 
 int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
                    const int32_t* group, const int32_t* shared, int groups, uint16_t* out, float* lse, int q_heads,
-                   int max_len, float scale, void* workspace, size_t workspace_bytes, void* scratch,
-                   size_t scratch_bytes, void* stream) {
+                   int max_len, float scale, void* scratch, size_t scratch_bytes, void* stream) {
     AttnArgs a{};
     int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, kv ? kv->batch : 0, q_heads, max_len, scale, 0,
                         0, &a);
@@ -254,13 +260,13 @@ int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
     if (a.q_head == 0 || a.q_tok == 0) return W4_ERR_INVALID_ARG;
     // the lists of units, steps of 128 keys and of 16, are counted in 32 bits
     const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)max_len);
-    if ((cap / 64 + 8) * q_heads * kv->batch > (1LL << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
+    if ((cap / 16 + 8) * q_heads * kv->batch > (1LL << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
     if (!scratch) return W4_ERR_WORKSPACE;
     if (!aligned(scratch, 16)) return W4_ERR_MISALIGNED;
     const int sms = current_sm_count();
-    rc = attn_workspace(&a, attn_decode_ws_bytes(q_heads, kv->heads, kv->head_dim, sms), workspace, workspace_bytes);
-    if (rc) return rc;
-    if (scratch_bytes < shared_scratch(&a.sh, scratch, kv->batch, q_heads, kv->head_dim, sms)) return W4_ERR_WORKSPACE;
+    if (scratch_bytes < shared_scratch(&a.sh, scratch, kv->batch, q_heads, kv->heads, kv->head_dim, sms)) return W4_ERR_WORKSPACE;
+    a.err = device_error_flag();
+    if (!a.err) return W4_ERR_CUDA;
     a.sh.group = group; a.sh.shared = shared; a.sh.groups = groups;
     a.T = kv->batch;
     a.max_q = 1;

@@ -60,7 +60,6 @@ namespace {
 // What starting and joining an item costs, in units: 64 ragged sequences take 55 us
 // with 0, 42 with 1, 41 with 2 and 3; uniform long ones do not depend on it.
 constexpr int kItemUnits = 2;
-constexpr float kLazy = 8.f;            // log2 units the maximum may lag behind
 
 // One CTA per SM; warps and ring depth fill its registers and shared memory.
 template <int D, int NT> struct Shape {
@@ -83,79 +82,19 @@ template <int D, int NT> struct Shape {
     static_assert(smem + 2048 <= 227 * 1024, "a CTA fits the SM's shared memory");
 };
 
-// Transpose of an 8 x 8 matrix of 16-bit values: lane holds (row lane / 4,
-// columns 2 (lane % 4) and + 1).
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
 // The part of an item that a CTA works on, as one of its warps sees it.
 struct Part {
     KeyBlocks kb;           // the sequence's visible 16-key blocks
-    int b, it, len, lo;     // sequence, item of it, clamped length, first key of its own
+    int b, it, len;         // sequence, item of it, clamped length
     int units;              // of each of its items: kItemUnits without keys, then a block per warp each
     int base;               // first unit of the sequence in the list
     int first_unit, end;    // of the item; end of the part (in the list)
-    int len_after, lo_after;    // of the sequence after b (loaded ahead)
+    int len_after;          // length of the sequence after b (loaded ahead)
     int first, n;           // the CTAs that hold parts of the item: the first, how many
     int c0, nb;             // this warp's first block, number of blocks
     int issued;             // blocks whose copies are on their way
     int page;               // page of the next one
 };
-
-// Adds to a row over a sequence's own keys (four columns, with its maximum and sum) the parts
-// of its shared prefix, in the order of the keys; hin: the head's number in its group of q_heads /
-// heads.  What the list of parts says is kept inside the workspace, whatever it holds.
-template <int D>
-__device__ __forceinline__ void add_shared(const AttnArgs& a, int b, int hk, int hin, int d, float4* o, float* m,
-                                           float* l) {
-    const int4 s = __ldg(a.sh.info + b);
-    if (s.z <= kSharedItemUnits) return;                // no shared keys
-    const int g = a.Hq / a.kv.heads, tpt = kSharedRows / 2 / g, share = max(__ldg(a.sh.share), 1), G = (int)gridDim.x;
-    const int u = s.y + hk * s.z, first = min(max((u + kSharedItemUnits) / share, 0), G - 1);
-    const int n = min(max((u + s.z - 1) / share - first + 1, 1), G - first);
-    const int tile = s.w >= tpt ? 1 : 0, r = min(max(tile * (kSharedRows / 2) + (s.w - tile * tpt) * g + hin, 0), kSharedRows - 1);
-    const float *po, *pml;                              // part 0, and from part to part
-    size_t step = 0;
-    if (n == 1) {
-        const size_t row = (size_t)b * a.Hq + hk * g + hin;
-        po = a.sh.row_o + row * D;
-        pml = a.sh.row_ml + row * 2;
-    } else {
-        po = a.sh.slot_o + ((size_t)2 * first * kSharedRows + r) * D;
-        pml = a.sh.slot_ml + ((size_t)2 * first * kSharedRows + r) * 2;
-        step = kSharedRows;                             // slots 2 c + 1 of the first CTA, then 2 c
-    }
-    auto at = [&](int x) { return x == 0 ? step : 2 * x * step; };
-    const float sc = a.scale;
-    constexpr int U = 8;                                // parts whose loads are in flight together
-    for (int x0 = 0; x0 < n; x0 += U) {
-        float2 ml[U];
-        float4 t[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const size_t p = at(min(x0 + i, n - 1));
-            ml[i] = __ldcg(reinterpret_cast<const float2*>(pml + p * 2));
-            t[i] = __ldcg(reinterpret_cast<const float4*>(po + p * D + d));
-        }
-        float mx = *m;
-#pragma unroll
-        for (int i = 0; i < U; ++i) mx = x0 + i < n ? fmaxf(mx, ml[i].x) : mx;
-        const float f0 = *m == mx ? 1.f : ex2_approx((*m - mx) * sc);
-        o->x *= f0; o->y *= f0; o->z *= f0; o->w *= f0;
-        *l *= f0;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (x0 + i >= n) break;
-            const float f = ml[i].x == mx ? 1.f : ex2_approx((ml[i].x - mx) * sc);
-            *l += f * ml[i].y;
-            o->x += f * t[i].x; o->y += f * t[i].y; o->z += f * t[i].z; o->w += f * t[i].w;
-        }
-        *m = mx;
-    }
-}
 
 // A finished head's output row (four columns) and log-sum-exp.
 template <int D>
@@ -166,9 +105,7 @@ __device__ __forceinline__ void put_out(const AttnArgs& a, size_t row, int d, fl
     if (a.lse && d == 0) a.lse[row] = l == 0.f ? kNegInf : (m * a.scale + log2f(l)) * 0.6931471805599453f;
 }
 
-// SHARED: of each sequence the keys behind its shared prefix (none where it has no more), to
-// which the prefix's parts are added.
-template <int D, int NT, bool SHARED>
+template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::threads, 1)
 k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
     using S = Shape<D, NT>;
@@ -195,18 +132,10 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
 
     // ---- this CTA's work (every warp finds it by itself)
     const int G = (int)gridDim.x;
-    auto blocks_of = [&](int len, int lo) {
-        if constexpr (SHARED) {
-            const int b0 = lo / 16;
-            return KeyBlocks{0, b0, len > lo ? (len - 1) / 16 + 1 - b0 : 0};
-        }
-        return key_blocks<16>(len - 1, len - 1, a.window, a.sinks);
-    };
+    auto blocks_of = [&](int len) { return key_blocks<16>(len - 1, len - 1, a.window, a.sinks); };
     auto len_of = [&](int b) { return b < B ? kv_length(a.kv, b, a.max_len, a.err) : 0; };
-    // the first key that is the sequence's own
-    auto lo_of = [&](int b) { return SHARED && b < B ? max(__ldg(&a.sh.info[b].x), 0) : 0; };
     // 0 keys: a unit that writes o = 0
-    auto units_of = [&](int len, int lo) { return max(1, (blocks_of(len, lo).n + W - 1) / W); };
+    auto units_of = [&](int len) { return max(1, (blocks_of(len).n + W - 1) / W); };
     auto warp_scan = [&](int v) {           // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -215,9 +144,9 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         }
         return v;
     };
-    const int len0 = len_of(lane), lo0 = lo_of(lane), real0 = lane < B ? units_of(len0, lo0) : 0;
+    const int len0 = len_of(lane), real0 = lane < B ? units_of(len0) : 0;
     int total = lane < B ? items * (real0 + kItemUnits) : 0;
-    for (int b = lane + 32; b < B; b += 32) total += items * (units_of(len_of(b), lo_of(b)) + kItemUnits);
+    for (int b = lane + 32; b < B; b += 32) total += items * (units_of(len_of(b)) + kItemUnits);
     total = __reduce_add_sync(0xffffffffu, total);
     // consecutive shares of the list
     const int share = (total + G - 1) / G;
@@ -246,19 +175,17 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         cur.b = __ffs(past) - 1;
         u0 = (int)blockIdx.x - __shfl_sync(0xffffffffu, v - mine, cur.b);      // part of the sequence
         cur.len = __shfl_sync(0xffffffffu, len0, cur.b);
-        cur.lo = __shfl_sync(0xffffffffu, lo0, cur.b);
     } else {
         if (u0 >= total) return;
         for (int b0 = 0;; b0 += 32) {
-            const int len = b0 ? len_of(b0 + lane) : len0, lo = b0 ? lo_of(b0 + lane) : lo0;
-            const int n = b0 + lane < B ? items * (units_of(len, lo) + kItemUnits) : 0, v = warp_scan(n);
+            const int len = b0 ? len_of(b0 + lane) : len0;
+            const int n = b0 + lane < B ? items * (units_of(len) + kItemUnits) : 0, v = warp_scan(n);
             const uint32_t past = __ballot_sync(0xffffffffu, cur.base + v > u0);
             if (past) {
                 const int f = __ffs(past) - 1;
                 cur.b = b0 + f;
                 cur.base += __shfl_sync(0xffffffffu, v - n, f);
                 cur.len = __shfl_sync(0xffffffffu, len, f);
-                cur.lo = __shfl_sync(0xffffffffu, lo, f);
                 break;
             }
             cur.base += __shfl_sync(0xffffffffu, v, 31);
@@ -269,9 +196,6 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
     const int lg = 31 - __clz(a.kv.page_size);
     const int ki = lane & 3, kj = lane >> 2, pj = (kj >> 1) + 4 * (kj & 1);
     const float sc = a.scale;
-    // shared-memory offsets of the lane's pieces in a stage
-    const uint32_t k_off = pj * 128 + ((ki ^ pj) << 4);                   // ^ 64: the panel's other half
-    const uint32_t v_off = 16 * D * 2 + ki * 128 + ((pj ^ ki) << 4);      // n odd: ^ 64
 
     auto page_at = [&](const Part& s, int i) {
         return i < s.nb ? page_of(a.kv, s.b, (s.kb(s.c0 + i * W) * 16) >> lg, a.err) : 0;
@@ -299,17 +223,15 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             n.b = s.b + 1;
             n.base = s.end;
             n.len = s.len_after;
-            n.lo = s.lo_after;
-            n.kb = blocks_of(n.len, n.lo);
-            n.units = units_of(n.len, n.lo) + kItemUnits;
+            n.kb = blocks_of(n.len);
+            n.units = units_of(n.len) + kItemUnits;
             n.len_after = len_of(n.b + 1);
-            n.lo_after = lo_of(n.b + 1);
         }
         start(n, s.end);
         return n;
     };
-    cur.kb = blocks_of(cur.len, cur.lo);
-    cur.units = units_of(cur.len, cur.lo) + kItemUnits;
+    cur.kb = blocks_of(cur.len);
+    cur.units = units_of(cur.len) + kItemUnits;
     if (part) {
         // the item's units in n runs equal to one, on CTAs first .. first + n - 1
         const int real = cur.units - kItemUnits;
@@ -323,7 +245,6 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         take(cur, s0, s0 + each + (x < rest ? 1 : 0));
     } else {
         cur.len_after = len_of(cur.b + 1);
-        cur.lo_after = lo_of(cur.b + 1);
         start(cur, u0);
     }
     uint32_t put = 0, got = 0;              // blocks issued and consumed by this warp
@@ -362,8 +283,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         const int hk = cur.it / ngrp, h0 = hk * g + (cur.it - hk * ngrp) * HP;
         const int rows = min(HP, (hk + 1) * g - h0);
         const int p = cur.len - 1;
-        const int lo = cur.lo;
-        auto seen = [&](int j) { return SHARED ? j <= p && j >= lo : key_visible(j, p, a.window, a.sinks); };
+        auto seen = [&](int j) { return key_visible(j, p, a.window, a.sinks); };
 
         // ---- query pieces: head 8 x + lane / 4
         uint4 qf[NT][D / 32];
@@ -390,94 +310,8 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
             if (!ok) break;
             const uint8_t* st = ring + (got % NS) * S::stage_bytes;
             const int j0 = cur.kb(cur.c0 + i * W) * 16;
-            const bool all = j0 + 15 <= p &&
-                             (SHARED ? j0 >= lo : a.window == 0 || p - j0 < a.window || j0 + 16 <= a.sinks);
-            float s[NT][2][4];
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][0][e] = s[x][1][e] = 0.f;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const uint8_t* kp = st + (c >> 1) * 2048 + (k_off ^ ((c & 1) * 64));
-                const uint4 k0 = *reinterpret_cast<const uint4*>(kp), k1 = *reinterpret_cast<const uint4*>(kp + 1024);
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    mma_bf16_16816(s[x][0], k0.x, k1.x, k0.y, k1.y, qf[x][c].x, qf[x][c].y, s[x][0]);
-                    mma_bf16_16816(s[x][1], k0.z, k1.z, k0.w, k1.w, qf[x][c].z, qf[x][c].w, s[x][1]);
-                }
-            }
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[x][0][e] += s[x][1][e];
-            if (!all) {
-#pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!seen(j0 + pj + 8 * (e >> 1))) s[x][0][e] = kNegInf;
-            }
-            bool grow = false;
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) grow |= (fmaxf(s[x][0][e], s[x][0][e + 2]) - m[x][e]) * sc > kLazy;
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = fmaxf(m[x][e], fmaxf(s[x][0][e], s[x][0][e + 2]));
-#pragma unroll
-                        for (int z = 4; z < 32; z <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, z));
-                        // both -inf (nothing seen yet): the factor multiplies zeros
-                        const float f = mx == m[x][e] ? 1.f : ex2_approx((m[x][e] - mx) * sc);
-                        m[x][e] = mx;
-                        off[x][e] = mx == kNegInf ? 0.f : -mx * sc;
-                        l[x][e] *= f;
-#pragma unroll
-                        for (int t = 0; t < D / 16; ++t) { o[x][t][e] *= f; o[x][t][e + 2] *= f; }
-                    }
-            }
-            uint32_t pb[NT][2], pl[NT][2];      // the weights' upper halves, and what they leave
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                float w0[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w0[e] = ex2_approx(fmaf(s[x][0][e], sc, off[x][e & 1]));
-                l[x][0] += w0[0] + w0[2];
-                l[x][1] += w0[1] + w0[3];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float u = w0[2 * h], v = w0[2 * h + 1];
-                    const uint32_t hi = prmt(__float_as_uint(u), __float_as_uint(v), 0x7632);
-                    pb[x][h] = movmatrix_trans(hi);
-                    // the factor keeps the rest of a bf16 weight above zero: 0 * inf is NaN
-                    constexpr float kUp = 1.f + 0x1p-23f;
-                    pl[x][h] = movmatrix_trans(pack_bf16x2(fmaf(u, kUp, -bf16x2_lo(hi)), fmaf(v, kUp, -bf16x2_hi(hi))));
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint4 v[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    v[n] = *reinterpret_cast<const uint4*>(st + c * 2048 + n * 512 + (v_off ^ ((n & 1) * 64)));
-                    if (!all && !seen(j0 + ki + 4 * n)) v[n] = make_uint4(0, 0, 0, 0);
-                }
-                const uint32_t *v0 = &v[0].x, *v1 = &v[1].x, *v2 = &v[2].x, *v3 = &v[3].x;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t a0 = prmt(v0[t], v1[t], 0x5410), a1 = prmt(v0[t], v1[t], 0x7632);
-                    const uint32_t a2 = prmt(v2[t], v3[t], 0x5410), a3 = prmt(v2[t], v3[t], 0x7632);
-#pragma unroll
-                    for (int x = 0; x < NT; ++x) {
-                        mma_bf16_16816(o[x][c * 4 + t], a0, a1, a2, a3, pb[x][0], pb[x][1], o[x][c * 4 + t]);
-                        mma_bf16_16816(o[x][c * 4 + t], a0, a1, a2, a3, pl[x][0], pl[x][1], o[x][c * 4 + t]);
-                    }
-                }
-            }
+            const bool all = j0 + 15 <= p && (a.window == 0 || p - j0 < a.window || j0 + 16 <= a.sinks);
+            attend_block<D, NT>(st, qf, o, m, l, off, sc, j0, all, seen);
             __syncwarp();                   // the stage is read: refill it
             ++got;
             fill();
@@ -561,7 +395,6 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                 v.x += f * t.x; v.y += f * t.y; v.z += f * t.z; v.w += f * t.w;
             }
             if (n == 1) {
-                if (SHARED && cur.len > 0) add_shared<D>(a, cur.b, hk, h0 - hk * g + r, d, &v, &mr, &lr);
                 put_out<D>(a, row0 + r, d, v, mr, lr);
             } else {
                 *reinterpret_cast<float4*>(mine + r * D + d) = v;
@@ -641,9 +474,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
                         const float4 t = *reinterpret_cast<const float4*>(so + (x * HP + r) * D + d);
                         v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
                     }
-                    float mr = s_m[0][r], lr = s_l[0][r];
-                    if (SHARED) add_shared<D>(a, cur.b, hk, h0 - hk * g + r, d, &v, &mr, &lr);
-                    put_out<D>(a, row0 + r, d, v, mr, lr);
+                    put_out<D>(a, row0 + r, d, v, s_m[0][r], s_l[0][r]);
                 }
             }
         }
@@ -656,7 +487,7 @@ k_attn_decode(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ C
         for (; got != put; ++got) mbar_wait_drain(&full[warp][got % NS], (got / NS) & 1, a.err);
 }
 
-template <int D, int NT, bool SHARED>
+template <int D, int NT>
 int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     using S = Shape<D, NT>;
     CUtensorMap tmK, tmV;
@@ -671,7 +502,7 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
         return W4_ERR_CUDA;
     const int grid = sm_count, bytes = (int)S::smem;
     static SmemLimit limit;
-    if (!limit.raise(k_attn_decode<D, NT, SHARED>, bytes)) return W4_ERR_CUDA;
+    if (!limit.raise(k_attn_decode<D, NT>, bytes)) return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(S::threads);
@@ -682,7 +513,7 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_decode<D, NT, SHARED>, tmK, tmV, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, k_attn_decode<D, NT>, tmK, tmV, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
 // Two tiles of 8 heads share the keys and values that one would read twice.
@@ -694,22 +525,10 @@ size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count) {
     return (size_t)sm_count * 2 * 8 * head_tiles(Hq, Hkv) * (D + 2) * sizeof(float);
 }
 
-namespace {
-template <bool SHARED>
-int launch(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-    const int nt = head_tiles(a.Hq, a.kv.heads);
-    if (a.kv.head_dim == 128)
-        return nt == 1 ? go<128, 1, SHARED>(a, sm_count, stream) : go<128, 2, SHARED>(a, sm_count, stream);
-    return nt == 1 ? go<64, 1, SHARED>(a, sm_count, stream) : go<64, 2, SHARED>(a, sm_count, stream);
-}
-}  // namespace
-
 int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-    return launch<false>(a, sm_count, stream);
-}
-
-int launch_attn_shared_own(const AttnArgs& a, int sm_count, cudaStream_t stream) {
-    return launch<true>(a, sm_count, stream);
+    const int nt = head_tiles(a.Hq, a.kv.heads);
+    if (a.kv.head_dim == 128) return nt == 1 ? go<128, 1>(a, sm_count, stream) : go<128, 2>(a, sm_count, stream);
+    return nt == 1 ? go<64, 1>(a, sm_count, stream) : go<64, 2>(a, sm_count, stream);
 }
 
 }  // namespace w4

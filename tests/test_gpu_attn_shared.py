@@ -227,7 +227,7 @@ def test_max_len_bounds_the_prefix(w4):
 
 
 def test_captured_and_replayed(w4):
-    """A graph whose lengths, offsets and queries change; scratch and workspace are the graph's."""
+    """A graph whose lengths, offsets and queries change; the scratch is the graph's."""
     b = Batch([(100, [9, 2]), (64, [1, 1, 5])], 28, 4, 128)
     b.check(w4)
     b.cache.table[3:5, :4] = b.cache.table[2, :4]            # pages that stop being shared below
@@ -256,12 +256,12 @@ def test_two_streams_with_their_own_buffers(w4):
     b = Batch([(3000, [9, 200, 1, 40])], 28, 4, 128)
     want, _ = b.check(w4, rows=[0])
     side = [torch.cuda.Stream() for _ in range(2)]
-    need = w4.w4_attn_decode_workspace_bytes(28, 4, 128)
-    ws = [torch.zeros(need, dtype=torch.uint8, device="cuda") for _ in side]
+    need = w4.w4_attn_shared_scratch_bytes(4, 28, 4, 128)
+    mine = torch.empty(need, dtype=torch.uint8, device="cuda")      # one stream's own, the other's from its calls
     outs = [torch.zeros(4, 28, 128, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
-        w4.w4_attn_shared(*b.args(), out=o, workspace=ws[i % 2], stream=side[i % 2])
+        w4.w4_attn_shared(*b.args(), out=o, scratch=mine if i % 2 else None, stream=side[i % 2])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs) and w4.w4_get_device_error() == 0
 

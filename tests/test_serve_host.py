@@ -116,9 +116,9 @@ def test_plan_refusals(w4):
 
 
 def _shared(lib, kv=None, q=OK16, qt=128 * 28, qh=128, group=OK16, shared=OK16, G=1, out=OK16, lse=None, hq=28, max_len=64,
-            scale=0.1, ws=OK16, wsb=1 << 30, scratch=OK16, sb=1 << 40):
+            scale=0.1, scratch=OK16, sb=1 << 40):
     return lib.w4_attn_shared(kv if kv is not None else _kv(), q, qt, qh, group, shared, G, out, lse, hq, max_len, scale,
-                              ws, wsb, scratch, sb, None)
+                              scratch, sb, None)
 
 
 def test_shared_attention_refusals(w4):
@@ -128,13 +128,13 @@ def test_shared_attention_refusals(w4):
                      (dict(hq=4 * 129), "UNSUPPORTED_SHAPE"), (dict(scale=0.0), "INVALID_ARG"),
                      (dict(max_len=-1), "INVALID_ARG"), (dict(qt=0), "INVALID_ARG"), (dict(qh=0), "INVALID_ARG"),
                      (dict(qt=4), "MISALIGNED"), (dict(q=ODD), "MISALIGNED"), (dict(group=0x10002), "MISALIGNED"),
-                     (dict(shared=0x10002), "MISALIGNED"), (dict(ws=None), "WORKSPACE"), (dict(wsb=16), "WORKSPACE"),
-                     (dict(scratch=None), "WORKSPACE")):
+                     (dict(shared=0x10002), "MISALIGNED"), (dict(scratch=None), "WORKSPACE"),
+                     (dict(scratch=0x10008), "MISALIGNED")):
         assert _shared(lib, **kw) == c["W4_ERR_" + code], kw
     for kw, code in ((dict(k=0), "NULL_PTR"), (dict(ps=48), "UNSUPPORTED_SHAPE"), (dict(d=96), "UNSUPPORTED_SHAPE"),
                      (dict(ks=132), "MISALIGNED"), (dict(maxp=0), "INVALID_ARG")):
         assert _shared(lib, _kv(**kw)) == c["W4_ERR_" + code], kw
-    assert _shared(lib, _kv(batch=0), ws=None, scratch=None) == c["W4_OK"]
+    assert _shared(lib, _kv(batch=0), scratch=None) == c["W4_OK"]
     assert lib.w4_attn_shared_scratch_bytes(4, 30, 4, 128) == 0
     assert struct.calcsize("4Q7q6i") == 112
 
