@@ -92,6 +92,9 @@ struct Ctl {
     // be any number of parts behind: those of one tile do not wait for the other):
     // looking through its slots then adds nothing
     int bad[2];
+    // twins: tile B's m and l, for tile A's warps to add
+    uint64_t mlready;
+    float ml[kTile][2];
 };
 
 // The join of an item's parts, over the space of Q and the ring: rows of o by
@@ -310,17 +313,23 @@ struct Walk {
 
 // Groups of sequences that share their first tokens (w4_attn_shared), one new token a
 // sequence: the same tiles, "tokens" being the sequences of a group, and every row sees the
-// same keys, the shared ones.  An item is a pair of tiles and a key-value head; the items of
-// all groups form one list of units, a step each and kSharedUnits for what starting and
-// finishing an item costs, cut into equal consecutive shares, one per CTA.
-constexpr int kSharedUnits = kSharedItemUnits;
-
-// What the list needs to know of a group.
+// same keys, the shared ones.  An item is a pair of tiles and a key-value head.  The items of all
+// groups form one list of units, two for a step and kSharedItemUnits for what starting and
+// finishing an item costs, cut into equal consecutive shares, one per CTA; a step belongs to the
+// CTA that has its first unit.
+//
+// Where a pair has one tile only, nothing runs while that tile's softmax does.  Heads of 64
+// are bound by that: there tiles A and B are the same rows over every second block of keys, and
+// are added at the end (a twin, a unit a block: 8 sequences behind 65536 tokens, 32 / 8
+// heads, 48.5 -> 40.5 us).  Heads of 128 are not (a block of theirs is 64 KB, 1.5 us of the
+// measured copy rate when all SMs read): 41.0 us for 28 / 4 heads, as twins 44.6.
+__host__ __device__ constexpr bool has_twins(int D) { return D == 64; }
 struct SharedGroup {
     int t0, nq, len;            // first sequence, sequences, shared keys
-    int steps, w, items;        // steps and units of an item, items
+    int steps, two, one;        // steps of an item; items of two tiles and of one
 
-    __device__ __forceinline__ int units() const { return w * items; }
+    __device__ __forceinline__ int w(bool twin) const { return steps * (twin ? 1 : 2) + kSharedItemUnits; }
+    template <int D> __device__ __forceinline__ int units() const { return two * w(false) + one * w(has_twins(D)); }
 };
 __device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int tpt, int i) {
     SharedGroup s{0, 0, 0, 0, 0, 0};
@@ -338,8 +347,9 @@ __device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int tpt, 
     s.nq = o1 - o0;
     s.steps = (s.len + kN - 1) / kN;
     if (s.steps > 0) {
-        s.w = s.steps + kSharedUnits;
-        s.items = (s.nq + 2 * tpt - 1) / (2 * tpt) * a.kv.heads;
+        const int tiles = (s.nq + tpt - 1) / tpt;
+        s.two = tiles / 2 * a.kv.heads;
+        s.one = tiles % 2 * a.kv.heads;
     }
     return s;
 }
@@ -352,44 +362,58 @@ __device__ __forceinline__ int warp_scan_sum(int v) {       // inclusive
     }
     return v;
 }
-// Units of all groups, by a whole warp.
-__device__ __forceinline__ int shared_total(const AttnArgs& a, int tpt) {
-    int v = 0;
-    for (int i = threadIdx.x & 31; i < a.sh.groups; i += 32) v += shared_group(a, tpt, i).units();
+// Units of all groups, by a whole warp, and the lane's group of the first 32.
+template <int D> __device__ __forceinline__ int shared_total(const AttnArgs& a, int tpt, SharedGroup* g0) {
+    const int lane = threadIdx.x & 31;
+    *g0 = shared_group(a, tpt, lane);
+    int v = g0->units<D>();
+    for (int i = lane + 32; i < a.sh.groups; i += 32) v += shared_group(a, tpt, i).units<D>();
     return __reduce_add_sync(0xffffffffu, v);
 }
-__device__ __forceinline__ int shared_share(int total) { return max((total + (int)gridDim.x - 1) / (int)gridDim.x, 1); }
+// At least two units, so that no CTA between an item's first and last is without a step of it.
+__device__ __forceinline__ int shared_share(int total) { return max((total + (int)gridDim.x - 1) / (int)gridDim.x, 2); }
 
 // A CTA's walk through its share, with the names that the kernel knows from Walk.
+template <int D>
 struct SharedWalk {
     int b, hk;                  // the group's first sequence, key-value head
-    int x, n, c0, c1;           // the part: number x of n, steps c0 .. c1 - 1
+    int n, x, c0, c1;           // the part: number x of n, steps c0 .. c1 - 1
     int t0, len, i0, n_tok, ntile, p0, p1;
     KeyBlocks kb;
-    int grp, idx, U, u1, share; // group, item of it, the item's first unit, end of the share
+    int grp, idx, U, w, u1, share;  // group, item of it, the item's first unit and units, end of the share
     SharedGroup g;
 
+    __device__ __forceinline__ bool twin() const { return has_twins(D) && ntile == 1; }
     __device__ __forceinline__ bool begin(const AttnArgs& a, int tpt) {
-        const int lane = threadIdx.x & 31, total = shared_total(a, tpt);
+        const int lane = threadIdx.x & 31;
+        SharedGroup mine;
+        const int total = shared_total<D>(a, tpt, &mine);
         share = shared_share(total);
         const int u0 = share * (int)blockIdx.x;
         u1 = min(u0 + share, total);
         if (u0 >= u1) return false;
         int base = 0;
         for (int i0 = 0;; i0 += 32) {
-            const int units = shared_group(a, tpt, i0 + lane).units(), v = warp_scan_sum(units);
+            if (i0) mine = shared_group(a, tpt, i0 + lane);
+            const int units = mine.units<D>(), v = warp_scan_sum(units);
             const uint32_t past = __ballot_sync(0xffffffffu, base + v > u0);
             if (past) {
                 const int f = __ffs(past) - 1;
                 grp = i0 + f;
                 base += __shfl_sync(0xffffffffu, v - units, f);
+                g.t0 = __shfl_sync(0xffffffffu, mine.t0, f);
+                g.nq = __shfl_sync(0xffffffffu, mine.nq, f);
+                g.len = __shfl_sync(0xffffffffu, mine.len, f);
+                g.steps = __shfl_sync(0xffffffffu, mine.steps, f);
+                g.two = __shfl_sync(0xffffffffu, mine.two, f);
+                g.one = __shfl_sync(0xffffffffu, mine.one, f);
                 break;
             }
             base += __shfl_sync(0xffffffffu, v, 31);
         }
-        g = shared_group(a, tpt, grp);
-        idx = (u0 - base) / g.w;
-        U = base + idx * g.w;
+        const int at = u0 - base, w2 = g.w(false), w1 = g.w(has_twins(D)), all_two = g.two * w2;
+        idx = at < all_two ? at / w2 : g.two + (at - all_two) / w1;
+        U = base + min(idx, g.two) * w2 + max(idx - g.two, 0) * w1;
         item(a, tpt);
         return c0 < c1 || next<false>(a, tpt);
     }
@@ -403,22 +427,24 @@ struct SharedWalk {
         ntile = n_tok > tpt ? 2 : 1;
         p0 = p1 = g.len - 1;
         kb = KeyBlocks{0, 0, g.steps};
-        c0 = min(max(u0 - U - kSharedUnits, 0), g.steps);
-        c1 = min(max(u1 - U - kSharedUnits, 0), g.steps);
-        const int first = (U + kSharedUnits) / share;
-        n = (U + g.w - 1) / share - first + 1;
+        w = g.w(twin());
+        const int k = twin() ? 1 : 2;
+        c0 = min((max(u0 - U - kSharedItemUnits, 0) + k - 1) / k, g.steps);
+        c1 = min((max(u1 - U - kSharedItemUnits, 0) + k - 1) / k, g.steps);
+        const int first = (U + kSharedItemUnits) / share;
+        n = (U + w - k) / share - first + 1;
         x = (int)blockIdx.x - first;
     }
     template <bool>
     __device__ __forceinline__ bool next(const AttnArgs& a, int tpt) {
         for (;;) {
-            U += g.w;
+            U += w;
             if (U >= u1) return false;
-            if (++idx == g.items) {
+            if (++idx == g.two + g.one) {
                 do {                                    // units are left, so a group with items follows
                     if (++grp >= a.sh.groups) return false;
                     g = shared_group(a, tpt, grp);
-                } while (g.items == 0);
+                } while (g.two + g.one == 0);
                 idx = 0;
             }
             item(a, tpt);
@@ -429,12 +455,15 @@ struct SharedWalk {
 };
 
 // For the kernel that joins the parts: the list's shares, and each sequence's shared length,
-// first unit (of key-value head 0), units of an item and place in its pair of tiles.  Groups are
-// dealt out over the CTAs; a whole warp.  Sequences outside every group share nothing.
+// first unit (of key-value head 0), units of an item, place in its pair of tiles and, from bit 16
+// on, units of a step.  Groups are dealt out over the CTAs; a whole warp.  Sequences outside
+// every group share nothing.
+template <int D>
 __device__ __noinline__ void publish_shared(const AttnArgs& a, int tpt) {
     const int lane = threadIdx.x & 31, G = (int)gridDim.x;
     if (blockIdx.x == 0) {
-        const int total = shared_total(a, tpt);
+        SharedGroup mine;
+        const int total = shared_total<D>(a, tpt, &mine);
         if (lane == 0) *a.sh.share = shared_share(total);
         const int lo = min(max(__ldg(a.sh.group), 0), a.kv.batch), hi = min(max(__ldg(a.sh.group + a.sh.groups), 0), a.kv.batch);
         for (int b = lane; b < lo; b += 32) a.sh.info[b] = make_int4(0, 0, 0, 0);
@@ -443,16 +472,19 @@ __device__ __noinline__ void publish_shared(const AttnArgs& a, int tpt) {
     int base = 0;
     for (int i0 = 0; i0 < a.sh.groups; i0 += 32) {
         const SharedGroup g = shared_group(a, tpt, i0 + lane);
-        const int v = warp_scan_sum(g.units()), at = base + v - g.units();
+        const int v = warp_scan_sum(g.units<D>()), at = base + v - g.units<D>();
         for (uint32_t m = __ballot_sync(0xffffffffu, g.nq > 0 && (i0 + lane) % G == (int)blockIdx.x); m; m &= m - 1) {
             const int f = __ffs(m) - 1, t0 = __shfl_sync(0xffffffffu, g.t0, f), nq = __shfl_sync(0xffffffffu, g.nq, f);
-            const int w = __shfl_sync(0xffffffffu, g.w, f), len = __shfl_sync(0xffffffffu, g.len, f);
-            const int u = __shfl_sync(0xffffffffu, at, f);
+            const int steps = __shfl_sync(0xffffffffu, g.steps, f), two = __shfl_sync(0xffffffffu, g.two, f);
+            const int len = __shfl_sync(0xffffffffu, g.len, f), u = __shfl_sync(0xffffffffu, at, f);
+            const SharedGroup s{t0, nq, len, steps, two, 0};
             for (int t = lane; t < nq; t += 32) {
                 const int y = t / (2 * tpt), n = __ldg(a.kv.kv_len + t0 + t);
+                const bool twin = has_twins(D) && y * a.kv.heads >= two;
                 // a sequence is unused or has its group's keys
                 if (n != 0 && n < len) atomicCAS(a.err, 0, W4_ERR_PAGE_TABLE);
-                a.sh.info[t0 + t] = make_int4(len, u + y * a.kv.heads * w, w, t - y * 2 * tpt);
+                a.sh.info[t0 + t] = make_int4(len, u + y * a.kv.heads * s.w(false), steps > 0 ? s.w(twin) : 0,
+                                              t - y * 2 * tpt + ((twin ? 1 : 2) << 16));
             }
         }
         base += __shfl_sync(0xffffffffu, v, 31);
@@ -542,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const int tpt) {
     constexpr bool SPLIT = MODE == kSplit;
-    using WalkT = std::conditional_t<MODE == kShared, SharedWalk, Walk>;
+    using WalkT = std::conditional_t<MODE == kShared, SharedWalk<D>, Walk>;
+    constexpr bool TWIN = MODE == kShared && has_twins(D);
     constexpr int NS = slots<D>(), SB = slot_bytes<D>();
     constexpr uint32_t IDESC_S = idesc_bf16_f32(kTile, kN);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(kTile, D) | (1u << 16);      // B is MN major
@@ -569,6 +602,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_init(&ctl->oempty[i], 4);
         }
         mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->mlready, 4);
         ctl->abort = ctl->bad[0] = ctl->bad[1] = 0;
         fence_mbar_init();
     }
@@ -669,14 +703,15 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 };
                 const uint32_t q_lo = desc_k(smem_u32(qs)), k_lo = desc_k(smem_u32(ring));
                 const uint32_t v_lo = desc_mn(smem_u32(ring), kN * 128);
-                auto mma_s = [&](int x, int st) {         // S_x = Q_x K^T
-                    const uint32_t q = q_lo + x * (kTile * D * 2 >> 4), k = k_lo + st * (SB >> 4);
+                auto mma_sq = [&](int x, int qt, int st) {      // S_x = Q_qt K^T
+                    const uint32_t q = q_lo + qt * (kTile * D * 2 >> 4), k = k_lo + st * (SB >> 4);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const uint32_t off = ((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4;
                         mma_ss(s_col(x), q + off, k + off, IDESC_S, i > 0);
                     }
                 };
+                auto mma_s = [&](int x, int st) { mma_sq(x, x, st); };
                 auto mma_o = [&](int x, int st, int half, uint32_t acc) {   // O_x += P_x V over 64 keys
                     const uint32_t v = v_lo + st * (SB >> 4) + half * (4 * 2048 >> 4);
                     const uint32_t p = s_col(x) + 32 * half;
@@ -691,6 +726,49 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                     if (w.kb.n == 0 || w.c0 == w.c1) continue;
                     const int c0 = w.c0, c1 = w.c1;
+                    if constexpr (TWIN) {
+                        if (w.twin()) {                   // tile x: blocks x, x + 2, .. of the part
+                            const int nb = c1 - c0;
+                            ok = wait(&ctl->qfull, part & 1);
+                            auto twin_s = [&](int j) {    // S of block j
+                                const uint32_t ik = 2 * (step + j);
+                                ok = ok && wait(&ctl->full[ik % NS], (ik / NS) & 1);
+                                if (!ok) return;
+                                tc_fence_after();
+                                mma_sq(j & 1, 0, ik % NS);
+                                commit_elected(&ctl->sfull[j & 1]);
+                                commit_elected(&ctl->empty[ik % NS]);
+                                if (j + 1 == nb) commit_elected(&ctl->qempty);
+                            };
+                            twin_s(0);
+                            if (nb > 1) twin_s(1);
+                            for (int j = 0; j < nb && ok; ++j) {
+                                const int x = j & 1;
+                                const uint32_t iv = 2 * (step + j) + 1;
+                                if (j < 2 && no[x] > 0) ok = wait(&ctl->oempty[x], (no[x] - 1) & 1);
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    ok = ok && wait(&ctl->pready[x][half], np[x] & 1) &&
+                                         (half || wait(&ctl->vready[iv % NS], (iv / NS) & 1));
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                    mma_o(x, iv % NS, half, half || j > 1);
+                                }
+                                if (!ok) break;
+                                ++np[x];
+                                commit_elected(&ctl->empty[iv % NS]);
+                                if (j + 2 < nb) {
+                                    twin_s(j + 2);
+                                } else {
+                                    commit_elected(&ctl->ofull[x]);
+                                    ++no[x];
+                                }
+                            }
+                            step += nb;
+                            ++part;
+                            continue;
+                        }
+                    }
                     int end[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) end[x] = x < w.ntile ? min(w.tile_steps(x, tpt), c1) : 0;
@@ -809,7 +887,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 ++part;
             }
             if constexpr (MODE == kShared) {
-                if (warp == 11) publish_shared(a, tpt);
+                if (warp == 11) publish_shared<D>(a, tpt);
             }
         }
         if (joins) { cluster_sync(); cluster_sync(); }
@@ -821,6 +899,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const uint32_t s_addr = s_col(tile) + lane_base, o_addr = o_col(tile) + lane_base;
         const float sc = a.scale;
         uint32_t ns = 0, no = 0, part = 0;                // steps and parts of this tile, parts of the CTA
+        uint32_t no_b = 0, n_ml = 0;                      // twins: tile B's parts as tile A counts them, handed-over m, l
         bool ok = true;
         WalkT w = w0;
         for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
@@ -828,13 +907,16 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int bad_at = (int)part;
             if (w.kb.n > 0 && c0 < c1) ++part;
             // row r of tile x: token i0 + x tpt + r / g, query head hk g + r % g
-            const int tok_in = tile * tpt + rt;
+            bool twin = false;
+            if constexpr (TWIN) twin = w.twin();
+            const int tok_in = (twin ? 0 : tile) * tpt + rt, first = twin ? c0 + tile : c0, stride = twin ? 2 : 1;
             const bool have = rt < tpt && tok_in < w.n_tok;
             const int tok = w.t0 + w.i0 + tok_in, head = w.hk * g + (r - rt * g);
             const int p = !have ? -1 : MODE == kShared ? w.p1 : w.p0 + tok_in;
             const size_t row = (size_t)tok * a.Hq + head;
-            const int n_steps = tile < w.ntile ? w.tile_steps(tile, tpt) : 0, end = min(n_steps, c1);
-            if (!joins && end <= c0) {
+            const int n_steps = tile < w.ntile || twin ? w.tile_steps(tile, tpt) : 0, end = min(n_steps, c1);
+            if (!joins && end <= first) {
+                if constexpr (MODE == kShared) continue;
                 // rows that see no key (where parts are joined, the join writes them)
                 if (c0 == 0 && have) {
                     for (int d = 0; d < D; d += 8) *reinterpret_cast<uint4*>(a.out + row * D + d) = make_uint4(0, 0, 0, 0);
@@ -843,7 +925,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 continue;
             }
             float m = kNegInf, l = 0.f;
-            for (int c = c0; c < end; ++c, ++ns) {
+            for (int c = first; c < end; c += stride, ++ns) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl->sfull[tile], ns & 1, abort, a.err));
                 if (!ok) break;
                 tc_fence_after();
@@ -877,7 +959,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     const float f = mn == m ? 1.f : ex2_approx((m - mn) * sc);
                     m = mn;
                     l *= f;
-                    if (c > c0) {
+                    if (c > first) {
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             uint32_t o[16];
@@ -916,9 +998,42 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 l += x + z;
             }
             // -------------------------------------------------------- O to memory
-            const bool act = c0 < end;
+            const bool act = first < end;
+            float f_own = 1.f, f_b = 0.f;                 // twins: tile A's factors on both tiles' rows
+            bool add_b = false;
+            if constexpr (TWIN) {
+                const bool two = c0 + 1 < c1;             // tile B has blocks
+                if (tile == 0) {
+                    add_b = twin && two;
+                    if (!twin ? w.ntile == 2 : two) ++no_b;
+                } else if (twin) {
+                    // its O stays in TMEM, for tile A's warps, which have the same lanes; once it is
+                    // complete they have read what the part before left
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[1], no & 1, abort, a.err));
+                    if (ok) {
+                        ctl->ml[r][0] = m;
+                        ctl->ml[r][1] = l;
+                    }
+                    ++no;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->mlready);
+                    continue;
+                }
+            }
             if (act) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[tile], no & 1, abort, a.err));
+                if (add_b) {
+                    ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[1], (no_b - 1) & 1, abort, a.err)) &&
+                         __all_sync(0xffffffffu, mbar_wait(&ctl->mlready, n_ml & 1, abort, a.err));
+                    ++n_ml;
+                    if (ok) {
+                        const float mb = ((volatile float*)ctl->ml[r])[0], lb = ((volatile float*)ctl->ml[r])[1], mx = fmaxf(m, mb);
+                        f_own = m == mx ? 1.f : ex2_approx((m - mx) * sc);
+                        f_b = mb == mx ? 1.f : ex2_approx((mb - mx) * sc);
+                        l = l * f_own + lb * f_b;
+                        m = mx;
+                    }
+                }
                 ++no;
                 tc_fence_after();
             }
@@ -951,6 +1066,15 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
                     tmem_ld_32x32b_x32(o_addr + 32 * i, o);
+                    if constexpr (TWIN) {
+                        if (add_b) {
+                            uint32_t ob[32];
+                            tmem_ld_32x32b_x32(o_col(1) + lane_base + 32 * i, ob);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f_own + __uint_as_float(ob[e]) * f_b);
+                        }
+                    }
                     if (!have) continue;
                     if constexpr (MODE == kShared) {
 #pragma unroll
@@ -979,6 +1103,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->oempty[tile]);      // O may be overwritten
+                if (add_b && lane == 0) mbar_arrive(&ctl->oempty[1]);
                 if (MODE != kShared && bad)
                     add_non_finite<D>(a, w.b, w.hk, w.p0, w.p1, w.kb, c0, end, p, a.out + row * D, dst_o);
                 if constexpr (MODE == kShared) {

@@ -298,9 +298,9 @@ __device__ __forceinline__ RowParts row_parts(const AttnArgs& a, int b, int h, i
     const size_t row = (size_t)b * a.Hq + h;
     if (s.z > kSharedItemUnits) {
         const int tpt = kSharedRows / 2 / g, u = s.y + hk * s.z, first = min(max((u + kSharedItemUnits) / share, 0), ctas - 1);
-        r.np = min(max((u + s.z - 1) / share - first + 1, 1), ctas - first);
-        const int tile = s.w >= tpt ? 1 : 0;
-        const int at = min(max(tile * (kSharedRows / 2) + (s.w - tile * tpt) * g + hin, 0), kSharedRows - 1);
+        const int place = s.w & 0xFFFF, tile = place >= tpt ? 1 : 0;
+        r.np = min(max((u + s.z - (s.w >> 16)) / share - first + 1, 1), ctas - first);
+        const int at = min(max(tile * (kSharedRows / 2) + (place - tile * tpt) * g + hin, 0), kSharedRows - 1);
         const size_t slot = (size_t)2 * first * kSharedRows + at;
         r.pstep = r.np == 1 ? 0 : kSharedRows;
         r.po = r.np == 1 ? a.sh.row_o + row * D : a.sh.slot_o + slot * D;

@@ -254,7 +254,7 @@ int launch_rope_append(const RopeArgs& a, cudaStream_t stream);
 // Prefixes shared by groups of sequences, and the results of parts (of the prefixes and of the
 // sequences' own keys) on the way from the kernels that compute them to the one that joins them.
 constexpr int kSharedRows = 256;           // rows of a part
-constexpr int kSharedItemUnits = 2;        // units of an item besides its steps
+constexpr int kSharedItemUnits = 4;        // units of an item besides its steps
 struct AttnShared {
     const int32_t *group, *shared;         // [groups + 1] first sequences, [groups] lengths
     int groups;
