@@ -14,8 +14,9 @@
 // have the order of the scores.  With one, the warp looks at the gaps between the chosen and
 // to what is left.  Where one is closer than the errors allow (and the two experts do not have
 // the same logit and bias, which is a true tie), the chosen and those as close are ranked by
-// their scores in 64 bits, one candidate a lane (settle).  Where groups ranked by scores are
-// that close, the token is chosen again in 64 bits (choose_wide).
+// their scores in 64 bits, one candidate a lane (settle).  So are groups whose ranks are that
+// close, by the experts that can be among their best (settle_groups).  A token with more
+// candidates than lanes is chosen again in 64 bits altogether (choose_wide, 20 times as long).
 //
 // The order is a counting sort without atomics on results: in a run of 32 tokens, bit t of an
 // expert's word says that token t chose it, so a choice's rank among the run's is a population
@@ -36,11 +37,11 @@ constexpr uint32_t kAll = 0xffffffffu;
 // the exponential's 2^-22 of p (a sigmoid: of p (1 - p) <= 1/4) and the quotient's 2^-22, a softmax
 // also by its argument's rounding, 2^-24 |x - m| e^-|x - m| < 2^-25; the roundings of a softmax's
 // sum, over V registers and 5 steps, and of its reciprocal are the same for both.  The
-// rounding of p + bias adds kCloseSum of the score.
+// rounding of p + bias adds kCloseSum of the larger score.
 template <int V> __device__ __forceinline__ float close_of(bool sigmoid) {
     return sigmoid ? 0x1p-20f : 0x1p-20f + (V + 7) * 0x1p-24f;
 }
-constexpr float kCloseSum = 0x1p-22f;
+constexpr float kCloseSum = 0x1p-23f;
 
 // Order-preserving key of a float that is not NaN; 0 is below every key of a value over -inf.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -179,25 +180,29 @@ __device__ __noinline__ int choose_wide(const RouteArgs& a, int t) {
     return id;
 }
 
-// Ranks up to 32 candidates of token t, one a lane (e < 0: none), by their scores in 64 bits; returns
-// the one of rank `lane`.  m: the row's largest logit.
-template <int V>
-__device__ __noinline__ int settle(const RouteArgs& a, int t, int e, float m) {
-    const int lane = threadIdx.x & 31;
-    double s = -kInf, sum = 1.;
+// p of expert e in 64 bits, for the lanes that have one (e >= 0), plus its bias.
+__device__ __forceinline__ double wide_score(const RouteArgs& a, int t, int e, float m) {
+    double sum = 1.;
     if (!a.sigmoid) {
         sum = 0.;
 #pragma unroll 1
-        for (int i = lane; i < a.E; i += 32) {
+        for (int i = threadIdx.x & 31; i < a.E; i += 32) {
             const float x = logit_of(a, t, i);
             sum += x > -kInf ? soft_num((double)x, (double)m) : 0.;
         }
         sum = warp_sum_wide(sum);
     }
-    if (e >= 0) {
-        const double x = logit_of(a, t, e);
-        s = (a.sigmoid ? sigmoid(x) : soft_num(x, (double)m) / sum) + (double)__ldg(a.bias + e);
-    }
+    if (e < 0) return -kInf;
+    const double x = logit_of(a, t, e), p = a.sigmoid ? sigmoid(x) : soft_num(x, (double)m) / sum;
+    return a.bias ? p + (double)__ldg(a.bias + e) : p;
+}
+
+// Ranks up to 32 candidates of token t, one a lane (e < 0: none), by their scores in 64 bits; returns
+// the one of rank `lane`.  m: the row's largest logit.
+template <int V>
+__device__ __noinline__ int settle(const RouteArgs& a, int t, int e, float m) {
+    const int lane = threadIdx.x & 31;
+    const double s = wide_score(a, t, e, m);
     int rank = 0, got = -1;
 #pragma unroll 1
     for (int o = 0; o < 32; ++o) {
@@ -211,6 +216,46 @@ __device__ __noinline__ int settle(const RouteArgs& a, int t, int e, float m) {
         if (w >= 0 && r == lane) got = w;
     }
     return got;
+}
+
+// Whether a lane's group is kept, where the last kept one (lo) and the best of the others (hi) are
+// closer than `tol`.  Groups further than that from the border are what they are; the others are
+// ranked in 64 bits by those of their experts that can be among the best (buf over edge - tol; edge:
+// the group's last score that counts).  False in *fits: more candidates than lanes.
+template <int V>
+__device__ __noinline__ bool settle_groups(const RouteArgs& a, int t, const float* buf, float mine, float edge, float lo,
+                                           float hi, float tol, float m, bool* fits) {
+    const int lane = threadIdx.x & 31, L = a.lanes, g = lane / L;
+    const bool clear = g < a.groups && mine > hi + tol, open = g < a.groups && !clear && mine >= lo - tol;
+    const int left = a.top_groups - __popc(__ballot_sync(kAll, clear && lane == g * L));
+    int n = 0, cand = -1, its = -1;
+#pragma unroll 1
+    for (int i = 0; i < V; ++i) {
+        const int e = i * 32 + lane, ge = e < a.E ? e * a.group_inv >> 20 : 0;
+        const bool o = __shfl_sync(kAll, open, ge * L);
+        const float b = __shfl_sync(kAll, edge, ge * L);
+        const bool in = e < a.E && o && buf[e] > -kInf && !(buf[e] < b - tol);
+        for (uint32_t w = __ballot_sync(kAll, in); w; w &= w - 1, ++n)
+            if (lane == n) cand = i * 32 + __ffs(w) - 1;
+    }
+    *fits = n <= 32;
+    if (n > 32) return false;
+    if (cand >= 0) its = cand * a.group_inv >> 20;
+    const double s = wide_score(a, t, cand, m);
+    double b1 = -kInf, b2 = -kInf;
+#pragma unroll 1
+    for (int o = 0; o < n; ++o) {
+        const double v = __shfl_sync(kAll, s, o);
+        if (__shfl_sync(kAll, its, o) == g) top_two<double>(b1, b2, v, -kInf);
+    }
+    const double rank = group_rank(b1, b2, a.best);
+    int above = 0;
+#pragma unroll 1
+    for (int i = 0; i < a.groups; ++i) {
+        const double v = __shfl_sync(kAll, rank, i * L);
+        if (__shfl_sync(kAll, open, i * L)) above += v > rank || (v == rank && i < g);
+    }
+    return clear || (open && above < left);
 }
 
 // The best two of a lane's values behind (v0, i0) in the order of falling values and rising
@@ -289,6 +334,13 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
             for (int i = 0; i < V; ++i)
                 if (i * 32 + lane < a.E) buf[i * 32 + lane] = x[i];
         }
+        float largest = 0.f;                        // of the scores' sizes
+        if (scored) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) largest = fmaxf(largest, x[i] > -kInf ? fabsf(x[i]) : 0.f);
+            if (!a.bias) largest = 1.f;             // x are logits; scores are at most 1
+            largest = warp_max(largest);
+        }
         __syncwarp();
         // L lanes a group, each with every L-th of its scores; groups start at different ones,
         // so that the lanes' words lie in different banks
@@ -318,10 +370,16 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
             const float v = __shfl_sync(kAll, mine, i * L);
             above += v > mine || (v == mine && i < g);
         }
-        const bool in = g < a.groups && above < a.top_groups;
+        bool in = g < a.groups && above < a.top_groups;
         if (scored) {
             const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
-            again = hi > -kInf && lo - hi <= 2.f * err + 2.f * kCloseSum * (fabsf(lo) + fabsf(hi));
+            // two scores each, their sums' roundings and those of p + bias
+            const float tol = 2.f * err + 4.f * kCloseSum * largest;
+            if (hi > -kInf && lo - hi <= tol) {
+                bool fits = false;
+                if (tol < kInf) in = settle_groups<V>(a, t, buf, mine, a.best == 2 && b2 > -kInf ? b2 : b1, lo, hi, tol, m, &fits);
+                again = !fits;
+            }
         }
         const uint32_t keep = __ballot_sync(kAll, in && sub == 0);
 #pragma unroll
@@ -407,10 +465,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
     *w_out = w;
 }
 
-#ifndef RT
-#define RT 1024
-#endif
-template <int V> constexpr int route_threads() { return V <= 8 ? RT : 512; }
+template <int V> constexpr int route_threads() { return V <= 8 ? 1024 : 512; }
 
 // Inclusive sum over a CTA's threads; part: a word per warp.
 __device__ __forceinline__ int block_scan(int v, int* part) {
@@ -510,21 +565,25 @@ __global__ void __launch_bounds__(route_threads<V>(), 1) k_moe_route(const Route
 }
 
 // The rows of a CTA's tokens: counts of all CTAs and of those before it, then ranks in runs of
-// 128 tokens.
-constexpr int kOrderThreads = 512, kOrderRun = 128;
+// 128 tokens, whose ids are on their way while the counts are added.
+constexpr int kOrderThreads = 512, kOrderRun = 128, kOrderAhead = 2;
+constexpr int kOrderSums = kOrderThreads * 8;    // a thread adds eight experts of every `rows`-th CTA
 __global__ void __launch_bounds__(kOrderThreads, 1) k_moe_order(const RouteArgs a) {
-    extern __shared__ int order_smem[];             // base [pitch], total [pitch], bits [run / 32][pitch]
+    extern __shared__ int order_smem[];             // base [pitch], total [pitch], sums 2 x [rows][pitch] or bits
     __shared__ int part[32];
-    int *base = order_smem, *total = base + a.pitch;
-    uint32_t* bits = reinterpret_cast<uint32_t*>(total + a.pitch);
+    int *base = order_smem, *total = base + a.pitch, *sums = total + a.pitch;
+    uint32_t* bits = reinterpret_cast<uint32_t*>(sums);            // [run / 32][pitch]
     const int tid = threadIdx.x, me = blockIdx.x, B = gridDim.x;
-    for (int i = tid; i < (2 + kOrderRun / 32) * a.pitch; i += blockDim.x) order_smem[i] = 0;
-    __syncthreads();
+    const int cols = a.pitch / 8, rows = min(kOrderThreads / cols, 16), c = tid % cols, r = tid / cols;
     pdl_wait();
     pdl_launch();
+    const int t1 = min(a.T, (me + 1) * a.per);
+    int ahead[kOrderAhead];
     {
-        // a thread: eight experts of every `rows`-th CTA
-        const int cols = a.pitch / 8, rows = blockDim.x / cols, c = tid % cols, r = tid / cols;
+        const int n = min(kOrderRun, t1 - me * a.per) * a.k;
+#pragma unroll
+        for (int i = 0; i < kOrderAhead; ++i)
+            ahead[i] = tid + i * kOrderThreads < n ? a.ids[(size_t)me * a.per * a.k + tid + i * kOrderThreads] : -1;
         int all[8], before[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) all[i] = before[i] = 0;
@@ -534,19 +593,31 @@ __global__ void __launch_bounds__(kOrderThreads, 1) k_moe_order(const RouteArgs 
                 const uint4 u = *reinterpret_cast<const uint4*>(a.hist + (size_t)b * a.pitch + c * 8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int n = (int)((&u.x)[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
-                    all[i] += n;
-                    if (b < me) before[i] += n;
+                    const int v = (int)((&u.x)[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
+                    all[i] += v;
+                    if (b < me) before[i] += v;
                 }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (all[i]) atomicAdd(total + c * 8 + i, all[i]);
-                if (before[i]) atomicAdd(base + c * 8 + i, before[i]);
-            }
+            int4* to = reinterpret_cast<int4*>(sums + r * a.pitch + c * 8);
+            to[0] = make_int4(all[0], all[1], all[2], all[3]);
+            to[1] = make_int4(all[4], all[5], all[6], all[7]);
+            to += kOrderSums / 4;
+            to[0] = make_int4(before[0], before[1], before[2], before[3]);
+            to[1] = make_int4(before[4], before[5], before[6], before[7]);
         }
     }
     __syncthreads();
+    for (int e = tid; e < a.pitch; e += blockDim.x) {
+        int x = 0, y = 0;
+        for (int i = 0; i < rows; ++i) {
+            x += sums[i * a.pitch + e];
+            y += sums[kOrderSums + i * a.pitch + e];
+        }
+        total[e] = x;
+        base[e] = y;
+    }
+    __syncthreads();
+    for (int i = tid; i < kOrderRun / 32 * a.pitch; i += blockDim.x) bits[i] = 0;
     int carry = 0;
     for (int e0 = 0; e0 < a.E; e0 += blockDim.x) {
         const int e = e0 + tid, c = e < a.E ? total[e] : 0, v = block_scan(c, part);
@@ -560,17 +631,24 @@ __global__ void __launch_bounds__(kOrderThreads, 1) k_moe_order(const RouteArgs 
         carry += part[(blockDim.x >> 5) - 1];
         __syncthreads();
     }
-    const int t1 = min(a.T, (me + 1) * a.per);
     for (int t0 = me * a.per; t0 < t1; t0 += kOrderRun) {
         const int n = min(kOrderRun, t1 - t0) * a.k;
         const int32_t* ids = a.ids + (size_t)t0 * a.k;
+        auto id_of = [&](int i) {
+            if (t0 == me * a.per) {
+#pragma unroll
+                for (int j = 0; j < kOrderAhead; ++j)
+                    if (i == tid + j * kOrderThreads) return ahead[j];
+            }
+            return ids[i];
+        };
         for (int i = tid; i < n; i += blockDim.x) {
-            const int t = i / a.k, id = ids[i];
+            const int t = i / a.k, id = id_of(i);
             if (id >= 0) atomicOr(bits + (t >> 5) * a.pitch + id, 1u << (t & 31));
         }
         __syncthreads();
         for (int i = tid; i < n; i += blockDim.x) {
-            const int t = i / a.k, id = ids[i];
+            const int t = i / a.k, id = id_of(i);
             int r = -1;
             if (id >= 0) {
                 r = base[id];
@@ -625,13 +703,16 @@ int go(const RouteArgs& a, cudaStream_t stream) {
     if (!limit[1].raise(k_moe_route<V, false>, most)) return W4_ERR_CUDA;
     const int grid = (a.T + a.per - 1) / a.per;
     if (!launch(k_moe_route<V, false>, grid, threads, smem, stream, a)) return W4_ERR_CUDA;
-    return launch(k_moe_order, grid, kOrderThreads, (2 + kOrderRun / 32) * a.pitch * sizeof(int), stream, a)
+    static SmemLimit order_limit;
+    if (!order_limit.raise(k_moe_order, (2 * W4_MOE_MAX_EXPERTS + 2 * kOrderSums) * (int)sizeof(int))) return W4_ERR_CUDA;
+    return launch(k_moe_order, grid, kOrderThreads, (2 * a.pitch + 2 * kOrderSums) * sizeof(int), stream, a)
                ? W4_OK : W4_ERR_CUDA;
 }
 
 }  // namespace
 
-int route_blocks(int T) { return std::min(kRouteBlocks, (T + 31) / 32); }
+// A few tokens a CTA: warps of one SM slow each other down (1003 tokens in CTAs of 32: 10.4 us).
+int route_blocks(int T) { return std::min(kRouteBlocks, (T + 7) / 8); }
 
 int launch_moe_route(const RouteArgs& a, cudaStream_t stream) {
     return a.E <= 64 ? go<2>(a, stream) : a.E <= 128 ? go<4>(a, stream) : a.E <= 256 ? go<8>(a, stream)
