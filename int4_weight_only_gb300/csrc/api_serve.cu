@@ -49,6 +49,7 @@ int w4_kv_plan(const int32_t* lens, const int32_t* new_tokens, const int32_t* fr
     a.table = table; a.table_stride = table_stride;
     a.n_free = n_free; a.batch = batch; a.max_pages = max_pages; a.page_size = page_size; a.pages = pages; a.T = T;
     a.kv_len = kv_len; a.goff = goff; a.pos = pos; a.slots = slots; a.lens_out = lens_out; a.used_out = used_out;
+    a.in_place = (lens_out && lens_out == lens) || (used_out && used_out == used);
     a.err = device_error_flag();
     if (!a.err) return W4_ERR_CUDA;
     return launch_kv_plan(a, static_cast<cudaStream_t>(stream));

@@ -3,11 +3,11 @@
 //
 // Two sums over the requests, of the new rows and of the new pages, place everything: row t
 // of the step belongs to the last request whose rows begin at or before it, and new page i
-// of the step to the last request whose pages do.  All in one launch of a cluster: each CTA
-// takes the sums for itself, in shared memory (a few thousand requests are a few rounds of
-// a scan), then, once all have read the lengths (outputs may be the inputs), its share
-// of the requests, pages and rows.  Bound by latency: lengths, scan, table or free list,
-// and the barrier between them.
+// of the step to the last request whose pages do.  All in one launch: each CTA takes the sums
+// for itself, in shared memory (a few thousand requests are a few rounds of a scan), then its
+// share of the requests, pages and rows.  Where outputs are the inputs (lengths and pages used
+// in place) the CTAs are a cluster, which meets once all have read them.  Bound by latency:
+// lengths, scan, table or free list.
 #include "block_device.cuh"
 #include "w4_internal.h"
 
@@ -17,6 +17,7 @@ namespace w4 {
 namespace {
 
 constexpr int kThreads = 1024;
+constexpr int kMostCtas = 64;           // each repeats the sums
 constexpr uint32_t kAll = 0xffffffffu;
 
 // Inclusive sum over the CTA, saturating at `most` (so that sums of any inputs stay in range).
@@ -53,6 +54,7 @@ __device__ __forceinline__ int last_at(const int* at, int n, int v) {
     return lo;
 }
 
+template <int R>
 __global__ void __launch_bounds__(kThreads, 1) k_kv_plan(const PlanArgs a) {
     extern __shared__ int smem[];
     __shared__ unsigned part[32];
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_plan(const PlanArgs a) {
     }
     __syncthreads();
     const int G = (int)gridDim.x, me = (int)blockIdx.x * kThreads + tid, all = G * kThreads;
-    if (G > 1) cluster_sync();              // every CTA has read what outputs may overwrite
+    if (a.in_place && G > 1) cluster_sync();            // every CTA has read what outputs overwrite
     const int end = s_end;
     if (me == 0 && a.used_out) *a.used_out = used + end;
     for (int b = me; b <= B; b += all) {
@@ -116,34 +118,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv_plan(const PlanArgs a) {
         const int b = last_at(pages, B + 1, i);
         a.table[b * a.table_stride + ((old[b] + in_page) >> lg) + (i - pages[b])] = __ldg(a.free_pages + used + i);
     }
-    for (int t = me; t < a.T; t += all) {
-        int p = -1;
-        long long slot = -1;
-        if (t < rows[B]) {
-            const int b = last_at(rows, B + 1, t);
-            if (old[b] >= 0) {
-                p = old[b] + t - rows[b];
-                const int held = (old[b] + in_page) >> lg, j = p >> lg;
-                const int page = j < held ? __ldcg(a.table + b * a.table_stride + j)
-                                          : __ldg(a.free_pages + used + pages[b] + (j - held));
-                if ((unsigned)page < (unsigned)a.pages) slot = (long long)page * a.page_size + (p & in_page);
-                else atomicCAS(a.err, 0, W4_ERR_PAGE_TABLE);
-            }
+    // a thread takes R rows in a row, which are of one request more often than not, with one
+    // search; their lookups are in flight together
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.pos) | reinterpret_cast<uintptr_t>(a.slots)) & 15) == 0;
+    for (int t0 = R * me; t0 < a.T; t0 += R * all) {
+        int pos[R], page[R], b = -1;
+        long long slot[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int t = t0 + i;
+            pos[i] = page[i] = -1;
+            if (t >= min(rows[B], a.T)) continue;
+            if (b < 0 || t >= rows[b + 1]) b = last_at(rows, B + 1, t);
+            if (old[b] < 0) continue;
+            const int p = old[b] + t - rows[b], held = (old[b] + in_page) >> lg, j = p >> lg;
+            pos[i] = p;
+            page[i] = j < held ? __ldcg(a.table + b * a.table_stride + j)
+                               : __ldg(a.free_pages + used + pages[b] + (j - held));
         }
-        a.pos[t] = p;
-        a.slots[t] = slot;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            slot[i] = -1;
+            if (pos[i] < 0) continue;
+            if ((unsigned)page[i] < (unsigned)a.pages) slot[i] = (long long)page[i] * a.page_size + (pos[i] & in_page);
+            else atomicCAS(a.err, 0, W4_ERR_PAGE_TABLE);
+        }
+        if (R == 4 && wide && t0 + R <= a.T) {
+            *reinterpret_cast<int4*>(a.pos + t0) = make_int4(pos[0], pos[1 % R], pos[2 % R], pos[3 % R]);
+            *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1 % R]);
+            *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2 % R], slot[3 % R]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (t0 + i < a.T) {
+                    a.pos[t0 + i] = pos[i];
+                    a.slots[t0 + i] = slot[i];
+                }
+        }
     }
 }
 
 }  // namespace
 
-int launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
-    // eight CTAs at most, the portable size of a cluster; one has room for 1024 requests or rows
-    int ctas = 1;
-    while (ctas < 8 && ctas * kThreads < std::max(a.T, a.batch)) ctas *= 2;
+template <int R>
+static int go(const PlanArgs& a, int ctas, cudaStream_t stream) {
     const size_t smem = (size_t)(3 * a.batch + 2) * sizeof(int);
     static SmemLimit limit;
-    if (!limit.raise(k_kv_plan, (3 * W4_KV_PLAN_MAX_BATCH + 2) * (int)sizeof(int))) return W4_ERR_CUDA;
+    if (!limit.raise(k_kv_plan<R>, (3 * W4_KV_PLAN_MAX_BATCH + 2) * (int)sizeof(int))) return W4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
@@ -156,8 +177,22 @@ int launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
     attr[1].val.clusterDim.x = (unsigned)ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_kv_plan, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+    cfg.numAttrs = a.in_place && ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_kv_plan<R>, a) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+int launch_kv_plan(const PlanArgs& a, cudaStream_t stream) {
+    // A CTA has a row or a request for each thread, four rows where that is more than eight CTAs
+    // (one launch's rows are then prompts', whose neighbours share request and page).  Outputs in
+    // place of inputs need all CTAs in one cluster, eight at most (the portable size).
+    const bool four = a.T > 8 * kThreads;
+    const int want = (std::max(four ? a.T / 4 : a.T, a.batch) + kThreads - 1) / kThreads;
+    int ctas = std::min(std::max(want, 1), kMostCtas);
+    if (a.in_place) {
+        ctas = 1;
+        while (ctas < 8 && ctas < want) ctas *= 2;
+    }
+    return four ? go<4>(a, ctas, stream) : go<1>(a, ctas, stream);
 }
 
 }  // namespace w4

@@ -19,12 +19,17 @@ template <> struct Word<8> { using T = uint4; };
 template <> struct Word<4> { using T = uint2; };
 template <> struct Word<1> { using T = uint16_t; };
 
-// Row j of token t, or -1.
-__device__ __forceinline__ int row_of(const MoveArgs& a, long long i) {
-    const int r = __ldg(a.row + i);
-    if ((unsigned)r < (unsigned)a.R) return r;
-    if (r != -1) atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
-    return -1;
+// Rows j0 .. j0 + 7 of token t, -1 where there is none; `tell` reports the wrong ones.
+constexpr int kRows = 8;
+__device__ __forceinline__ void rows_of(const MoveArgs& a, long long t, int j0, bool tell, int* r) {
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) r[j] = j0 + j < a.k ? __ldg(a.row + t * a.k + j0 + j) : -1;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j)
+        if ((unsigned)r[j] >= (unsigned)a.R) {
+            if (tell && r[j] != -1) atomicCAS(a.err, 0, W4_ERR_GROUP_TOKENS);
+            r[j] = -1;
+        }
 }
 
 template <int N>
@@ -36,18 +41,19 @@ __global__ void __launch_bounds__(256) k_moe_gather(const MoveArgs a) {
     if (c >= words) return;
     const long long t = blockIdx.x;
     const T v = *reinterpret_cast<const T*>(a.x + t * a.stride + (size_t)c * N);
-#pragma unroll 8
-    for (int j = 0; j < a.k; ++j) {
-        const int r = row_of(a, t * a.k + j);
-        if (r >= 0) *reinterpret_cast<T*>(a.out + (size_t)r * a.K + (size_t)c * N) = v;
+    for (int j0 = 0; j0 < a.k; j0 += kRows) {
+        int r[kRows];
+        rows_of(a, t, j0, c == 0, r);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            if (r[j] >= 0) *reinterpret_cast<T*>(a.out + (size_t)r[j] * a.K + (size_t)c * N) = v;
     }
 }
 
-template <int N> __device__ __forceinline__ void add_word(float* acc, const void* p, float w) {
+template <int N> __device__ __forceinline__ void add_word(float* acc, typename Word<N>::T u, float w) {
     if constexpr (N == 1) {
-        acc[0] = fmaf(w, bf16_bits_to_f32(*static_cast<const uint16_t*>(p)), acc[0]);
+        acc[0] = fmaf(w, bf16_bits_to_f32(u), acc[0]);
     } else {
-        const typename Word<N>::T u = *static_cast<const typename Word<N>::T*>(p);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const uint32_t z = (&u.x)[i];
@@ -59,21 +65,33 @@ template <int N> __device__ __forceinline__ void add_word(float* acc, const void
 
 template <int N>
 __global__ void __launch_bounds__(256) k_moe_combine(const MoveArgs a) {
+    using T = typename Word<N>::T;
     pdl_wait();
     pdl_launch();
     const int words = a.K / N, c = blockIdx.y * blockDim.x + threadIdx.x;
     if (c >= words) return;
     const long long t = blockIdx.x;
+    const size_t at = (size_t)t * a.K + (size_t)c * N;
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
-#pragma unroll 8
-    for (int j = 0; j < a.k; ++j) {
-        const int r = row_of(a, t * a.k + j);
-        if (r >= 0) add_word<N>(acc, a.x + (size_t)r * a.K + (size_t)c * N, __ldg(a.weights + t * a.k + j));
+    T own{};
+    if (a.shared) own = *reinterpret_cast<const T*>(a.shared + at);
+    for (int j0 = 0; j0 < a.k; j0 += kRows) {
+        int r[kRows];
+        T u[kRows];
+        float w[kRows];
+        rows_of(a, t, j0, c == 0, r);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            w[j] = r[j] >= 0 ? __ldg(a.weights + t * a.k + j0 + j) : 0.f;
+            u[j] = r[j] >= 0 ? __ldcs(reinterpret_cast<const T*>(a.x + (size_t)r[j] * a.K + (size_t)c * N)) : T{};
+        }
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+            if (r[j] >= 0) add_word<N>(acc, u[j], w[j]);
     }
-    const size_t at = (size_t)t * a.K + (size_t)c * N;
-    if (a.shared) add_word<N>(acc, a.shared + at, 1.f);
+    if (a.shared) add_word<N>(acc, own, 1.f);
     if constexpr (N == 1) {
         a.out[at] = f32_to_bf16_bits(acc[0]);
     } else {

@@ -197,21 +197,20 @@ __device__ __forceinline__ double wide_score(const RouteArgs& a, int t, int e, f
     return a.bias ? p + (double)__ldg(a.bias + e) : p;
 }
 
-// Ranks up to 32 candidates of token t, one a lane (e < 0: none), by their scores in 64 bits; returns
-// the one of rank `lane`.  m: the row's largest logit.
-template <int V>
-__device__ __noinline__ int settle(const RouteArgs& a, int t, int e, float m) {
+// Ranks the n <= 32 candidates of token t, one a lane (e < 0: none), by their scores in 64 bits;
+// returns the one of rank `lane`.  m: the row's largest logit.
+__device__ __noinline__ int settle(const RouteArgs& a, int t, int e, int n, float m) {
     const int lane = threadIdx.x & 31;
     const double s = wide_score(a, t, e, m);
     int rank = 0, got = -1;
 #pragma unroll 1
-    for (int o = 0; o < 32; ++o) {
+    for (int o = 0; o < n; ++o) {
         const double v = __shfl_sync(kAll, s, o);
         const int w = __shfl_sync(kAll, e, o);
         rank += w >= 0 && (v > s || (v == s && w < e));
     }
 #pragma unroll 1
-    for (int o = 0; o < 32; ++o) {
+    for (int o = 0; o < n; ++o) {
         const int w = __shfl_sync(kAll, e, o), r = __shfl_sync(kAll, rank, o);
         if (w >= 0 && r == lane) got = w;
     }
@@ -437,7 +436,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
                 }
                 if (__any_sync(kAll, open)) {
                     if (n > 32) again = true;
-                    else id = settle<V>(a, t, cand, m);
+                    else id = settle(a, t, cand, n, m);
                     if (lane >= a.k) id = -1;
                 }
             }

@@ -333,7 +333,7 @@ struct PlanArgs {
     const int32_t *lens, *fresh, *free_pages, *used;
     int32_t* table;
     long long table_stride;
-    int n_free, batch, max_pages, page_size, pages, T;
+    int n_free, batch, max_pages, page_size, pages, T, in_place;
     int32_t *kv_len, *goff, *pos, *lens_out, *used_out;
     int64_t* slots;
     int* err;
