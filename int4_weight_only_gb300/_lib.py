@@ -907,11 +907,13 @@ def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         at = mine = _alloc(max(need, 16), s)
     else:
         at, need = scratch.data_ptr(), scratch.numel() * scratch.element_size()
-    rc = lib.w4_attn_shared(
-        kv, q.data_ptr(), qs[0], qs[1], group.data_ptr(), shared.data_ptr(), G, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), Hq, max_len, D ** -0.5 if scale is None else scale, at, need, s)
-    if mine is not None:
-        _free(mine)
+    try:
+        rc = lib.w4_attn_shared(
+            kv, q.data_ptr(), qs[0], qs[1], group.data_ptr(), shared.data_ptr(), G, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), Hq, max_len, D ** -0.5 if scale is None else scale, at, need, s)
+    finally:
+        if mine is not None:
+            _free(mine)
     if rc:
         raise W4Error("w4_attn_shared", rc)
     return out
@@ -1014,12 +1016,14 @@ def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
         need = lib.w4_moe_route_workspace_bytes(T, E)
         if need:
             at = mine = _alloc(need, s)
-    rc = lib.w4_moe_route(
-        logits.data_ptr(), half, ls[0], None if bias is None else bias.data_ptr(),
-        None if count is None else count.data_ptr(), T, E, k, MOE_SCORES[score], groups, top_groups, group_best,
-        1 if renorm else 0, scale, weights.data_ptr(), ids.data_ptr(), row.data_ptr(), goff.data_ptr(), at, need, s)
-    if mine is not None:
-        _free(mine)
+    try:
+        rc = lib.w4_moe_route(
+            logits.data_ptr(), half, ls[0], None if bias is None else bias.data_ptr(),
+            None if count is None else count.data_ptr(), T, E, k, MOE_SCORES[score], groups, top_groups, group_best,
+            1 if renorm else 0, scale, weights.data_ptr(), ids.data_ptr(), row.data_ptr(), goff.data_ptr(), at, need, s)
+    finally:
+        if mine is not None:
+            _free(mine)
     if rc:
         raise W4Error("w4_moe_route", rc)
     return weights, ids, row, goff

@@ -120,10 +120,21 @@ def test_groups_of_every_kind(w4):
     Batch([(16 + 7 * (i % 9), [1 + i % 3] * (1 + i % 2)) for i in range(70)], 4, 2, 64, before=1, after=1).check(w4)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [140, 900])
 @pytest.mark.parametrize("B", [1, 17, 18, 19, 36, 37, 40, 120])
-def test_tiles(w4, B):
-    """18 sequences of 7 heads fill a tile; sequences of every place in a pair of tiles."""
-    Batch([(140, [1 + b % 4 for b in range(B)])], 7, 1, 128, seed=B).check(w4)
+def test_tiles(w4, B, n, D):
+    """18 sequences of 7 heads fill a tile; sequences of every place in a pair of tiles, pairs and lone tiles."""
+    Batch([(n, [1 + b % 4 for b in range(B)])], 7, 1, D, seed=B).check(w4)
+
+
+@pytest.mark.parametrize("blocks", list(range(1, 10)))
+def test_lone_tiles_over_few_blocks(w4, blocks):
+    """Items of 64-wide heads with one tile take every second block in turn: parts of one block, of odd and
+    even numbers of them, one item after the other in a CTA (more items than CTAs)."""
+    Batch([(128 * blocks - 7, [2, 1])] * 3, 4, 2, 64, 64, seed=blocks).check(w4)
+    b = Batch([(128 * (1 + (i + blocks) % 5), [1]) for i in range(90)], 4, 4, 64, 64, seed=blocks)
+    b.check(w4, rows=range(0, 90, 7))
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,n", [(28, 4, 128, 9000), (8, 1, 64, 30000), (16, 16, 64, 3000)])

@@ -71,7 +71,7 @@ def test_decode_steps(w4, B, ps):
     plan(w4, lens, [r.randrange(2) for _ in range(B)], perm(B + 9), 0, 5, ps, B + 9, B + 2, seed=B, inplace=True, wide=3)
 
 
-@pytest.mark.parametrize("B,most,T_more", [(1, 1, 0), (1, 70000, 5), (3, 5000, 0), (40, 300, 1000), (97, 900, 1),
+@pytest.mark.parametrize("B,most,T_more", [(1, 1, 0), (1, 70000, 5), (2, 40000, 3), (3, 5000, 0), (40, 300, 1000), (97, 900, 1),
                                            (1500, 40, 3)])
 @pytest.mark.parametrize("ps", [16, 128])
 def test_prompts(w4, B, most, T_more, ps):
