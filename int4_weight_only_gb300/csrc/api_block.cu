@@ -249,7 +249,7 @@ size_t w4_attn_shared_scratch_bytes(int batch, int q_heads, int heads, int head_
 int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride, long long q_head_stride,
                    const int32_t* group, const int32_t* shared, int groups, uint16_t* out, float* lse, int q_heads,
                    int max_len, float scale, void* scratch, size_t scratch_bytes, void* stream) {
-    AttnArgs a{};
+    SharedArgs a{};
     int rc = check_attn(kv, q, q_token_stride, q_head_stride, out, lse, kv ? kv->batch : 0, q_heads, max_len, scale, 0,
                         0, &a);
     if (rc) return rc;

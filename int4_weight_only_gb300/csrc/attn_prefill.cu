@@ -92,7 +92,9 @@ struct Ctl {
     // be any number of parts behind: those of one tile do not wait for the other):
     // looking through its slots then adds nothing
     int bad[2];
-    // twins: tile B's m and l, for tile A's warps to add
+};
+// Twins: tile B's m and l, for tile A's warps to add.
+struct TwinCtl : Ctl {
     uint64_t mlready;
     float ml[kTile][2];
 };
@@ -102,8 +104,8 @@ struct Ctl {
 // different banks; then m and l of the same rows.
 template <int D> __host__ __device__ constexpr int join_row() { return D + 4; }
 
-template <int D> __host__ __device__ constexpr size_t smem_total() {
-    return 1024 + 2 * kTile * D * 2 + (size_t)slots<D>() * slot_bytes<D>() + sizeof(Ctl);
+template <int D> __host__ __device__ constexpr size_t smem_total(bool shared = false) {
+    return 1024 + 2 * kTile * D * 2 + (size_t)slots<D>() * slot_bytes<D>() + (shared ? sizeof(TwinCtl) : sizeof(Ctl));
 }
 
 // Shared-memory descriptors for the 128-byte swizzled layouts differ only in
@@ -331,7 +333,7 @@ struct SharedGroup {
     __device__ __forceinline__ int w(bool twin) const { return steps * (twin ? 1 : 2) + kSharedItemUnits; }
     template <int D> __device__ __forceinline__ int units() const { return two * w(false) + one * w(has_twins(D)); }
 };
-__device__ __forceinline__ SharedGroup shared_group(const AttnArgs& a, int tpt, int i) {
+__device__ __forceinline__ SharedGroup shared_group(const SharedArgs& a, int tpt, int i) {
     SharedGroup s{0, 0, 0, 0, 0, 0};
     if (i >= a.sh.groups) return s;
     const int o0 = __ldg(a.sh.group + i), o1 = __ldg(a.sh.group + i + 1), n = __ldg(a.sh.shared + i);
@@ -363,7 +365,7 @@ __device__ __forceinline__ int warp_scan_sum(int v) {       // inclusive
     return v;
 }
 // Units of all groups, by a whole warp, and the lane's group of the first 32.
-template <int D> __device__ __forceinline__ int shared_total(const AttnArgs& a, int tpt, SharedGroup* g0) {
+template <int D> __device__ __forceinline__ int shared_total(const SharedArgs& a, int tpt, SharedGroup* g0) {
     const int lane = threadIdx.x & 31;
     *g0 = shared_group(a, tpt, lane);
     int v = g0->units<D>();
@@ -384,7 +386,7 @@ struct SharedWalk {
     SharedGroup g;
 
     __device__ __forceinline__ bool twin() const { return has_twins(D) && ntile == 1; }
-    __device__ __forceinline__ bool begin(const AttnArgs& a, int tpt) {
+    __device__ __forceinline__ bool begin(const SharedArgs& a, int tpt) {
         const int lane = threadIdx.x & 31;
         SharedGroup mine;
         const int total = shared_total<D>(a, tpt, &mine);
@@ -417,7 +419,7 @@ struct SharedWalk {
         item(a, tpt);
         return c0 < c1 || next<false>(a, tpt);
     }
-    __device__ __forceinline__ void item(const AttnArgs& a, int tpt) {
+    __device__ __forceinline__ void item(const SharedArgs& a, int tpt) {
         const int y = idx / a.kv.heads, u0 = share * (int)blockIdx.x;
         hk = idx - y * a.kv.heads;
         b = t0 = g.t0;
@@ -436,7 +438,7 @@ struct SharedWalk {
         x = (int)blockIdx.x - first;
     }
     template <bool>
-    __device__ __forceinline__ bool next(const AttnArgs& a, int tpt) {
+    __device__ __forceinline__ bool next(const SharedArgs& a, int tpt) {
         for (;;) {
             U += w;
             if (U >= u1) return false;
@@ -459,7 +461,7 @@ struct SharedWalk {
 // on, units of a step.  Groups are dealt out over the CTAs; a whole warp.  Sequences outside
 // every group share nothing.
 template <int D>
-__device__ __noinline__ void publish_shared(const AttnArgs& a, int tpt) {
+__device__ __noinline__ void publish_shared(const SharedArgs& a, int tpt) {
     const int lane = threadIdx.x & 31, G = (int)gridDim.x;
     if (blockIdx.x == 0) {
         SharedGroup mine;
@@ -568,11 +570,12 @@ __device__ __noinline__ void take_out(uint8_t* v, int t, int lo, int hi) {
 // Whole items; the CTAs of a cluster share the steps of one item; parts of the items of
 // groups with a shared prefix, to be joined by another kernel.
 enum Mode { kWhole, kSplit, kShared };
+template <Mode MODE> using ArgsOf = std::conditional_t<MODE == kShared, SharedArgs, AttnArgs>;
 
 template <int D, Mode MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, const AttnArgs a, const int tpt) {
+               const __grid_constant__ CUtensorMap tmV, const ArgsOf<MODE> a, const int tpt) {
     constexpr bool SPLIT = MODE == kSplit;
     using WalkT = std::conditional_t<MODE == kShared, SharedWalk<D>, Walk>;
     constexpr bool TWIN = MODE == kShared && has_twins(D);
@@ -583,7 +586,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     uint8_t* base = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     uint8_t* qs = base;                                   // [2][D/64 panels][128 rows][128 B]
     uint8_t* ring = qs + 2 * kTile * D * 2;
-    Ctl* ctl = reinterpret_cast<Ctl*>(ring + NS * SB);
+    using CtlT = std::conditional_t<TWIN, TwinCtl, Ctl>;
+    CtlT* ctl = reinterpret_cast<CtlT*>(ring + NS * SB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -602,7 +606,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_init(&ctl->oempty[i], 4);
         }
         mbar_init(&ctl->drain, 1);
-        mbar_init(&ctl->mlready, 4);
+        if constexpr (TWIN) mbar_init(&ctl->mlready, 4);
         ctl->abort = ctl->bad[0] = ctl->bad[1] = 0;
         fence_mbar_init();
     }
@@ -1022,7 +1026,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             if (act) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[tile], no & 1, abort, a.err));
-                if (add_b) {
+                if constexpr (TWIN) if (add_b) {
                     ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl->ofull[1], (no_b - 1) & 1, abort, a.err)) &&
                          __all_sync(0xffffffffu, mbar_wait(&ctl->mlready, n_ml & 1, abort, a.err));
                     ++n_ml;
@@ -1222,11 +1226,11 @@ int go(const AttnArgs& a, int sm_count, cudaStream_t stream) {
 }
 
 template <int D>
-int go_shared(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+int go_shared(const SharedArgs& a, int sm_count, cudaStream_t stream) {
     const int tpt = kTile / (a.Hq / a.kv.heads);
     CUtensorMap tmQ, tmK, tmV;
     if (!encode_maps<D>(a, tpt, &tmQ, &tmK, &tmV)) return W4_ERR_CUDA;
-    constexpr size_t bytes = smem_total<D>();
+    constexpr size_t bytes = smem_total<D>(true);
     auto kern = k_attn_prefill<D, kShared>;
     static SmemLimit limit;
     if (!limit.raise(kern, (int)bytes)) return W4_ERR_CUDA;
@@ -1247,7 +1251,7 @@ int go_shared(const AttnArgs& a, int sm_count, cudaStream_t stream) {
 
 static_assert(kSharedRows == 2 * kTile, "as the join reads them");
 
-int launch_attn_shared_prefix(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+int launch_attn_shared_prefix(const SharedArgs& a, int sm_count, cudaStream_t stream) {
     return a.kv.head_dim == 128 ? go_shared<128>(a, sm_count, stream) : go_shared<64>(a, sm_count, stream);
 }
 

@@ -47,14 +47,14 @@ template <int D, int NT> struct Shape {
 struct Group {
     int i, end, len;                    // number, end of its sequences, shared keys
 
-    __device__ __forceinline__ void read(const AttnArgs& a) {
+    __device__ __forceinline__ void read(const SharedArgs& a) {
         const long long cap = min((long long)a.kv.max_pages * a.kv.page_size, (long long)a.max_len);
         const bool in = i >= 0 && i < a.sh.groups;
         end = i >= a.sh.groups ? 0x7fffffff : __ldg(a.sh.group + i + 1);
         len = in ? (int)min(max((long long)__ldg(a.sh.shared + i), 0LL), cap) : 0;
     }
     // the last group that begins at or before sequence b: -1 before all of them, `groups` behind
-    __device__ __forceinline__ void find(const AttnArgs& a, int b) {
+    __device__ __forceinline__ void find(const SharedArgs& a, int b) {
         int lo = -1, hi = a.sh.groups;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -64,10 +64,10 @@ struct Group {
         read(a);
         if (b >= end) next(a, b);
     }
-    __device__ __forceinline__ void next(const AttnArgs& a, int b) {
+    __device__ __forceinline__ void next(const SharedArgs& a, int b) {
         while (b >= end && i < a.sh.groups) { ++i; read(a); }
     }
-    __device__ __forceinline__ int at(const AttnArgs& a, int b) {
+    __device__ __forceinline__ int at(const SharedArgs& a, int b) {
         if (b >= end) next(a, b);
         return len;
     }
@@ -84,7 +84,7 @@ struct Part {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::threads, 1)
-k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnArgs a) {
+k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const SharedArgs a) {
     using S = Shape<D, NT>;
     constexpr int W = S::warps, NS = S::stages, HP = S::heads;
     extern __shared__ uint8_t smem_raw[];
@@ -288,7 +288,7 @@ struct RowParts {
 };
 
 template <int D>
-__device__ __forceinline__ RowParts row_parts(const AttnArgs& a, int b, int h, int HP, int workers, int ctas) {
+__device__ __forceinline__ RowParts row_parts(const SharedArgs& a, int b, int h, int HP, int workers, int ctas) {
     RowParts r{};
     const int g = a.Hq / a.kv.heads, hk = h / g, hin = h - hk * g, len = kv_length(a.kv, b, a.max_len, a.err);
     const int4 s = __ldg(a.sh.info + b);
@@ -321,7 +321,7 @@ __device__ __forceinline__ RowParts row_parts(const AttnArgs& a, int b, int h, i
 // WPR warps a row; D / 4 lanes a part.
 constexpr int kJoinThreads = 256;
 template <int D, int WPR>
-__global__ void __launch_bounds__(kJoinThreads) k_shared_join(const AttnArgs a, int HP, int workers, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) k_shared_join(const SharedArgs a, int HP, int workers, int ctas) {
     constexpr int LP = D / 4, PW = 32 / LP, RPC = kJoinThreads / 32 / WPR;       // parts a warp, rows a CTA
     __shared__ float4 s_o[WPR > 1 ? RPC * WPR : 1][LP];
     __shared__ float2 s_ml[WPR > 1 ? RPC * WPR : 1];
@@ -407,7 +407,7 @@ bool launch(const void* kern, long long grid, int threads, size_t smem, void** a
 }
 
 template <int D, int NT>
-int go(AttnArgs a, int sm_count, cudaStream_t stream) {
+int go(SharedArgs a, int sm_count, cudaStream_t stream) {
     using S = Shape<D, NT>;
     CUtensorMap tmK, tmV;
     const uint64_t dims[5] = {64, (uint64_t)a.kv.page_size, D / 64, (uint64_t)a.kv.heads, (uint64_t)a.kv.pages};
@@ -442,7 +442,7 @@ int shared_own_slots(int Hq, int Hkv, int D, int sm_count) {
     return 2 * sm_count * (D == 64 && nt == 1 ? 16 : 8) * 8 * nt;
 }
 
-int launch_attn_shared_own(const AttnArgs& a, int sm_count, cudaStream_t stream) {
+int launch_attn_shared_own(const SharedArgs& a, int sm_count, cudaStream_t stream) {
     const int nt = head_tiles(a.Hq, a.kv.heads);
     if (a.kv.head_dim == 128) return nt == 1 ? go<128, 1>(a, sm_count, stream) : go<128, 2>(a, sm_count, stream);
     return nt == 1 ? go<64, 1>(a, sm_count, stream) : go<64, 2>(a, sm_count, stream);

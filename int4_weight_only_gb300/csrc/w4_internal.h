@@ -251,6 +251,24 @@ struct RopeArgs {
 };
 int launch_rope_append(const RopeArgs& a, cudaStream_t stream);
 
+// Attention over the paged cache (attn_decode.cu, attn_prefill.cu).
+struct AttnArgs {
+    w4_paged_kv kv;
+    const uint16_t* q;
+    long long q_tok, q_head;
+    const int32_t* goff;           // prefill; decode: nullptr
+    uint16_t* out;
+    float* lse;
+    int T, Hq, max_q, max_len;
+    float scale;                   // softmax scale times log2(e)
+    int window, sinks;             // window 0: none
+    int* tickets;                  // decode: arrival counters and partial results
+    float* partial;
+    int* err;
+};
+size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count);   // of partial results
+int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream);
+int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream);
 // Prefixes shared by groups of sequences, and the results of parts (of the prefixes and of the
 // sequences' own keys) on the way from the kernels that compute them to the one that joins them.
 constexpr int kSharedRows = 256;           // rows of a part
@@ -267,30 +285,13 @@ struct AttnShared {
     float *own_row_o, *own_row_ml;         // as above; slots: [2 workers][heads of an item]
     float *own_slot_o, *own_slot_ml;
 };
-
-// Attention over the paged cache (attn_decode.cu, attn_prefill.cu).
-struct AttnArgs {
-    w4_paged_kv kv;
-    const uint16_t* q;
-    long long q_tok, q_head;
-    const int32_t* goff;           // prefill; decode: nullptr
-    uint16_t* out;
-    float* lse;
-    int T, Hq, max_q, max_len;
-    float scale;                   // softmax scale times log2(e)
-    int window, sinks;             // window 0: none
-    int* tickets;                  // decode: arrival counters and partial results
-    float* partial;
-    int* err;
+struct SharedArgs : AttnArgs {
     AttnShared sh;
 };
-size_t attn_decode_ws_bytes(int Hq, int Hkv, int D, int sm_count);   // of partial results
-int launch_attn_decode(const AttnArgs& a, int sm_count, cudaStream_t stream);
-int launch_attn_prefill(const AttnArgs& a, int sm_count, cudaStream_t stream);
 // The shared prefixes' parts, then (attn_shared.cu) every sequence's own keys and the join.
 int shared_own_slots(int Hq, int Hkv, int D, int sm_count);      // rows of own_slot_o
-int launch_attn_shared_prefix(const AttnArgs& a, int sm_count, cudaStream_t stream);
-int launch_attn_shared_own(const AttnArgs& a, int sm_count, cudaStream_t stream);
+int launch_attn_shared_prefix(const SharedArgs& a, int sm_count, cudaStream_t stream);
+int launch_attn_shared_own(const SharedArgs& a, int sm_count, cudaStream_t stream);
 
 
 // ---------------------------------------------------------------- experts
