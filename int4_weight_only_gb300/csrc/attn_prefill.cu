@@ -93,10 +93,13 @@ struct Ctl {
     // looking through its slots then adds nothing
     int bad[2];
 };
-// Twins: tile B's m and l, for tile A's warps to add.
-struct TwinCtl : Ctl {
+template <int D> struct SharedWalk;
+// Shared prefixes: the warps' walks, which are long and hardly read (in registers they cost the
+// softmax's), and of twins tile B's m and l, for tile A's warps to add.
+template <int D> struct SharedCtl : Ctl {
     uint64_t mlready;
     float ml[kTile][2];
+    int walk[kThreads / 32][32];
 };
 
 // The join of an item's parts, over the space of Q and the ring: rows of o by
@@ -105,7 +108,7 @@ struct TwinCtl : Ctl {
 template <int D> __host__ __device__ constexpr int join_row() { return D + 4; }
 
 template <int D> __host__ __device__ constexpr size_t smem_total(bool shared = false) {
-    return 1024 + 2 * kTile * D * 2 + (size_t)slots<D>() * slot_bytes<D>() + (shared ? sizeof(TwinCtl) : sizeof(Ctl));
+    return 1024 + 2 * kTile * D * 2 + (size_t)slots<D>() * slot_bytes<D>() + (shared ? sizeof(SharedCtl<D>) : sizeof(Ctl));
 }
 
 // Shared-memory descriptors for the 128-byte swizzled layouts differ only in
@@ -417,7 +420,7 @@ struct SharedWalk {
         idx = at < all_two ? at / w2 : g.two + (at - all_two) / w1;
         U = base + min(idx, g.two) * w2 + max(idx - g.two, 0) * w1;
         item(a, tpt);
-        return c0 < c1 || next<false>(a, tpt);
+        return c0 < c1 || advance(a, tpt);
     }
     __device__ __forceinline__ void item(const SharedArgs& a, int tpt) {
         const int y = idx / a.kv.heads, u0 = share * (int)blockIdx.x;
@@ -437,8 +440,18 @@ struct SharedWalk {
         n = (U + w - k) / share - first + 1;
         x = (int)blockIdx.x - first;
     }
+    // A walk in shared memory, by a whole warp: lanes all read it before any writes it.
     template <bool>
     __device__ __forceinline__ bool next(const SharedArgs& a, int tpt) {
+        __syncwarp();
+        SharedWalk n = *this;
+        __syncwarp();
+        const bool more = n.advance(a, tpt);
+        *this = n;                                        // every lane the same
+        __syncwarp();
+        return more;
+    }
+    __device__ __forceinline__ bool advance(const SharedArgs& a, int tpt) {
         for (;;) {
             U += w;
             if (U >= u1) return false;
@@ -586,7 +599,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     uint8_t* base = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
     uint8_t* qs = base;                                   // [2][D/64 panels][128 rows][128 B]
     uint8_t* ring = qs + 2 * kTile * D * 2;
-    using CtlT = std::conditional_t<TWIN, TwinCtl, Ctl>;
+    using CtlT = std::conditional_t<MODE == kShared, SharedCtl<D>, Ctl>;
     CtlT* ctl = reinterpret_cast<CtlT*>(ring + NS * SB);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -617,10 +630,20 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 
     // ---- this CTA's work (every thread finds it by itself)
     const int Hkv = a.kv.heads, nc = SPLIT ? (int)cluster_nctas() : 1;
-    WalkT w0;
+    WalkT w_here;
     bool mine;
+    // where a warp's walk lives
+    WalkT* at = &w_here;
     if constexpr (MODE == kShared) {
-        mine = w0.begin(a, tpt);
+        static_assert(sizeof(WalkT) <= sizeof(ctl->walk[0]), "a warp's walk");
+        at = reinterpret_cast<WalkT*>(ctl->walk[warp]);
+    }
+    WalkT& w0 = *at;
+    using WalkRef = std::conditional_t<MODE == kShared, WalkT&, WalkT>;
+    if constexpr (MODE == kShared) {
+        mine = w_here.begin(a, tpt);
+        w0 = w_here;                                      // every lane the same
+        __syncwarp();
     } else if constexpr (SPLIT) {
         mine = w0.pick(a, tpt, (int)blockIdx.x / nc);
         w0.x = (int)cluster_ctarank();
@@ -656,7 +679,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int R = min(a.kv.page_size, kN), npg = kN / R, g = a.Hq / Hkv;
             uint32_t it = 0, part = 0;
             bool ok = true;
-            WalkT w = w0;
+            WalkRef w = w0;
             for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                 if (w.kb.n == 0 || w.c0 == w.c1) continue;
                 const int c0 = w.c0, c1 = w.c1;
@@ -726,7 +749,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 uint32_t step = 0, part = 0;              // steps and parts of this CTA so far
                 uint32_t np[2] = {0, 0}, no[2] = {0, 0};  // steps, parts by tile
                 bool ok = true;
-                WalkT w = w0;
+                WalkRef w = w0;
                 for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                     if (w.kb.n == 0 || w.c0 == w.c1) continue;
                     const int c0 = w.c0, c1 = w.c1;
@@ -842,7 +865,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             // -------------------------------------------------------- V release
             uint32_t step = 0, part = 0;
             bool ok = true;
-            WalkT w = w0;
+            WalkRef w = w0;
             for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
                 if (w.kb.n == 0 || w.c0 == w.c1) continue;
                 const int c0 = w.c0, c1 = w.c1;
@@ -905,7 +928,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint32_t ns = 0, no = 0, part = 0;                // steps and parts of this tile, parts of the CTA
         uint32_t no_b = 0, n_ml = 0;                      // twins: tile B's parts as tile A counts them, handed-over m, l
         bool ok = true;
-        WalkT w = w0;
+        WalkRef w = w0;
         for (bool go = mine; go && ok; go = w.template next<SPLIT>(a, tpt)) {
             const int c0 = w.c0, c1 = w.c1;
             const int bad_at = (int)part;
