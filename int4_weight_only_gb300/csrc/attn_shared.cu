@@ -19,8 +19,7 @@
 // only once all that precedes the call is complete, and it waits for that kernel at its end,
 // so that the join sees both.
 //
-// The join is one row (sequence, head) a warp, or four warps where rows are few and their
-// parts many.  Parts are added in an order that depends on the inputs' shapes alone: the
+// The join is one to eight warps a row (sequence, head).  Parts are added in an order that depends on the inputs' shapes alone: the
 // same inputs give the same bits.
 #include "attn_device.cuh"
 #include "w4_internal.h"
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_shared_join(const SharedArgs a
         const int b = (int)(row / a.Hq);
         const RowParts r = row_parts<D>(a, b, (int)(row - (long long)b * a.Hq), HP, workers, ctas);
         const int n = r.np + r.no;
-        constexpr int U = 4;                            // parts whose loads are in flight together
+        constexpr int U = WPR == 8 || WPR == 2 ? 8 : 4; // parts whose loads are in flight together
         for (int x0 = (warp % WPR) * PW + lane / LP; x0 < n; x0 += WPR * PW * U) {
             float2 ml[U];
             float4 t[U];
@@ -426,11 +425,17 @@ int go(SharedArgs a, int sm_count, cudaStream_t stream) {
     int HP = S::heads, workers = sm_count * S::warps, ctas = sm_count;
     void* join[] = {&a, &HP, &workers, &ctas};
     const long long rows = (long long)a.kv.batch * a.Hq;
-    // one warp a row fills the SMs from 16 rows an SM on
-    const bool many = rows >= 16LL * sm_count;
-    const int per = kJoinThreads / 32 / (many ? 1 : 4);
-    return launch(many ? (const void*)k_shared_join<D, 1> : (const void*)k_shared_join<D, 4>, (rows + per - 1) / per,
-                  kJoinThreads, 0, join, stream) ? W4_OK : W4_ERR_CUDA;
+    // Warps a row: rows are few where their parts are many.  28 / 4 heads of 128, 1, 2, 4, 8
+    // warps: 8 sequences behind 8192 tokens (224 rows) -, 23.8, 22.1, 21.1 us; 32 (896) -, 31.7,
+    // 30.3, 31.5; 64 behind 32768 (1792) -, 56.8, 58.7, 61; 256 (7168) 143.7, 148.7, 152.8, 170.
+    auto with = [&](const void* kern, int warps) {
+        const int per = kJoinThreads / 32 / warps;
+        return launch(kern, (rows + per - 1) / per, kJoinThreads, 0, join, stream) ? W4_OK : W4_ERR_CUDA;
+    };
+    if (rows <= 2LL * sm_count) return with((const void*)k_shared_join<D, 8>, 8);
+    if (rows <= 8LL * sm_count) return with((const void*)k_shared_join<D, 4>, 4);
+    if (rows <= 16LL * sm_count) return with((const void*)k_shared_join<D, 2>, 2);
+    return with((const void*)k_shared_join<D, 1>, 1);
 }
 
 int head_tiles(int Hq, int Hkv) { return Hq / Hkv <= 8 ? 1 : 2; }
