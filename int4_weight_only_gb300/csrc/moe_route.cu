@@ -34,12 +34,14 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr uint32_t kAll = 0xffffffffu;
 
 // How far two scores of a row can be off against each other, over its largest p.  Each is off by
-// the exponential's 2^-22 of p (a sigmoid: of p (1 - p) <= 1/4) and the quotient's 2^-22, a softmax
-// also by its argument's rounding, 2^-24 |x - m| e^-|x - m| < 2^-25; the roundings of a softmax's
-// sum, over V registers and 5 steps, and of its reciprocal are the same for both.  The
-// rounding of p + bias adds kCloseSum of the larger score.
-template <int V> __device__ __forceinline__ float close_of(bool sigmoid) {
-    return sigmoid ? 0x1p-20f : 0x1p-20f + (V + 7) * 0x1p-24f;
+// the exponential's 2^-22 of p (a sigmoid: of p (1 - p) <= 1/4) and the reciprocal's 2^-23.  The
+// exponential's argument is rounded to 2^-23 of its size: times p that is below 2^-24 of the largest
+// p where it is a distance from the largest logit; a sigmoid of a negative logit x is off by
+// 2^-23 |x| of itself, at worst that of the largest.  The roundings of a softmax's sum, over
+// V registers and 5 steps, and of its reciprocal are the same for both.  The rounding of
+// p + bias adds kCloseSum of the larger score.
+template <int V> __device__ __forceinline__ float close_of(bool sigmoid, float m) {
+    return sigmoid ? 0x1.4p-20f + 0x1p-22f * fmaxf(-m, 0.f) : 0x1p-20f + (V + 7) * 0x1p-24f;
 }
 constexpr float kCloseSum = 0x1p-23f;
 
@@ -61,7 +63,7 @@ __device__ __forceinline__ double warp_sum_wide(double v) {
 }
 
 // Logit e of token t: NaN as -inf, -0 as +0 (equal values have equal bits).
-__device__ __forceinline__ float clean(float v) { return v != v ? -kInf : v + 0.f; }
+__device__ __forceinline__ float clean(float v) { return fmaxf(v, -kInf) + 0.f; }
 __device__ __forceinline__ float logit_of(const RouteArgs& a, int t, int e) {
     const long long at = t * a.stride + e;
     return clean(a.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(a.logits)[at])
@@ -84,6 +86,14 @@ template <int V> __device__ __forceinline__ void load_logits(const RouteArgs& a,
 // p of logit x, given the row's largest logit and sum of exponentials over it.
 __device__ __forceinline__ float soft_num(float x, float m) { return m == kInf ? (x == kInf ? 1.f : 0.f) : expf(x - m); }
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
+// The same for comparisons, by the hardware's 2^x (2^-22) and reciprocal (2^-23).
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float fast_sigmoid(float x) { return rcp_approx(1.f + ex2_approx(-kLog2e * x)); }
 __device__ __forceinline__ double soft_num(double x, double m) { return isinf(m) && m > 0 ? (x == m ? 1. : 0.) : exp(x - m); }
 __device__ __forceinline__ double sigmoid(double x) { return 1. / (1. + exp(-x)); }
 
@@ -257,24 +267,30 @@ __device__ __noinline__ bool settle_groups(const RouteArgs& a, int t, const floa
     return clear || (open && above < left);
 }
 
-// The best two of a lane's values behind (v0, i0) in the order of falling values and rising
-// registers.
-template <int V>
-__device__ __forceinline__ void best_two(const float* s, float v0, int i0, float* b1, int* i1, float* b2, int* i2) {
-    *b1 = *b2 = -kInf;
+// Keys of the best two of a lane's values, in the order of falling values and rising registers, 0
+// where there is none; AFTER: of those behind (v0, i0).
+template <int V, bool AFTER>
+__device__ __forceinline__ void best_two(const float* s, float v0, int i0, uint32_t* k1, int* i1, uint32_t* k2, int* i2) {
+    float b1 = -kInf, b2 = -kInf;
     *i1 = *i2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float v = s[i] < v0 || (s[i] == v0 && i > i0) ? s[i] : -kInf;
-        if (v > *b1) { *b2 = *b1; *i2 = *i1; *b1 = v; *i1 = i; }
-        else if (v > *b2) { *b2 = v; *i2 = i; }
+        const float v = !AFTER || s[i] < v0 || (s[i] == v0 && i > i0) ? s[i] : -kInf;
+        const bool first = v > b1, second = v > b2;
+        *i2 = first ? *i1 : second ? i : *i2;
+        b2 = fmaxf(b2, fminf(b1, v));
+        *i1 = first ? i : *i1;
+        b1 = fmaxf(b1, v);
     }
+    *k1 = b1 > -kInf ? key_of(b1) : 0u;
+    *k2 = b2 > -kInf ? key_of(b2) : 0u;
 }
 
 // The experts of token t, whose logits a lane has in x: lane j gets the j-th (or -1) and its
-// weight.  buf: E floats of the warp's own (groups).
+// weight.  buf: E floats of the warp's own (groups); bias: 32 V in shared memory.
 template <int V>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, float* buf, int* id_out, float* w_out) {
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, float* buf, const float* bias, int* id_out,
+                                       float* w_out) {
     const int lane = threadIdx.x & 31;
     const bool two = a.groups > 1 && a.best == 2;   // groups ranked by sums of scores
     const bool scored = a.bias || two;
@@ -293,9 +309,9 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
                 for (int i = 0; i < V; ++i) sum += x[i] == kInf ? 1.f : 0.f;
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum += expf(x[i] - m);
+                for (int i = 0; i < V; ++i) sum += ex2_approx((x[i] - m) * kLog2e);
             }
-            inv = __fdividef(1.f, warp_sum(sum));
+            inv = rcp_approx(warp_sum(sum));
         }
     }
     auto prob = [&](float v) { return a.sigmoid ? sigmoid(v) : soft_num(v, m) * inv; };
@@ -303,23 +319,23 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
     // (s may be x)
     auto scores = [&](float* s) {
         auto put = [&](int i, float p) {
-            if (a.bias) p += __ldg(a.bias + min(i * 32 + lane, a.E - 1));
-            s[i] = x[i] > -kInf && p > -kInf ? p : -kInf;
+            if (a.bias) p += bias[i * 32 + lane];
+            s[i] = x[i] > -kInf ? p : -kInf;
         };
         if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) put(i, sigmoid(x[i]));
+            for (int i = 0; i < V; ++i) put(i, fast_sigmoid(x[i]));
         } else if (fabsf(m) == kInf) {
 #pragma unroll
             for (int i = 0; i < V; ++i) put(i, x[i] == kInf ? inv : 0.f);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) put(i, expf(x[i] - m) * inv);
+            for (int i = 0; i < V; ++i) put(i, ex2_approx((x[i] - m) * kLog2e) * inv);
         }
     };
     // from here x is what experts are chosen by, -inf where they are not offered
     if (a.bias) scores(x);
-    const float err = scored && m > -kInf ? close_of<V>(a.sigmoid) * prob(m) : 0.f;
+    const float err = scored && m > -kInf ? close_of<V>(a.sigmoid, m) * prob(m) : 0.f;
     bool again = false;
     if (a.groups > 1) {
         if (two && !a.bias) {
@@ -387,30 +403,38 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
         __syncwarp();                               // buf is read
     }
     int id = -1;
-    float mine = -kInf;                             // what it was chosen by
     if (!__any_sync(kAll, again)) {
-        float b1, b2, out = kInf;
-        int i1, i2, known = 2, at_out = -1;
-        best_two<V>(x, kInf, -1, &b1, &i1, &b2, &i2);
-        int chosen = 0;
+        uint32_t k1, k2, out = 0, mine_key = 0;     // the lane's best two; its last given; what it holds was chosen by
+        int i1, i2, at_out = -1, chosen = 0;
+        bool second = true;                         // k2 is known
+        best_two<V, false>(x, 0.f, 0, &k1, &i1, &k2, &i2);
         for (; chosen < a.k; ++chosen) {
-            const uint32_t head = b1 > -kInf ? key_of(b1) : 0u, best = __reduce_max_sync(kAll, head);
+            const uint32_t best = __reduce_max_sync(kAll, k1);
             if (best == 0) break;
-            const uint32_t who = __ballot_sync(kAll, head == best);
+            const uint32_t who = __ballot_sync(kAll, k1 == best);
             int from = __ffs(who) - 1;
             if (who & (who - 1)) {                  // equal ones: the lowest expert
-                const uint32_t e = __reduce_min_sync(kAll, head == best ? (uint32_t)(i1 * 32 + lane) : ~0u);
+                const uint32_t e = __reduce_min_sync(kAll, k1 == best ? (uint32_t)(i1 * 32 + lane) : ~0u);
                 from = (int)(e & 31);
             }
             const int e = __shfl_sync(kAll, i1, from) * 32 + from;
-            if (lane == chosen) { id = e; mine = value_of(best); }
-            if (lane == from) { out = b1; at_out = i1; b1 = b2; i1 = i2; --known; }
-            if (__any_sync(kAll, known == 0)) {
-                if (known == 0) { best_two<V>(x, out, at_out, &b1, &i1, &b2, &i2); known = 2; }
+            if (lane == chosen) { id = e; mine_key = best; }
+            bool look = false;
+            if (lane == from) {
+                out = best;
+                at_out = i1;
+                k1 = k2;
+                i1 = i2;
+                look = !second;
+                second = false;
+            }
+            if (__any_sync(kAll, look)) {
+                if (look) { best_two<V, true>(x, value_of(out), at_out, &k1, &i1, &k2, &i2); second = true; }
             }
         }
         if (a.bias && chosen > 0) {
             // each chosen one against the one before, then what is left against the last
+            const float mine = id >= 0 ? value_of(mine_key) : -kInf;
             const float s1 = __shfl_up_sync(kAll, mine, 1), last = __shfl_sync(kAll, mine, chosen - 1);
             const int e1 = __shfl_up_sync(kAll, id, 1), e_last = __shfl_sync(kAll, id, chosen - 1);
             bool close = lane > 0 && id >= 0 && s1 - mine <= err + kCloseSum * fmaxf(fabsf(s1), fabsf(mine));
@@ -456,7 +480,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
             else w = c >= 0.f ? sigmoid(z) : __fdividef(expf(z - c), 1.f + expf(z));
         }
         const float total = warp_sum(w);
-        w = have && total > 0.f ? w / total * a.scale : 0.f;
+        w = have && total > 0.f ? __fdividef(w, total) * a.scale : 0.f;
     } else if (have) {
         w = prob(z) * a.scale;
     }
@@ -495,14 +519,18 @@ __device__ __forceinline__ int block_scan(int v, int* part) {
 template <int V, bool ONE>
 __global__ void __launch_bounds__(route_threads<V>(), 1) k_moe_route(const RouteArgs a) {
     extern __shared__ float group_buf[];
+    __shared__ float bias[V * 32];
     __shared__ uint32_t bits[ONE ? kRouteOne / 32 : 1][V * 32];       // ONE: who chose; else counts
     __shared__ int base[V * 32];
     __shared__ int part[32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
     for (int i = tid; i < (ONE ? kRouteOne / 32 : 1) * V * 32; i += blockDim.x) (&bits[0][0])[i] = 0;
-    __syncthreads();
     pdl_wait();
     pdl_launch();
+    // a bias that is NaN or -inf takes its expert out
+    if (a.bias)
+        for (int e = tid; e < V * 32; e += blockDim.x) bias[e] = e < a.E ? fmaxf(__ldg(a.bias + e), -kInf) : 0.f;
+    __syncthreads();
     const int t0 = ONE ? 0 : (int)blockIdx.x * a.per, t1 = min(a.T, t0 + (ONE ? a.T : a.per));
     const int real = a.count ? min(max(__ldg(a.count), 0), a.T) : a.T;
     float x[V], nx[V];
@@ -514,7 +542,7 @@ __global__ void __launch_bounds__(route_threads<V>(), 1) k_moe_route(const Route
 #pragma unroll
             for (int i = 0; i < V; ++i) x[i] = nx[i];
             if (t + warps < min(t1, real)) load_logits<V>(a, t + warps, nx);
-            choose<V>(a, t, x, group_buf + warp * a.E, &id, &w);
+            choose<V>(a, t, x, group_buf + warp * a.E, bias, &id, &w);
         }
         if (lane < a.k) {
             a.ids[(size_t)t * a.k + lane] = id;
