@@ -678,6 +678,8 @@ W4_API int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_
  *  slots[t]    = its place in the pool, page * page_size + pos % page_size;
  *  rows from goff[batch] to T - 1 get pos = slots = -1.
  *  kv_len, goff and table are what w4_rope_append and the attention calls take.
+ *  (Without offsets those take row b for request b: the rows of such a step are
+ *  pos's and slots' only where every request has one new token.)
  *
  *  lens, new_tokens  [batch] int32.  free_pages  [n_free] int32, page numbers;
  *  used        [1] int32: how many of them are given out already.

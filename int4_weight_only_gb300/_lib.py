@@ -894,7 +894,7 @@ def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     out = _attn_outputs(q, out, lse)
     if B == 0 or Hq == 0:
         return out
-    if max_len > 0x7FFFFFFF:
+    if not -0x80000000 <= max_len <= 0x7FFFFFFF:
         _past_32_bits(max_len=max_len)
     lib = _lib or load()
     key = (B, Hq, pool[1], D, q.get_device())
@@ -950,7 +950,7 @@ def w4_kv_plan(lens: torch.Tensor, new_tokens: Optional[torch.Tensor], free_page
         _i32(lens_out, (B,), "lens_out")
     if used_out is not None:
         _i32(used_out, (1,), "used_out")
-    if T < 0 or (T | pages | page_size) > 0x7FFFFFFF:
+    if min(T, pages, page_size) < 0 or max(T, pages, page_size) > 0x7FFFFFFF:
         raise ValueError(f"T={T}, pages={pages}, page_size={page_size}: out of range")
     dev, i32 = lens.device, torch.int32
     kv_len = torch.empty_like(lens)
@@ -1000,8 +1000,8 @@ def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
         _need(bias, torch.float32, (E,), "bias")
     if count is not None:
         _i32(count, (1,), "count")
-    if not 1 <= k <= 0x7FFFFFFF or (groups | top_groups | group_best) > 0x7FFFFFFF:
-        raise ValueError(f"k={k}, groups={groups}, top_groups={top_groups}, group_best={group_best}: out of range")
+    if not 1 <= k <= E or min(groups, top_groups) < 1 or max(groups, top_groups) > E or group_best not in (1, 2):
+        raise ValueError(f"k={k}, groups={groups}, top_groups={top_groups}, group_best={group_best} of {E} experts")
     lib = _lib or load()
     dev = logits.device
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -1012,8 +1012,10 @@ def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
     need, at, mine = 0, None, None
     if workspace is not None:
         at, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif T > 64:
-        need = lib.w4_moe_route_workspace_bytes(T, E)
+    elif T > 64 and E > 0:
+        need = _scratch_sizes.get(E)                # the most that any number of tokens takes
+        if need is None:
+            need = _scratch_sizes[E] = lib.w4_moe_route_workspace_bytes(1 << 22, E)
         if need:
             at = mine = _alloc(need, s)
     try:

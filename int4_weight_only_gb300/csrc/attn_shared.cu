@@ -150,14 +150,15 @@ k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
     const int ki = lane & 3, kj = lane >> 2, pj = (kj >> 1) + 4 * (kj & 1);
     const float sc = a.scale;
     auto page_at = [&](const Part& s, int i) { return i < s.nb ? page_of(a.kv, s.b, ((s.j0 + i) * 16) >> lg, a.err) : 0; };
-    // the part of sequence s.b's items that starts at unit u
+    // the part of sequence s.b's items that starts at unit u (offsets that decrease can make the list and
+    // this walk differ: the item stays one of the sequence's, and blocks stay inside it)
     auto start = [&](Part& s, int u) {
-        s.it = (u - s.base) / s.units;
+        s.it = min(max(u - s.base, 0) / s.units, items - 1);
         s.U = s.base + s.it * s.units;
         s.end = min(u1, s.U + s.units);
         const int c0 = max(u - s.U - kOwnUnits, 0), c1 = max(s.end - s.U - kOwnUnits, 0);
         s.j0 = s.lo / 16 + c0;
-        s.nb = c1 - c0;
+        s.nb = max(c1 - c0, 0);
         s.issued = 0;
         s.page = page_at(s, 0);
     };

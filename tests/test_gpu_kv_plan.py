@@ -127,8 +127,9 @@ def test_binding_refusals(w4):
         w4.w4_kv_plan(lens, None, free, used, table.t(), 16, 9, 2)
     with pytest.raises(ValueError):
         w4.w4_kv_plan(lens, None, free, used, table, 16, 9, -1)
-    with pytest.raises(ValueError):
-        w4.w4_kv_plan(lens, None, free, used, table, 16, 9, 1 << 32)
+    for pages, T in ((9, 1 << 32), (-(1 << 32) + 9, 2), (9, -(1 << 32) + 2)):
+        with pytest.raises(ValueError):
+            w4.w4_kv_plan(lens, None, free, used, table, 16, pages, T)
     with pytest.raises(ValueError):
         w4.w4_kv_plan(lens, None, free, used, table, 16, 9, 2, lens_out=i32([1]))
     with pytest.raises(w4.W4Error):

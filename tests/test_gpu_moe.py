@@ -195,15 +195,17 @@ def test_route_no_tokens_and_refusals(w4):
     z = torch.zeros(4, 8, device="cuda")
     with pytest.raises(ValueError):
         w4.w4_moe_route(z, 2, score="other")
-    with pytest.raises(ValueError):
-        w4.w4_moe_route(z, 1 << 32)
+    for bad in (dict(k=1 << 32), dict(k=1 << 30), dict(k=9), dict(k=0), dict(k=2, groups=0), dict(k=2, groups=9),
+                dict(k=2, groups=-(1 << 33) + 1), dict(k=2, group_best=3), dict(k=2, top_groups=0)):
+        with pytest.raises(ValueError):
+            w4.w4_moe_route(z, **bad)
     with pytest.raises(TypeError):
         w4.w4_moe_route(z.half(), 2)
     with pytest.raises(TypeError):
         w4.w4_moe_route(z, 2, bias=torch.zeros(8, device="cuda", dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         w4.w4_moe_route(z.t(), 2)
-    for bad in (dict(k=9), dict(k=2, groups=3), dict(k=2, top_groups=2)):
+    for bad in (dict(k=2, groups=3), dict(k=2, top_groups=2), dict(k=3, groups=4)):
         with pytest.raises(w4.W4Error):
             w4.w4_moe_route(z, **bad)
     with pytest.raises(w4.W4Error):
