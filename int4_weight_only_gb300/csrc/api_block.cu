@@ -270,8 +270,10 @@ int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
     a.sh.group = group; a.sh.shared = shared; a.sh.groups = groups;
     a.T = kv->batch;
     a.max_q = 1;
-    rc = launch_attn_shared_prefix(a, sms, static_cast<cudaStream_t>(stream));
-    return rc ? rc : launch_attn_shared_own(a, sms, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    rc = launch_attn_shared_own(a, sms, s);
+    if (rc == W4_OK) rc = launch_attn_shared_prefix(a, sms, s);
+    return rc ? rc : launch_attn_shared_join(a, sms, s);
 }
 
 }  // extern "C"

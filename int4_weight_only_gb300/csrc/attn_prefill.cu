@@ -29,6 +29,9 @@
 // value product where the tensor cores are the scarce part (the output is 0.0022
 // from 64 bits, against 0.0016 of one rounding of the result).
 //
+// The same kernel serves groups of sequences that share their first tokens (w4_attn_shared), with a
+// list of work and results of its own; see SharedGroup.
+//
 // Warp roles (384 threads):
 //   warps 0-3, 4-7  softmax of tile A, B (one row per thread), O to memory
 //   warp 8          TMA: Q of an item, then K and V blocks into a ring of slots
@@ -325,7 +328,7 @@ struct Walk {
 //
 // Where a pair has one tile only, nothing runs while that tile's softmax does.  Heads of 64
 // are bound by that: there tiles A and B are the same rows over every second block of keys, and
-// are added at the end (a twin, a unit a block: 8 sequences behind 65536 tokens, 32 / 8
+// are added at the end (a twin, a unit a block: a call for 8 sequences behind 65536 tokens, 32 / 8
 // heads, 48.5 -> 40.5 us).  Heads of 128 are not (a block of theirs is 64 KB, 1.5 us of the
 // measured copy rate when all SMs read): 41.0 us for 28 / 4 heads, as twins 44.6.
 __host__ __device__ constexpr bool has_twins(int D) { return D == 64; }
@@ -625,7 +628,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
     if (warp == 8 && lane == 0) { tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV); }
     if (warp == 9) { tmem_alloc(&ctl->tmem, 512); tmem_relinquish(); }
-    pdl_wait();
+    // Shared prefixes: the kernel before is the same call's, of the sequences' own keys, which lets this one
+    // start once all that precedes the call is complete, and of which it needs nothing
+    if constexpr (MODE != kShared) pdl_wait();
     pdl_launch();
 
     // ---- this CTA's work (every thread finds it by itself)
@@ -1179,6 +1184,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     }
     __syncthreads();
     if (warp == 9) tmem_dealloc(tmem, 512);
+    if constexpr (MODE == kShared) pdl_wait();            // complete only with the kernel before
 }
 
 // The tensor maps of a launch: Q by tiles of whole tokens, K and V by pages.

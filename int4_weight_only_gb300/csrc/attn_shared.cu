@@ -4,23 +4,28 @@
 //   softmax over the shared and the own keys = parts (m, l, o) over any runs of
 //   them, joined by  m = max m_i,  l = sum e^(m_i - m) l_i,  o = sum e^(m_i - m) o_i
 //
-// Three kernels: the shared keys (attn_prefill.cu: the sequences of a group are the
-// rows of tensor-core tiles, so that a key is read once for all of them), the own keys
-// and the join.  Own keys are many short pieces (a question behind a document), where
-// what counts is latency: k_attn_decode, a CTA's eight warps meeting at every
-// item's end, took 77 us for 256 sequences of 1 to 2000 own keys (125 MB, 18 us of
-// reading).  So here a warp is a worker of its own.  The list of all items' 16-key blocks
+// Three kernels: the own keys, the shared keys (attn_prefill.cu: the sequences of a group are the
+// rows of tensor-core tiles, so that a key is read once for all of them) and the join.  Own keys are many short pieces (a question behind a document), where
+// what counts is latency: in k_attn_decode's form, a CTA's eight warps meeting at every
+// item's end, 256 sequences of 1 to 2000 own keys (125 MB, 18 us of reading) took 77 us with
+// their join.  So here a warp is a worker of its own.  The list of all items' 16-key blocks
 // (and kOwnUnits an item for starting and finishing one) is cut into equal consecutive
 // shares, one per warp; a warp's ring of blocks runs on across the end of an item, it meets no
 // barrier, and writes each part of an item as fp32 rows straight from its registers.
 //
-// The own kernel needs nothing of the one before it, so it begins on SMs that have
-// finished the shared keys while others still work on them: the kernel before lets it start
-// only once all that precedes the call is complete, and it waits for that kernel at its end,
-// so that the join sees both.
+// The own keys come first.  The kernel of the shared keys needs nothing of them, so it begins
+// on SMs that have finished theirs while others still work on them: the first kernel lets it
+// start only once all that precedes the call is complete, and it waits for the first at its end,
+// so that the join sees both.  The join then finds the shared keys' parts, which are more, in L2
+// (64 sequences behind 32768 tokens 55.1 us, the other way round 56.8).
 //
-// The join is one to eight warps a row (sequence, head).  Parts are added in an order that depends on the inputs' shapes alone: the
-// same inputs give the same bits.
+// The join is one to eight warps a row (sequence, head).  Parts are added in an order that
+// depends on the inputs' shapes alone: the same inputs give the same bits.
+//
+// Measured (28 / 4 heads of 128, in a graph, own keys 1 to 2000): 256 sequences behind 32768
+// shared tokens 143 us, of which the shared keys take 105 (1140 TFLOP/s: two tiles' steps of
+// 1.95 us), the own keys about 28 (two thirds of the measured copy rate) and the join 10.
+// 64 behind 32768 55 us, 8 behind 8192 21.5, 4 behind 1024 14 (latency of the three kernels).
 #include "attn_device.cuh"
 #include "w4_internal.h"
 
@@ -98,6 +103,7 @@ k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         s_b[warp] = -1;
         if (warp == 0) { s_abort = 0; tma_prefetch_desc(&tmK); tma_prefetch_desc(&tmV); }
     }
+    pdl_wait();
     pdl_launch();
 
     // ---- the list: a thread takes a run of sequences
@@ -190,6 +196,20 @@ k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         grp.find(a, s_b[warp]);
         sequence(cur, s_b[warp], s_base[warp]);
         start(cur, u0);
+        // query pieces: head 8 x + lane / 4; those of the next part are loaded ahead where registers allow
+        constexpr bool AHEAD = NT == 1;
+        auto load_q = [&](const Part& s, uint4 (&q)[NT][D / 32]) {
+            const int hk = s.it / ngrp, h0 = hk * g + (s.it - hk * ngrp) * HP, rows = min(HP, (hk + 1) * g - h0);
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c)
+                    q[x][c] = 8 * x + kj < rows
+                        ? __ldg(reinterpret_cast<const uint4*>(a.q + s.b * a.q_tok + (h0 + 8 * x + kj) * a.q_head + c * 32 + ki * 8))
+                        : make_uint4(0, 0, 0, 0);
+        };
+        uint4 qn[AHEAD ? NT : 1][D / 32];
+        if constexpr (AHEAD) load_q(cur, qn);
         auto issue = [&](Part& s) {
             if (lane == 0) {
                 uint64_t* bar = &full[warp][put % NS];
@@ -214,18 +234,21 @@ k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
                 }
             };
             fill();
+            if (AHEAD && cur.nb == 0 && more) {
+                if constexpr (AHEAD) load_q(nxt, qn);
+            }
             if (cur.nb > 0) {
                 const int hk = cur.it / ngrp, h0 = hk * g + (cur.it - hk * ngrp) * HP, rows = min(HP, (hk + 1) * g - h0);
                 const int p = cur.len - 1, lo = cur.lo;
                 auto seen = [&](int j) { return j <= p && j >= lo; };
-                uint4 qf[NT][D / 32];                   // query pieces: head 8 x + lane / 4
+                uint4 qf[NT][D / 32];
+                if constexpr (AHEAD) {
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c)
-                        qf[x][c] = 8 * x + kj < rows
-                            ? __ldg(reinterpret_cast<const uint4*>(a.q + cur.b * a.q_tok + (h0 + 8 * x + kj) * a.q_head + c * 32 + ki * 8))
-                            : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < D / 32; ++c) qf[0][c] = qn[0][c];
+                    if (more) load_q(nxt, qn);
+                } else {
+                    load_q(cur, qf);
+                }
                 // o[x][mt][e]: head 8 x + 2 ki + (e & 1), column 64 (mt / 4) + 8 pj + 2 (mt % 4) + (e >> 1)
                 float o[NT][D / 16][4], m[NT][2], l[NT][2], off[NT][2];
 #pragma unroll
@@ -274,7 +297,6 @@ k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CU
         if (!ok && lane == 0)
             for (; got != put; ++got) mbar_wait_drain(&full[warp][got % NS], (got / NS) & 1, a.err);
     }
-    pdl_wait();                         // complete only with the kernel before
 }
 
 // The parts of one row: from the kernel of the shared keys, then of the own keys.  What the lists
@@ -407,7 +429,7 @@ bool launch(const void* kern, long long grid, int threads, size_t smem, void** a
 }
 
 template <int D, int NT>
-int go(SharedArgs a, int sm_count, cudaStream_t stream) {
+int own(SharedArgs a, int sm_count, cudaStream_t stream) {
     using S = Shape<D, NT>;
     CUtensorMap tmK, tmV;
     const uint64_t dims[5] = {64, (uint64_t)a.kv.page_size, D / 64, (uint64_t)a.kv.heads, (uint64_t)a.kv.pages};
@@ -421,17 +443,22 @@ int go(SharedArgs a, int sm_count, cudaStream_t stream) {
         return W4_ERR_CUDA;
     static SmemLimit limit;
     if (!limit.raise(k_shared_own<D, NT>, (int)S::smem)) return W4_ERR_CUDA;
-    void* own[] = {&tmK, &tmV, &a};
-    if (!launch((const void*)k_shared_own<D, NT>, sm_count, S::threads, S::smem, own, stream)) return W4_ERR_CUDA;
+    void* args[] = {&tmK, &tmV, &a};
+    return launch((const void*)k_shared_own<D, NT>, sm_count, S::threads, S::smem, args, stream) ? W4_OK : W4_ERR_CUDA;
+}
+
+template <int D, int NT>
+int join(SharedArgs a, int sm_count, cudaStream_t stream) {
+    using S = Shape<D, NT>;
     int HP = S::heads, workers = sm_count * S::warps, ctas = sm_count;
-    void* join[] = {&a, &HP, &workers, &ctas};
+    void* args[] = {&a, &HP, &workers, &ctas};
     const long long rows = (long long)a.kv.batch * a.Hq;
     // Warps a row: rows are few where their parts are many.  28 / 4 heads of 128, 1, 2, 4, 8
     // warps: 8 sequences behind 8192 tokens (224 rows) -, 23.8, 22.1, 21.1 us; 32 (896) -, 31.7,
     // 30.3, 31.5; 64 behind 32768 (1792) -, 56.8, 58.7, 61; 256 (7168) 143.7, 148.7, 152.8, 170.
     auto with = [&](const void* kern, int warps) {
         const int per = kJoinThreads / 32 / warps;
-        return launch(kern, (rows + per - 1) / per, kJoinThreads, 0, join, stream) ? W4_OK : W4_ERR_CUDA;
+        return launch(kern, (rows + per - 1) / per, kJoinThreads, 0, args, stream) ? W4_OK : W4_ERR_CUDA;
     };
     if (rows <= 2LL * sm_count) return with((const void*)k_shared_join<D, 8>, 8);
     if (rows <= 8LL * sm_count) return with((const void*)k_shared_join<D, 4>, 4);
@@ -448,10 +475,17 @@ int shared_own_slots(int Hq, int Hkv, int D, int sm_count) {
     return 2 * sm_count * (D == 64 && nt == 1 ? 16 : 8) * 8 * nt;
 }
 
+#define W4_BY_SHAPE(f)                                                                                   \
+    (a.kv.head_dim == 128 ? (nt == 1 ? f<128, 1>(a, sm_count, stream) : f<128, 2>(a, sm_count, stream))   \
+                          : (nt == 1 ? f<64, 1>(a, sm_count, stream) : f<64, 2>(a, sm_count, stream)))
 int launch_attn_shared_own(const SharedArgs& a, int sm_count, cudaStream_t stream) {
     const int nt = head_tiles(a.Hq, a.kv.heads);
-    if (a.kv.head_dim == 128) return nt == 1 ? go<128, 1>(a, sm_count, stream) : go<128, 2>(a, sm_count, stream);
-    return nt == 1 ? go<64, 1>(a, sm_count, stream) : go<64, 2>(a, sm_count, stream);
+    return W4_BY_SHAPE(own);
+}
+
+int launch_attn_shared_join(const SharedArgs& a, int sm_count, cudaStream_t stream) {
+    const int nt = head_tiles(a.Hq, a.kv.heads);
+    return W4_BY_SHAPE(join);
 }
 
 }  // namespace w4

@@ -7,7 +7,8 @@
 // for itself, in shared memory (a few thousand requests are a few rounds of a scan), then its
 // share of the requests, pages and rows.  Where outputs are the inputs (lengths and pages used
 // in place) the CTAs are a cluster, which meets once all have read them.  Bound by latency:
-// lengths, scan, table or free list.
+// lengths, scan, table or free list.  Measured in a graph: 256 requests of at most one token
+// 3.7 us; 97 with 118k new tokens 6.0 (a row a thread at a time on a cluster of eight 14.4).
 #include "block_device.cuh"
 #include "w4_internal.h"
 

@@ -5,7 +5,10 @@
 //
 // Both are bound by HBM: a token's row once on one side, k rows on the other.  A thread takes
 // one word of a token's row (16 bytes where rows allow it, else 8 or 2) and all its k
-// counterparts, so that their loads or stores are in flight together.
+// counterparts, eight at a time, so that their loads or stores are in flight together.  Measured
+// in a graph: 8192 tokens of 2048 values to 8 rows each (302 MB) 45.1 us, back 43.3: 0.98 and 1.02
+// of the measured copy rate (one row after the other, back: 53); 333 x 3580, 6 rows and a
+// shared one (8-byte words) 4.6 us; 16 x 2048 1.6.
 #include "block_device.cuh"
 #include "w4_internal.h"
 

@@ -22,6 +22,12 @@
 // expert's word says that token t chose it, so a choice's rank among the run's is a population
 // count.  Up to kRouteOne tokens one CTA does all; above, each CTA leaves its counts by
 // expert, and a second kernel's CTAs add those of all the CTAs (and of those before them).
+//
+// Bound by the instructions of the selection (16384 tokens of 256 experts: issue slots 72 % busy
+// with 32 warps an SM, HBM under 1 %; 770 instructions a token for k = 8, 60 a round before
+// the lanes kept their heads as keys, 50 since; scores and a bias add 225, groups 470).  Measured in
+// a graph: 16384 x 256 22.5 us without a bias, 29.0 with, 36.3 in 8 groups ranked by two
+// scores (17 MB of logits are 2.7 us); 1003 x 60 9.5; 16 x 128 in one CTA 4.3.
 #include "block_device.cuh"
 #include "w4_internal.h"
 

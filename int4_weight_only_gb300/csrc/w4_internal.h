@@ -288,10 +288,12 @@ struct AttnShared {
 struct SharedArgs : AttnArgs {
     AttnShared sh;
 };
-// The shared prefixes' parts, then (attn_shared.cu) every sequence's own keys and the join.
+// In this order: parts over every sequence's own keys (attn_shared.cu), over the shared prefixes
+// (attn_prefill.cu), the join (attn_shared.cu).
 int shared_own_slots(int Hq, int Hkv, int D, int sm_count);      // rows of own_slot_o
 int launch_attn_shared_prefix(const SharedArgs& a, int sm_count, cudaStream_t stream);
 int launch_attn_shared_own(const SharedArgs& a, int sm_count, cudaStream_t stream);
+int launch_attn_shared_join(const SharedArgs& a, int sm_count, cudaStream_t stream);
 
 
 // ---------------------------------------------------------------- experts

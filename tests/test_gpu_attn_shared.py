@@ -219,6 +219,8 @@ def test_the_same_as_attention_without_sharing(w4):
 
 def test_flags(w4):
     b = Batch([(40, [3, 1]), (40, [2])], 4, 2, 64)
+    table = b.cache.table.clone()
+    b.cache.table[b.cache.table >= b.cache.k.shape[0]] = 0   # no other flag than the one looked for
     for name, value, err in (("group", [0, 2, 9], ROWS_ERR), ("group", [0, -1, 3], ROWS_ERR), ("group", [2, 1, 3], ROWS_ERR),
                              ("group", [0, 2, 1 << 30], ROWS_ERR), ("shared_d", [1 << 30, 40], PAGE_ERR),
                              ("shared_d", [-1, 40], PAGE_ERR), ("shared_d", [42, 40], PAGE_ERR)):
@@ -226,6 +228,7 @@ def test_flags(w4):
         setattr(b, name, torch.tensor(value, dtype=torch.int32, device="cuda"))
         b.run(w4, want_err=err)
         setattr(b, name, keep)
+    b.cache.table = table
     b.check(w4)
     b.cache.table[0, 1] = b.cache.k.shape[0]
     b.run(w4, want_err=PAGE_ERR)
