@@ -17,7 +17,7 @@
 // on SMs that have finished theirs while others still work on them: the first kernel lets it
 // start only once all that precedes the call is complete, and it waits for the first at its end,
 // so that the join sees both.  The join then finds the shared keys' parts, which are more, in L2
-// (64 sequences behind 32768 tokens 55.1 us, the other way round 56.8).
+// (64 sequences behind 32768 tokens 55.1 us, in the other order 56.8).
 //
 // The join is one to eight warps a row (sequence, head).  Parts are added in an order that
 // depends on the inputs' shapes alone: the same inputs give the same bits.

@@ -233,6 +233,22 @@ __device__ __noinline__ int settle(const RouteArgs& a, int t, int e, int n, floa
     return got;
 }
 
+// Every expert offered to token t has the same logit and bias (a padded row's, say): all ties are true
+// ones.  m: the largest logit.
+__device__ __noinline__ bool all_alike(const RouteArgs& a, int t, const float* bias, float m) {
+    const int lane = threadIdx.x & 31;
+    float b = -kInf;
+    if (a.bias)
+        for (int e = lane; e < a.E; e += 32) b = fmaxf(b, bias[e]);
+    b = warp_max(b);
+    bool same = true;
+    for (int e = lane; e < a.E; e += 32) {
+        const float x = logit_of(a, t, e);
+        if (x > -kInf && !(a.bias && bias[e] == -kInf)) same &= x == m && (!a.bias || bias[e] == b);
+    }
+    return __all_sync(kAll, same);
+}
+
 // Whether a lane's group is kept, where the last kept one (lo) and the best of the others (hi) are
 // closer than `tol`.  Groups further than that from the border are what they are; the others are
 // ranked in 64 bits by those of their experts that can be among the best (buf over edge - tol; edge:
@@ -245,7 +261,7 @@ __device__ __noinline__ bool settle_groups(const RouteArgs& a, int t, const floa
     const int left = a.top_groups - __popc(__ballot_sync(kAll, clear && lane == g * L));
     int n = 0, cand = -1, its = -1;
 #pragma unroll 1
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V && n <= 32; ++i) {
         const int e = i * 32 + lane, ge = e < a.E ? e * a.group_inv >> 20 : 0;
         const bool o = __shfl_sync(kAll, open, ge * L);
         const float b = __shfl_sync(kAll, edge, ge * L);
@@ -396,7 +412,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
             const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
             // two scores each, their sums' roundings and those of p + bias
             const float tol = 2.f * err + 4.f * kCloseSum * largest;
-            if (hi > -kInf && lo - hi <= tol) {
+            if (hi > -kInf && lo - hi <= tol && !all_alike(a, t, bias, m)) {
                 bool fits = false;
                 if (tol < kInf) in = settle_groups<V>(a, t, buf, mine, a.best == 2 && b2 > -kInf ? b2 : b1, lo, hi, tol, m, &fits);
                 again = !fits;
@@ -456,15 +472,13 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
                 };
                 if (close && same(id, e1)) close = false;
                 bool open = close;
-                int n = chosen, cand = id;
-#pragma unroll 1
-                for (int i = 0; i < V; ++i) {
-                    bool in = left >> i & 1;
-                    if (in && !same(i * 32 + lane, e_last)) open = true;
-                    for (uint32_t b = __ballot_sync(kAll, in); b; b &= b - 1, ++n)
-                        if (lane == n) cand = i * 32 + __ffs(b) - 1;
-                }
+                for (uint32_t b = left; b && !open; b &= b - 1) open = !same((__ffs(b) - 1) * 32 + lane, e_last);
                 if (__any_sync(kAll, open)) {
+                    int n = chosen, cand = id;
+#pragma unroll 1
+                    for (int i = 0; i < V && n <= 32; ++i)
+                        for (uint32_t b = __ballot_sync(kAll, left >> i & 1); b; b &= b - 1, ++n)
+                            if (lane == n) cand = i * 32 + __ffs(b) - 1;
                     if (n > 32) again = true;
                     else id = settle(a, t, cand, n, m);
                     if (lane >= a.k) id = -1;

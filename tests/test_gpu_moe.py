@@ -130,6 +130,28 @@ def test_route_equal_scores_go_to_the_lower_index(w4):
             same(got, SO.route(to64(z), 10, None if b is None else to64(b), score, **rest), to64(z), (kw, score))
 
 
+@pytest.mark.parametrize("E,groups,top,best", [(256, 8, 4, 2), (256, 8, 4, 1), (96, 1, 1, 1), (1024, 32, 7, 2)])
+def test_route_rows_of_one_value(w4, E, groups, top, best):
+    """Padded rows: one logit for all experts; alone, with one bias, with experts taken out, with one that differs by
+    less than fp32 tells apart after the sigmoid, and with two values a group."""
+    g = torch.Generator().manual_seed(E)
+    z = torch.zeros(75, E)
+    z[1::5] = -3.25
+    z[2::5, torch.randperm(E, generator=g)[:E // 3]] = float("-inf")
+    z[3::5, 40] = 2.0 ** -20
+    z[4::5, ::2] = 1.5
+    one = torch.full((E,), 0.375)
+    most = one.clone()
+    most[7] = float("-inf")
+    other = one.clone()
+    other[33] += 2.0 ** -22
+    for b in (None, torch.zeros(E), one, most, other):
+        for score in ("softmax", "sigmoid"):
+            got = guarded_route(w4, z.cuda(), 8, None if b is None else b.cuda(), score, groups, top, best)
+            want = SO.route(to64(z), 8, None if b is None else to64(b), score, groups, top, best)
+            same(got, want, to64(z), f"E {E} groups {groups} best {best} {score}")
+
+
 def test_route_masked_and_infinite_logits(w4):
     inf, nan = float("inf"), float("nan")
     g = torch.Generator().manual_seed(3)
