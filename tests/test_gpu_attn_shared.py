@@ -282,6 +282,20 @@ def test_captured_and_replayed(w4):
     assert w4.w4_get_device_error() == 0
 
 
+def test_pages_past_two_to_the_31_values(w4):
+    """The batch's pages at the end of a pool of 2.2e9 values (4.4 GB each)."""
+    b = Batch([(150, [9, 70]), (64, [3])], 4, 2, 128, 64)
+    want, lse = b.check(w4)
+    c, far = b.cache, 2 ** 31 // (2 * 64 * 128) + 40
+    for name in ("k", "v"):
+        pool = torch.empty(far + getattr(c, name).shape[0], 2, 64, 128, dtype=torch.bfloat16, device="cuda")
+        pool[far:] = getattr(c, name)
+        setattr(c, name, pool)
+    c.table = torch.where(c.table < (1 << 30), c.table + far, c.table)
+    out, l2 = b.run(w4)
+    assert torch.equal(out, want) and torch.equal(l2, lse)
+
+
 def test_two_streams_with_their_own_buffers(w4):
     b = Batch([(3000, [9, 200, 1, 40])], 28, 4, 128)
     want, _ = b.check(w4, rows=[0])

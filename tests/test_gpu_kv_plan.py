@@ -109,6 +109,12 @@ def test_bad_lengths_offsets_and_pages(w4):
     plan(w4, [0, 20], [20, 1], perm(9), 10, 4, 16, 9, 21)
 
 
+def test_slots_past_32_bits(w4):
+    pages = (1 << 31) - 1
+    w = plan(w4, [4000, 0], [200, 4097], [pages - 1, 600000, 1 << 30], 0, 3, 4096, pages, 4297)
+    assert w["slots"].max() > 1 << 42
+
+
 def test_nothing_to_plan(w4):
     plan(w4, [], [], [], 0, 4, 16, 9, 0)
     plan(w4, [], [], [1, 2], 1, 4, 16, 9, 3)

@@ -317,6 +317,20 @@ def test_rows_out_of_range_are_skipped_and_flagged(w4):
         assert (y == 1).all() and w4.w4_get_device_error() == -11
 
 
+def test_rows_past_two_to_the_31_values(w4):
+    """A buffer of 2.4e9 values (4.8 GB): rows at its end."""
+    R, K = 60000, 40000
+    x = torch.randn(3, K, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    out = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    row = torch.tensor([[R - 1, 0], [53700, R - 2], [-1, 53686]], dtype=torch.int32, device="cuda")
+    w4.w4_moe_gather(x, row, out=out)
+    assert torch.equal(out[[R - 1, 0, 53700, R - 2, 53686]], x[[0, 0, 1, 1, 2]])
+    assert int(out.any(1).sum()) == 5
+    back = w4.w4_moe_combine(out, row, torch.tensor([[0.5, 0.25]] * 3, device="cuda"))
+    want = x.float() * torch.tensor([0.75, 0.75, 0.25], device="cuda")[:, None]
+    assert (back.float() - want).abs().le(2.0 ** -8 * want.abs()).all() and w4.w4_get_device_error() == 0
+
+
 def test_move_shapes_without_work(w4):
     row = torch.zeros(0, 3, dtype=torch.int32, device="cuda")
     assert w4.w4_moe_gather(torch.zeros(0, 8, dtype=torch.bfloat16, device="cuda"), row).shape == (0, 8)
