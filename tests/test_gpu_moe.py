@@ -395,3 +395,27 @@ def test_route_to_combine_around_the_grouped_linear(T):
     first = out.clone()
     graph.replay()
     assert torch.equal(out, first) and w4.w4_get_device_error() == 0
+
+
+@pytest.mark.parametrize("T,count,tile", [(20, 13, 4), (20, 0, 16), (300, 211, 64), (300, 1, 256), (300, 300, 16)])
+def test_padding_through_the_grouped_linear(w4, T, count, tile):
+    """Tokens behind `count` have no rows: the grouped linear's offsets end before its rows do, the rows behind stay as
+    they were (NaN), and nothing of them comes back."""
+    E, k, K, N, G = 8, 3, 128, 96, 32
+    g = torch.Generator().manual_seed(T + count)
+    p, s, _ = w4.w4_pack_rtn((torch.randn(E * N, K, generator=g) * 0.05).cuda(), G, True)
+    x = torch.randn(T, K, generator=g).bfloat16().cuda()
+    z = torch.randn(T, E, generator=g).cuda()
+    shared = torch.randn(T, N, generator=g).bfloat16().cuda()
+    w, ids, row, goff = w4.w4_moe_route(z, k, count=torch.tensor([count], dtype=torch.int32, device="cuda"))
+    xs = torch.full((T * k, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.w4_moe_gather(x, row, out=xs)
+    y = torch.full((T * k, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    w4.w4a16_grouped_linear(xs, goff, p, s, None, None, E, N, K, G, tile, y=y)
+    assert goff[-1] == count * k and y[count * k:].isnan().all() and torch.isfinite(y[:count * k].float()).all()
+    out = w4.w4_moe_combine(y, row, w, shared=shared)
+    assert torch.equal(out[count:], shared[count:]) and torch.isfinite(out.float()).all()
+    full = w4.w4_moe_route(z[:count], k) if count else None
+    if full:
+        assert torch.equal(full[1], ids[:count]) and torch.equal(full[2], row[:count]) and torch.equal(full[3], goff)
+    assert w4.w4_get_device_error() == 0
