@@ -296,6 +296,43 @@ def test_pages_past_two_to_the_31_values(w4):
     assert torch.equal(out, want) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("n,own,Hq,Hkv,D", [(700, [30, 300, 1, 9], 28, 4, 128), (3000, [200] * 24, 8, 2, 64), (64, [1, 2], 4, 4, 64)])
+def test_calls_in_a_row_see_what_was_written_just_before(w4, n, own, Hq, Hkv, D):
+    """Every call writes new keys at the end of each sequence (and into the prefix's last page) and reads them at
+    once, without a pause between calls; each result is that of the same call between synchronizes."""
+    import int4_weight_only_gb300 as raw
+    b = Batch([(n, own)], Hq, Hkv, D, 64)
+    c, B, steps = b.cache, len(own), 60
+    g = torch.Generator().manual_seed(n)
+    inv = raw.w4_rope_freqs(D)[0].cuda()
+    qkv = torch.randn(steps, B, Hq + 2 * Hkv, D, generator=g).bfloat16().cuda()
+    table = c.table.clone()
+    table[table >= c.k.shape[0]] = 0
+    first = torch.tensor([n], dtype=torch.int32, device="cuda")
+    k0, v0 = c.k.clone(), c.v.clone()
+
+    def step(i, q):
+        x = qkv[i]
+        raw.w4_rope_append(x[:1, :Hq], x[:1, Hq:Hq + Hkv], x[:1, Hq + Hkv:], c.k, c.v, first, table[:1], inv)   # key n - 1
+        raw.w4_rope_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], c.k, c.v, c.kv_len, table, inv, q_out=q)
+        return raw.w4_attn_shared(q, c.k, c.v, c.kv_len, table, b.group, b.shared_d, max(b.lens))
+    q = torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        c.k.copy_(k0)
+        c.v.copy_(v0)
+        torch.cuda.synchronize()
+        fast = [step(i, q) for i in range(steps)]
+        torch.cuda.synchronize()
+        c.k.copy_(k0)
+        c.v.copy_(v0)
+        for i in range(steps):
+            torch.cuda.synchronize()
+            want = step(i, q)
+            torch.cuda.synchronize()
+            assert torch.equal(fast[i], want), i
+    assert raw.w4_get_device_error() == 0
+
+
 def test_two_streams_with_their_own_buffers(w4):
     b = Batch([(3000, [9, 200, 1, 40])], 28, 4, 128)
     want, _ = b.check(w4, rows=[0])
