@@ -258,9 +258,11 @@ int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_s
     if (!aligned(group, 4) || !aligned(shared, 4)) return W4_ERR_MISALIGNED;
     if (kv->batch == 0) return W4_OK;
     if (a.q_head == 0 || a.q_tok == 0) return W4_ERR_INVALID_ARG;
-    // the lists of units, steps of 128 keys and of 16, are counted in 32 bits
+    // the lists of units (blocks of 16 keys of an item of up to 8 or 16 heads; half steps of 128 are fewer) are
+    // counted in 32 bits
+    const int g = q_heads / a.kv.heads, items = a.kv.heads * (g <= 8 ? 1 : (g + 15) / 16);
     const long long cap = std::min((long long)a.kv.max_pages * a.kv.page_size, (long long)max_len);
-    if ((cap / 16 + 8) * q_heads * kv->batch > (1LL << 30)) return W4_ERR_UNSUPPORTED_SHAPE;
+    if ((cap / 16 + 8) * items > (1LL << 30) / kv->batch) return W4_ERR_UNSUPPORTED_SHAPE;
     if (!scratch) return W4_ERR_WORKSPACE;
     if (!aligned(scratch, 16)) return W4_ERR_MISALIGNED;
     const int sms = current_sm_count();
