@@ -475,17 +475,16 @@ int shared_own_slots(int Hq, int Hkv, int D, int sm_count) {
     return 2 * sm_count * (D == 64 && nt == 1 ? 16 : 8) * 8 * nt;
 }
 
-#define W4_BY_SHAPE(f)                                                                                   \
-    (a.kv.head_dim == 128 ? (nt == 1 ? f<128, 1>(a, sm_count, stream) : f<128, 2>(a, sm_count, stream))   \
-                          : (nt == 1 ? f<64, 1>(a, sm_count, stream) : f<64, 2>(a, sm_count, stream)))
 int launch_attn_shared_own(const SharedArgs& a, int sm_count, cudaStream_t stream) {
     const int nt = head_tiles(a.Hq, a.kv.heads);
-    return W4_BY_SHAPE(own);
+    if (a.kv.head_dim == 128) return nt == 1 ? own<128, 1>(a, sm_count, stream) : own<128, 2>(a, sm_count, stream);
+    return nt == 1 ? own<64, 1>(a, sm_count, stream) : own<64, 2>(a, sm_count, stream);
 }
 
 int launch_attn_shared_join(const SharedArgs& a, int sm_count, cudaStream_t stream) {
     const int nt = head_tiles(a.Hq, a.kv.heads);
-    return W4_BY_SHAPE(join);
+    if (a.kv.head_dim == 128) return nt == 1 ? join<128, 1>(a, sm_count, stream) : join<128, 2>(a, sm_count, stream);
+    return nt == 1 ? join<64, 1>(a, sm_count, stream) : join<64, 2>(a, sm_count, stream);
 }
 
 }  // namespace w4
