@@ -233,8 +233,8 @@ __device__ __noinline__ int settle(const RouteArgs& a, int t, int e, int n, floa
     return got;
 }
 
-// Every expert offered to token t has the same logit and bias (a padded row's, say): all ties are true
-// ones.  m: the largest logit.
+// Every expert offered to token t has the same logit and bias (a padded row's, say): ties between groups that rank by
+// as many scores are true ones.  m: the largest logit.
 __device__ __noinline__ bool all_alike(const RouteArgs& a, int t, const float* bias, float m) {
     const int lane = threadIdx.x & 31;
     float b = -kInf;
@@ -412,7 +412,10 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
             const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
             // two scores each, their sums' roundings and those of p + bias
             const float tol = 2.f * err + 4.f * kCloseSum * largest;
-            if (hi > -kInf && lo - hi <= tol && !all_alike(a, t, bias, m)) {
+            // groups at the border of which some have one expert to rank by and others two
+            const bool border = g < a.groups && mine >= lo - tol && mine <= hi + tol, two_of = b2 > -kInf;
+            const bool mixed = a.best == 2 && __any_sync(kAll, border && two_of) && __any_sync(kAll, border && !two_of);
+            if (hi > -kInf && lo - hi <= tol && (mixed || !all_alike(a, t, bias, m))) {
                 bool fits = false;
                 if (tol < kInf) in = settle_groups<V>(a, t, buf, mine, a.best == 2 && b2 > -kInf ? b2 : b1, lo, hi, tol, m, &fits);
                 again = !fits;

@@ -1,0 +1,48 @@
+"""w4_moe_route where fp32 cannot tell scores or groups apart: rows with a few close candidates and the rest far
+off, ranks that are equal, tiny or out of fp32's range.  Ids, rows and offsets have to be the float64 oracle's."""
+import numpy as np
+import pytest
+import torch
+
+from block_helpers import to64
+from helpers import ensure_built
+from oracle import serve_oracle as SO
+from test_gpu_moe import guarded_route, same
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w4():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ensure_built()
+
+
+def check(w4, z, k, bias=None, score="sigmoid", groups=1, top=1, best=1, what="", **kw):
+    got = guarded_route(w4, z.cuda(), k, None if bias is None else bias.cuda(), score, groups, top, best, **kw)
+    want = SO.route(to64(z), k, None if bias is None else to64(bias), score, groups, top, best, **kw)
+    same(got, want, to64(z), what)
+    return want
+
+
+@pytest.mark.parametrize("E,G,top", [(32, 4, 2), (256, 8, 3), (96, 32, 20)])
+def test_groups_that_offer_one_expert_and_two(w4, E, G, top):
+    """Alike logits and biases are no tie where one group ranks by one score and another by the sum of two, however
+    near to zero the scores are."""
+    gs = E // G
+    rows = []
+    for x in (-100.0, -60.0, -17.5, 0.0, 0.3, 1.0, -0.7):
+        for alone in ((0,), (1,), (0, 2), (G - 1,), tuple(range(1, G))):
+            row = torch.full((E,), x)
+            for g in alone:
+                row[g * gs:(g + 1) * gs] = float("-inf")
+                row[g * gs + (g + 1) % gs] = x
+            rows.append(row)
+    z = torch.stack(rows + rows)
+    biases = [None, torch.zeros(E)]
+    for x in (0.0, 0.3, 1.0, -0.7):               # p + bias is what the rounding of the bias leaves
+        biases.append(torch.full((E,), -float(np.float32(1 / (1 + np.exp(-np.float64(np.float32(x))))))))
+    for b in biases:
+        for score in ("sigmoid", "softmax"):
+            check(w4, z, 6, b, score, G, top, 2, what=f"E {E} {score}")
