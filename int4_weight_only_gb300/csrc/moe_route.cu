@@ -110,8 +110,10 @@ template <typename F> __device__ __forceinline__ void top_two(F& a, F& b, F c, F
     a = hi;
     b = lo > other ? lo : other;
 }
+// What a group is ranked by; two scores by half their sum, which fp32 holds for any two.
 template <typename F> __device__ __forceinline__ F group_rank(F a, F b, int best) {
-    return best == 2 && b > -kInf ? a + b : a;
+    const F half = F(0.5);
+    return best == 2 ? (b > -kInf ? half * a + half * b : half * a) : a;
 }
 
 // The same choice in 64 bits: lane j's expert, or -1.
@@ -410,7 +412,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
         bool in = g < a.groups && above < a.top_groups;
         if (scored) {
             const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
-            // two scores each, their sums' roundings and those of p + bias
+            // two scores each, their sums' roundings and those of p + bias (ranks are halves: twice as far)
             const float tol = 2.f * err + 4.f * kCloseSum * largest;
             // groups at the border of which some have one expert to rank by and others two
             const bool border = g < a.groups && mine >= lo - tol && mine <= hi + tol, two_of = b2 > -kInf;

@@ -46,3 +46,24 @@ def test_groups_that_offer_one_expert_and_two(w4, E, G, top):
     for b in biases:
         for score in ("sigmoid", "softmax"):
             check(w4, z, 6, b, score, G, top, 2, what=f"E {E} {score}")
+
+
+def test_ranks_out_of_range_of_fp32(w4):
+    """Sums of two scores beyond the largest fp32 value of either sign: biases of the type's lowest value take experts
+    out as far as anything else is left, and large ones are compared as what they are."""
+    low, big = torch.finfo(torch.float32).min, 3.0e38
+    g = torch.Generator().manual_seed(0)
+    z = torch.randn(80, 32, generator=g)
+    z[::2, :8] = float("-inf")                    # nothing offered in group 0
+    masked = torch.zeros(32)
+    masked[8:24] = low                            # groups 1 and 2
+    check(w4, z, 12, masked, "sigmoid", 4, 2, 2, what="lowest")
+    check(w4, z, 12, masked, "softmax", 4, 3, 2, what="lowest")
+    up = torch.zeros(32)
+    up[[9, 10]], up[[17, 18]], up[[25, 26]] = big, 3.2e38, 3.1e38
+    for top in (1, 2, 3):
+        check(w4, z, 4, up, "sigmoid", 4, top, 2, what=f"large, {top}")
+    up[[10, 20]] = float("inf")
+    for top in (1, 2):
+        check(w4, z, 4, up, "sigmoid", 4, top, 2, what=f"infinite, {top}")
+        check(w4, z, 4, up, "sigmoid", 4, top, 1, what=f"infinite, by one, {top}")
