@@ -50,6 +50,10 @@ template <int V> __device__ __forceinline__ float close_of(bool sigmoid, float m
     return sigmoid ? 0x1.4p-20f + 0x1p-22f * fmaxf(-m, 0.f) : 0x1p-20f + (V + 7) * 0x1p-24f;
 }
 constexpr float kCloseSum = 0x1p-23f;
+// A group's rank is off by the errors of its scores and three roundings of 2^-24 of their sizes, of p + bias, of the
+// sum and of the bounds that it is compared by (a little more: the sizes are the computed ones).  Other experts' scores
+// are no part of it, or one that a bias of -1e9 switches off would make all groups look close (16384 x 256: 585 us).
+constexpr float kCloseRank = 0x1.82p-23f;
 
 // Order-preserving key of a float that is not NaN; 0 is below every key of a value over -inf.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -251,23 +255,24 @@ __device__ __noinline__ bool all_alike(const RouteArgs& a, int t, const float* b
     return __all_sync(kAll, same);
 }
 
-// Whether a lane's group is kept, where the last kept one (lo) and the best of the others (hi) are
-// closer than `tol`.  Groups further than that from the border are what they are; the others are
-// ranked in 64 bits by those of their experts that can be among the best (buf over edge - tol; edge:
-// the group's last score that counts).  False in *fits: more candidates than lanes.
+// Whether a lane's group is kept, where ranks lie within their errors of the border: low, high, the least and the most
+// that the group's exact rank can be; kept, what the computed ranks say.  A kept group above all that are not (hi, the
+// most of theirs) stays, one that is below all the kept (lo, the least of theirs) goes; the others are ranked in 64
+// bits by those of their experts that can be among the best (buf from `from` on).  False in *fits: more candidates
+// than lanes.
 template <int V>
-__device__ __noinline__ bool settle_groups(const RouteArgs& a, int t, const float* buf, float mine, float edge, float lo,
-                                           float hi, float tol, float m, bool* fits) {
+__device__ __noinline__ bool settle_groups(const RouteArgs& a, int t, const float* buf, bool kept, float low, float high,
+                                           float from, float lo, float hi, float m, bool* fits) {
     const int lane = threadIdx.x & 31, L = a.lanes, g = lane / L;
-    const bool clear = g < a.groups && mine > hi + tol, open = g < a.groups && !clear && mine >= lo - tol;
+    const bool clear = kept && low > hi, open = g < a.groups && !clear && high >= lo;
     const int left = a.top_groups - __popc(__ballot_sync(kAll, clear && lane == g * L));
     int n = 0, cand = -1, its = -1;
 #pragma unroll 1
     for (int i = 0; i < V && n <= 32; ++i) {
         const int e = i * 32 + lane, ge = e < a.E ? e * a.group_inv >> 20 : 0;
         const bool o = __shfl_sync(kAll, open, ge * L);
-        const float b = __shfl_sync(kAll, edge, ge * L);
-        const bool in = e < a.E && o && buf[e] > -kInf && !(buf[e] < b - tol);
+        const float b = __shfl_sync(kAll, from, ge * L);
+        const bool in = e < a.E && o && buf[e] > -kInf && !(buf[e] < b);
         for (uint32_t w = __ballot_sync(kAll, in); w; w &= w - 1, ++n)
             if (lane == n) cand = i * 32 + __ffs(w) - 1;
     }
@@ -373,13 +378,6 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
             for (int i = 0; i < V; ++i)
                 if (i * 32 + lane < a.E) buf[i * 32 + lane] = x[i];
         }
-        float largest = 0.f;                        // of the scores' sizes
-        if (scored) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) largest = fmaxf(largest, x[i] > -kInf ? fabsf(x[i]) : 0.f);
-            if (!a.bias) largest = 1.f;             // x are logits; scores are at most 1
-            largest = warp_max(largest);
-        }
         __syncwarp();
         // L lanes a group, each with every L-th of its scores; groups start at different ones,
         // so that the lanes' words lie in different banks
@@ -411,15 +409,17 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
         }
         bool in = g < a.groups && above < a.top_groups;
         if (scored) {
-            const float lo = -warp_max(in ? -mine : -kInf), hi = warp_max(g < a.groups && !in ? mine : -kInf);
-            // two scores each, their sums' roundings and those of p + bias (ranks are halves: twice as far)
-            const float tol = 2.f * err + 4.f * kCloseSum * largest;
+            const float size = a.best == 2 ? 0.5f * kCloseRank * fabsf(b1) + (b2 > -kInf ? 0.5f * kCloseRank * fabsf(b2) : 0.f)
+                                           : kCloseRank * fabsf(b1);
+            const float off = fabsf(mine) < kInf ? 0.5f * err + size : 0.f, low = mine - off, high = mine + off;
+            const float lo = -warp_max(in ? -low : -kInf), hi = warp_max(g < a.groups && !in ? high : -kInf);
             // groups at the border of which some have one expert to rank by and others two
-            const bool border = g < a.groups && mine >= lo - tol && mine <= hi + tol, two_of = b2 > -kInf;
+            const bool border = g < a.groups && high >= lo && low <= hi, two_of = b2 > -kInf;
             const bool mixed = a.best == 2 && __any_sync(kAll, border && two_of) && __any_sync(kAll, border && !two_of);
-            if (hi > -kInf && lo - hi <= tol && (mixed || !all_alike(a, t, bias, m))) {
+            if (hi > -kInf && lo <= hi && (mixed || !all_alike(a, t, bias, m))) {
+                const float edge = a.best == 2 && b2 > -kInf ? b2 : b1;
                 bool fits = false;
-                if (tol < kInf) in = settle_groups<V>(a, t, buf, mine, a.best == 2 && b2 > -kInf ? b2 : b1, lo, hi, tol, m, &fits);
+                in = settle_groups<V>(a, t, buf, in, low, high, edge - (err + kCloseRank * fabsf(edge)), lo, hi, m, &fits);
                 again = !fits;
             }
         }

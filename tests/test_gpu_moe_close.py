@@ -67,3 +67,53 @@ def test_ranks_out_of_range_of_fp32(w4):
     for top in (1, 2):
         check(w4, z, 4, up, "sigmoid", 4, top, 2, what=f"infinite, {top}")
         check(w4, z, 4, up, "sigmoid", 4, top, 1, what=f"infinite, by one, {top}")
+
+
+@pytest.mark.parametrize("off", [-1e4, -1e9, torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("best", [1, 2])
+def test_experts_switched_off_by_a_finite_bias(w4, off, best):
+    g = torch.Generator().manual_seed(5)
+    z = torch.randn(140, 256, generator=g)
+    b = torch.randn(256, generator=g) * 0.05
+    b[[3, 77, 78, 200]] = off
+    b[32:64] = off                                # a whole group
+    for score in ("sigmoid", "softmax"):
+        check(w4, z, 8, b, score, 8, 4, best, what=f"{off} {score}")
+    check(w4, z, 8, b, "sigmoid", what=f"{off}")
+    check(w4, z, 20, b, "sigmoid", 8, 8, best, what=f"{off}")
+
+
+def test_small_scores_in_groups(w4):
+    g = torch.Generator().manual_seed(6)
+    for shift in (-15.0, -40.0, -86.0):
+        z = torch.randn(140, 256, generator=g) + shift
+        check(w4, z, 8, None, "sigmoid", 8, 4, 2, what=f"{shift}")
+        check(w4, z, 8, torch.randn(256, generator=g) * 1e-7, "sigmoid", 8, 4, 2, what=f"{shift} biased")
+
+
+def test_masks_and_small_scores_cost_no_second_choice(w4):
+    """A token that has to be chosen in 64 bits altogether takes 20 times as long as one that has not.  A mask in the bias, or
+    scores that are all small, must not send every token there: the time stays within four times that of plain ones."""
+    g = torch.Generator().manual_seed(7)
+    z = torch.randn(8192, 256, generator=g).cuda()
+    b = (torch.randn(256, generator=g) * 0.05).cuda()
+
+    def us(z, b):
+        def call():
+            w4.w4_moe_route(z, 8, bias=b, score="sigmoid", groups=8, top_groups=4, group_best=2)
+        times = []
+        for _ in range(6):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            for _ in range(10):
+                call()
+            end.record()
+            end.synchronize()
+            times.append(start.elapsed_time(end))
+        return min(times[1:])
+    plain = us(z, b)
+    for off in (-1e4, -1e9, torch.finfo(torch.float32).min):
+        masked = b.clone()
+        masked[[3, 77]] = off
+        assert us(z, masked) < 4 * plain, off
+    assert us(z - 40.0, None) < 4 * us(z, None)
