@@ -45,11 +45,11 @@ constexpr uint32_t kAll = 0xffffffffu;
 // p where it is a distance from the largest logit; a sigmoid of a negative logit x is off by
 // 2^-23 |x| of itself, at worst that of the largest.  The roundings of a softmax's sum, over
 // V registers and 5 steps, and of its reciprocal are the same for both.  The rounding of
-// p + bias adds kCloseSum of the larger score.
+// p + bias adds kCloseSum of the larger score.  Scores below 2^-126 are flushed to zero: kFlushed.
 template <int V> __device__ __forceinline__ float close_of(bool sigmoid, float m) {
     return sigmoid ? 0x1.4p-20f + 0x1p-22f * fmaxf(-m, 0.f) : 0x1p-20f + (V + 7) * 0x1p-24f;
 }
-constexpr float kCloseSum = 0x1p-23f;
+constexpr float kCloseSum = 0x1p-23f, kFlushed = 0x1p-125f;
 // A group's rank is off by the errors of its scores and three roundings of 2^-24 of their sizes, of p + bias, of the
 // sum and of the bounds that it is compared by (a little more: the sizes are the computed ones).  Other experts' scores
 // are no part of it, or one that a bias of -1e9 switches off would make all groups look close (16384 x 256: 585 us).
@@ -364,7 +364,7 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, float* x, floa
     };
     // from here x is what experts are chosen by, -inf where they are not offered
     if (a.bias) scores(x);
-    const float err = scored && m > -kInf ? close_of<V>(a.sigmoid, m) * prob(m) : 0.f;
+    const float err = scored && m > -kInf ? close_of<V>(a.sigmoid, m) * prob(m) + kFlushed : 0.f;
     bool again = false;
     if (a.groups > 1) {
         if (two && !a.bias) {

@@ -117,3 +117,15 @@ def test_masks_and_small_scores_cost_no_second_choice(w4):
         masked[[3, 77]] = off
         assert us(z, masked) < 4 * plain, off
     assert us(z - 40.0, None) < 4 * us(z, None)
+
+
+def test_scores_below_the_normal_range(w4):
+    """Scores that the approximate exponential flushes to zero against biases of their size."""
+    z = torch.full((70, 16), -1000.0)
+    bias = torch.zeros(16)
+    bias[3] = 3e-39
+    z[:, 5] = -88.0                               # p = 6.1e-39
+    z[1::2, 9] = -88.5                            # 3.7e-39
+    want = check(w4, z, 3, bias, what="flushed")
+    assert want[1][0, :2].tolist() == [5, 3] and want[1][1].tolist() == [5, 9, 3]
+    check(w4, z, 3, bias, "sigmoid", 4, 2, 2, what="flushed, in groups")
