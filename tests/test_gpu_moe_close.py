@@ -26,6 +26,141 @@ def check(w4, z, k, bias=None, score="sigmoid", groups=1, top=1, best=1, what=""
     return want
 
 
+def probabilities(z, score, dtype):
+    z = z.astype(dtype)
+    if score == "sigmoid":
+        return 1 / (1 + np.exp(-z))
+    e = np.exp(z - z.max(1, keepdims=True))
+    return e / e.sum(1, keepdims=True)
+
+
+def logits_of(p, score):
+    return np.log(p / (1 - p)) if score == "sigmoid" else np.log(p)
+
+
+def close_rows(E, k, above, n, rows, score, seed):
+    """Logits and a bias that cancels the scores of n experts to within fp32's rounding at a height T; `above` experts
+    clearly over them, the others clearly under.  Returns (z, bias, how many scores lie at T)."""
+    r = np.random.default_rng(seed)
+    perm = r.permutation(E)
+    C, A, R = perm[:n], perm[n:n + above], perm[n + above:]
+    T, unit = (0.8, 0.5) if score == "sigmoid" else (4.0 / E, 0.5 / E)
+    p = np.empty((rows, E))
+    p[:, C] = unit * r.uniform(0.6, 1.4, n) * (1 + 8e-8 * r.standard_normal((rows, n)))
+    for t in range(rows):
+        p[t, A] = unit * (0.8 + 0.02 * r.permutation(above))
+        p[t, R] = unit * (0.1 + 0.8 * r.permutation(E - n - above) / E)
+    if score == "softmax":
+        p /= p.sum(1, keepdims=True)
+    z = logits_of(p, score).astype(np.float32)
+    exact = probabilities(z, score, np.float64)
+    bias = np.zeros(E, np.float32)
+    bias[C] = (T - exact[:, C].mean(0)).astype(np.float32)
+    bias[A] = np.float32(T)                       # T + unit * 0.8 and more
+    s = exact + bias.astype(np.float64)
+    near = np.abs(s - T) < 4e-6 * unit / 0.5
+    assert (near.sum(1) == n).all() and (np.abs(s - T)[~near] > 0.02 * unit).all()
+    return torch.tensor(z), torch.tensor(bias), s, C
+
+
+def fp32_order_differs(z, bias, score, k):
+    """Rows whose choice in plain fp32 is not that of 64 bits."""
+    def order(dtype):
+        s = probabilities(z.numpy(), score, dtype) + bias.numpy().astype(dtype)
+        return np.argsort(-s, axis=1, kind="stable")[:, :k]
+    return (order(np.float32) != order(np.float64)).any(1)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,above,n", [(64, 8, 0, 2), (64, 8, 6, 3), (128, 8, 4, 5), (128, 6, 5, 12), (256, 8, 7, 20),
+                                         (60, 4, 3, 2), (384, 8, 2, 9), (1024, 32, 20, 12), (33, 32, 0, 20)])
+def test_a_few_close_candidates(w4, E, k, above, n, score):
+    """They are chosen, or the last place is among them; the fp32 order is wrong in many rows."""
+    z, bias, s, C = close_rows(E, k, above, n, 150, score, E + n)
+    assert fp32_order_differs(z, bias, score, k).any()
+    for rows in (150, 40):
+        check(w4, z[:rows], k, bias, score, what=f"E {E} k {k} {above} above {n} close {score}")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("above,n", [(0, 31), (0, 32), (0, 33), (4, 27), (4, 28), (4, 29), (7, 25), (7, 26)])
+def test_as_many_candidates_as_lanes(w4, above, n, score):
+    """k + n - (k - above) of them: 31, 32 and 33 for the last place and all behind it."""
+    z, bias, s, C = close_rows(256, 8, above, n, 90, score, above * 40 + n)
+    assert fp32_order_differs(z, bias, score, 8).any()
+    check(w4, z, 8, bias, score, what=f"{above} above {n} close {score}")
+
+
+def close_groups(E, G, above, near, rows, score, with_bias, seed, spread):
+    """Logits and a bias whose sums of two scores differ by about `spread` between the border groups (near[i] experts at
+    the second score or within its rounding); `above` groups lie over them, the others under."""
+    r = np.random.default_rng(seed)
+    gs, border = E // G, len(near)
+    unit = 0.5 if score == "sigmoid" else 1.0 / E
+    s = np.tile(unit * (0.05 + 0.05 * r.random(E)), (rows, 1))
+    for i, g in enumerate(r.permutation(G)):
+        at = g * gs + r.permutation(gs)
+        if i < border:
+            one, two, m = 1.4, 1.0, near[i] - 1
+        elif i < border + above:
+            one, two, m = 1.6 + 0.01 * i, 1.2 + 0.01 * i, 1
+        else:
+            one, two, m = 0.8 - 0.01 * i, 0.5 - 0.005 * i, 1
+        s[:, at[0]] = unit * one * (1 + spread * r.standard_normal(rows))
+        s[:, at[1:1 + m]] = unit * two * (1 + spread * r.standard_normal((rows, m)))
+    bias = (unit * r.uniform(-0.04, 0.04, E) * with_bias).astype(np.float32)
+    p = s - bias
+    if score == "softmax":                        # of a sum of one
+        bias, p = (bias / p.sum(1).mean()).astype(np.float32), p / p.sum(1).mean()
+    z = logits_of(p, score).astype(np.float32)
+    return torch.tensor(z), torch.tensor(bias) if with_bias else None
+
+
+def group_sums(z, bias, score, G, dtype):
+    s = probabilities(z.numpy(), score, dtype)
+    if bias is not None:
+        s = s + bias.numpy().astype(dtype)
+    top = -np.sort(-s.reshape(len(s), G, -1), axis=2)[..., :2]
+    return top[..., 0] + top[..., 1], top[..., 1], s
+
+
+def border_differs(z, bias, score, G, top):
+    """Rows in which plain fp32 keeps other groups than 64 bits; and each row's experts that can be among the best two of
+    a group within 2e-6 of the border."""
+    kept = []
+    for dtype in (np.float32, np.float64):
+        rank, second, s = group_sums(z, bias, score, G, dtype)
+        order = np.argsort(-rank, axis=1, kind="stable")[:, :top]
+        kept.append(np.sort(order, axis=1))
+    last = -np.sort(-rank, axis=1)[:, top - 1:top]
+    scale = s.max(1, keepdims=True)
+    open_ = np.abs(rank - last) < 6e-6 * scale
+    cand = (s.reshape(len(s), G, -1) > (second - 4e-6 * scale)[..., None]) & open_[..., None]
+    return (kept[0] != kept[1]).any(1), cand.sum((1, 2))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E,G,top,above,near,k", [(64, 8, 4, 3, [2, 2], 6), (256, 8, 4, 2, [2, 3, 2, 4], 8),
+                                                  (128, 4, 2, 1, [2, 2, 5], 4), (96, 32, 9, 7, [2, 2, 2, 3], 8),
+                                                  (512, 8, 2, 0, [3, 4, 2], 4)])
+def test_a_few_close_groups(w4, E, G, top, above, near, k, bias, score):
+    z, b = close_groups(E, G, above, near, 150, score, bias, E + top, 1.5e-7)
+    wrong, cand = border_differs(z, b, score, G, top)
+    assert wrong.any() and np.mean(cand <= 32) > 0.9 and np.mean(cand >= 4) > 0.9
+    for rows in (150, 40):
+        check(w4, z[:rows], k, b, score, G, top, 2, what=f"E {E} {G} groups {near} {score} bias {bias}")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("near", [[8, 8, 8, 7], [8, 8, 8, 8], [8, 8, 8, 9]])
+def test_as_many_candidates_of_close_groups_as_lanes(w4, near, score):
+    z, b = close_groups(256, 8, 2, near, 120, score, False, sum(near), 1.5e-7)
+    wrong, cand = border_differs(z, b, score, 8, 4)
+    assert wrong.any() and np.mean(cand == sum(near)) > 0.9
+    check(w4, z, 8, b, score, 8, 4, 2, what=f"{near} {score}")
+
+
 @pytest.mark.parametrize("E,G,top", [(32, 4, 2), (256, 8, 3), (96, 32, 20)])
 def test_groups_that_offer_one_expert_and_two(w4, E, G, top):
     """Alike logits and biases are no tie where one group ranks by one score and another by the sum of two, however
