@@ -762,7 +762,7 @@ W4_API int w4_moe_route(const void* logits, int logits_bf16, long long logits_st
  *  row -1 is skipped (a weight there is not read into the sum); any other value
  *  outside [0, R) is skipped and raises W4_ERR_GROUP_TOKENS.  No two places of
  *  `row` may name the same row of a gather's out.  out must not overlap x or y;
- *  it may be `shared`.
+ *  it may be `shared`.  A gather's out and a combine's y may be NULL when R is 0.
  *  k <= W4_MOE_MAX_TOPK, K, N <= 2^22; buffers need 2-byte alignment (rows that are multiples
  *  of 16 bytes, 16-byte aligned, run fastest).
  * ------------------------------------------------------------------------- */

@@ -96,7 +96,8 @@ int w4_moe_route(const void* logits, int logits_bf16, long long logits_stride, c
 
 int w4_moe_gather(const uint16_t* x, long long x_stride, const int32_t* row, uint16_t* out, int T, int k, int K, int R,
                   void* stream) {
-    const int rc = check_move(x, row, out, T, k, K, R);
+    // a buffer of no rows: nothing is copied, rows other than -1 are flagged
+    const int rc = check_move(x, row, R == 0 && !out ? x : out, T, k, K, R);
     if (rc) return rc;
     if (x_stride < 0) return W4_ERR_INVALID_ARG;
     if (T == 0) return W4_OK;

@@ -28,3 +28,17 @@ def test_later_runs_of_the_order(w4, T, E, k, count):
     c = None if count is None else torch.tensor([count], dtype=torch.int32, device="cuda")
     got = guarded_route(w4, z.cuda(), k, count=c)
     same(got, SO.route(to64(z), k, count=count), to64(z), f"T {T} E {E} k {k}")
+
+
+@pytest.mark.parametrize("K", [8, 2, 7])
+def test_rows_to_and_from_a_buffer_without_rows(w4, K):
+    """Every place is -1: nothing is copied, the sum is the shared row; any other place is flagged."""
+    x = torch.ones(3, K, dtype=torch.bfloat16, device="cuda")
+    none = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
+    empty = torch.empty(0, K, dtype=torch.bfloat16, device="cuda")
+    assert w4.w4_moe_gather(x, none, out=empty) is empty
+    assert torch.equal(w4.w4_moe_combine(empty, none, torch.ones(3, 2, device="cuda"), shared=x), x)
+    assert w4.w4_get_device_error() == 0
+    none[1, 1] = 0
+    w4.w4_moe_gather(x, none, out=empty)
+    assert w4.w4_get_device_error() == -11
