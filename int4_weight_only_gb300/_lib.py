@@ -867,6 +867,16 @@ if _alloc is None or _free is None:
     _alloc, _free = (lambda n, s: torch.cuda.caching_allocator_alloc(n, stream=s)), torch.cuda.caching_allocator_delete
 
 
+def _scratch(t, name, like):
+    """(address, bytes) of a caller's scratch: the kernels write all of it, so it has to be memory of the tensor
+    `like`'s device, in one piece."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {like.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def w4_attn_shared_scratch_bytes(batch: int, q_heads: int, heads: int, head_dim: int) -> int:
     return int(load().w4_attn_shared_scratch_bytes(batch, q_heads, heads, head_dim))
 
@@ -906,7 +916,7 @@ def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if scratch is None:
         at = mine = _alloc(max(need, 16), s)
     else:
-        at, need = scratch.data_ptr(), scratch.numel() * scratch.element_size()
+        at, need = _scratch(scratch, "scratch", q)
     try:
         rc = lib.w4_attn_shared(
             kv, q.data_ptr(), qs[0], qs[1], group.data_ptr(), shared.data_ptr(), G, out.data_ptr(),
@@ -1011,7 +1021,7 @@ def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
     s = _stream(logits, stream)
     need, at, mine = 0, None, None
     if workspace is not None:
-        at, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        at, need = _scratch(workspace, "workspace", logits)
     elif T > 64 and E > 0:
         need = _scratch_sizes.get(E)                # the most that any number of tokens takes
         if need is None:
