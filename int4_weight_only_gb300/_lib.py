@@ -904,8 +904,8 @@ def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     out = _attn_outputs(q, out, lse)
     if B == 0 or Hq == 0:
         return out
-    if not -0x80000000 <= max_len <= 0x7FFFFFFF:
-        _past_32_bits(max_len=max_len)
+    if not -0x80000000 <= max_len <= 0x7FFFFFFF or G > 0x7FFFFFFF:
+        _past_32_bits(max_len=max_len, groups=G)
     lib = _lib or load()
     key = (B, Hq, pool[1], D, q.get_device())
     need = _scratch_sizes.get(key)
@@ -962,6 +962,8 @@ def w4_kv_plan(lens: torch.Tensor, new_tokens: Optional[torch.Tensor], free_page
         _i32(used_out, (1,), "used_out")
     if min(T, pages, page_size) < 0 or max(T, pages, page_size) > 0x7FFFFFFF:
         raise ValueError(f"T={T}, pages={pages}, page_size={page_size}: out of range")
+    if max(B, free_pages.numel(), table.shape[1]) > 0x7FFFFFFF:
+        _past_32_bits(requests=B, free_pages=free_pages.numel(), columns=table.shape[1])
     dev, i32 = lens.device, torch.int32
     kv_len = torch.empty_like(lens)
     goff = torch.empty(B + 1, dtype=i32, device=dev)
@@ -1012,6 +1014,8 @@ def w4_moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = No
         _i32(count, (1,), "count")
     if not 1 <= k <= E or min(groups, top_groups) < 1 or max(groups, top_groups) > E or group_best not in (1, 2):
         raise ValueError(f"k={k}, groups={groups}, top_groups={top_groups}, group_best={group_best} of {E} experts")
+    if max(T, E) > 0x7FFFFFFF:
+        _past_32_bits(tokens=T, experts=E)
     lib = _lib or load()
     dev = logits.device
     weights = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -1055,6 +1059,8 @@ def w4_moe_gather(x: torch.Tensor, row: torch.Tensor, out=None, stream=None) -> 
         _need(out, torch.bfloat16, (out.shape[0], K), "out")
     if T == 0 or K == 0:
         return out
+    if max(T, k, K, out.shape[0]) > 0x7FFFFFFF:
+        _past_32_bits(tokens=T, k=k, width=K, rows=out.shape[0])
     rc = (_lib or load()).w4_moe_gather(x.data_ptr(), xs[0], row.data_ptr(), out.data_ptr(), T, k, K,
                                         out.shape[0], _stream(x, stream))
     if rc:
@@ -1080,6 +1086,8 @@ def w4_moe_combine(y: torch.Tensor, row: torch.Tensor, weights: torch.Tensor,
         _need(out, torch.bfloat16, (T, N), "out")
     if T == 0 or N == 0:
         return out
+    if max(T, k, N, R) > 0x7FFFFFFF:
+        _past_32_bits(tokens=T, k=k, width=N, rows=R)
     rc = (_lib or load()).w4_moe_combine(y.data_ptr(), row.data_ptr(), weights.data_ptr(),
                                          None if shared is None else shared.data_ptr(), out.data_ptr(), T, k, N, R,
                                          _stream(y, stream))

@@ -1,4 +1,5 @@
-"""A caller's own scratch in the calls of a serving step: memory of another kind is refused before anything is launched."""
+"""Arguments of the calls of a serving step that are refused before anything is launched: a caller's own scratch in
+memory of another kind, and sizes that do not fit in 32 bits, whose lower halves would be calls of other sizes."""
 import pytest
 import torch
 
@@ -43,3 +44,23 @@ def test_routing(w4):
             w4.w4_moe_route(z, 3, workspace=workspace)
     got = w4.w4_moe_route(z, 3, workspace=torch.zeros(n, dtype=torch.uint8, device="cuda"))
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_sizes_past_32_bits(w4):
+    """(Views of one row where the call takes them, else up to 9 GB that nothing writes.)"""
+    far, bf = 1 << 32, torch.bfloat16
+    one = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    row = torch.zeros(1, 8, dtype=bf, device="cuda")
+    weight = torch.ones(1, 1, device="cuda")
+    with pytest.raises(ValueError, match="32-bit"):
+        w4.w4_moe_route(row.expand(far + 1, 8), 2)
+    with pytest.raises(ValueError, match="32-bit"):
+        w4.w4_moe_combine(torch.empty(far + 1, 1, dtype=bf, device="cuda"), one, weight)
+    with pytest.raises(ValueError, match="32-bit"):
+        w4.w4_moe_gather(torch.empty(1, 1, dtype=bf, device="cuda"), one, out=torch.empty(far + 1, 1, dtype=bf, device="cuda"))
+    with pytest.raises(ValueError, match="32-bit"):
+        w4.w4_moe_gather(torch.empty(1, far + 8, dtype=bf, device="cuda"), one)
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32-bit"):
+        w4.w4_kv_plan(lens, None, lens, lens, torch.empty(1, far // 2, dtype=torch.int32, device="cuda"), 16, 9, 1)
+    torch.cuda.empty_cache()
