@@ -657,6 +657,11 @@ W4_API int w4_attn_prefill(const w4_paged_kv* kv, const uint16_t* q, long long q
  *          need not be initialised: results of parts between the kernels of a
  *          call.  Calls that can overlap need one each.
  *  groups >= 1; head counts and head_dim as in w4_attn_decode.
+ *  The list of 16-key blocks is counted in 32 bits, from what the launch knows:
+ *          batch * heads * (n / 16 + 8) <= 2^30, n the smaller of max_len and
+ *          max_pages * page_size (of more than 8 query heads to a key-value head
+ *          each 16 count as one); W4_ERR_UNSUPPORTED_SHAPE otherwise.  A max_len
+ *          near the lengths leaves the most room.
  * ------------------------------------------------------------------------- */
 W4_API size_t w4_attn_shared_scratch_bytes(int batch, int q_heads, int heads, int head_dim);
 W4_API int w4_attn_shared(const w4_paged_kv* kv, const uint16_t* q, long long q_token_stride,

@@ -143,3 +143,23 @@ def test_shared_attention_counts_units_in_32_bits(w4):
     lib, c = w4.load(), _codes()
     kv = _kv(batch=1 << 14, maxp=1 << 20, ts=1 << 20)
     assert _shared(lib, kv, max_len=1 << 24) == c["W4_ERR_UNSUPPORTED_SHAPE"]
+
+
+def test_shared_attention_takes_what_its_header_says(w4):
+    """The largest launch that is taken (it goes on to ask for its scratch) and the first that is refused, by batch and by
+    length, for one list item a key-value head and for several."""
+    lib, c = w4.load(), _codes()
+    taken, refused = c["W4_ERR_WORKSPACE"], c["W4_ERR_UNSUPPORTED_SHAPE"]
+    for heads, hq, per in ((4, 28, 1), (4, 32, 1), (4, 36, 1), (2, 64, 2), (1, 128, 8), (1, 17, 2)):
+        for n in (16, 4096, 1 << 20):
+            most = (1 << 30) // (heads * per * (n // 16 + 8))
+            for batch, want in ((most, taken), (most + 1, refused)):
+                kv = _kv(heads=heads, batch=batch, maxp=1 << 20, ts=1 << 20)
+                assert _shared(lib, kv, hq=hq, max_len=n, scratch=None) == want, (heads, hq, n, batch)
+                kv = _kv(heads=heads, batch=batch, maxp=n // 16, ts=n // 16)      # the table is the bound
+                assert _shared(lib, kv, hq=hq, max_len=1 << 30, scratch=None) == want, (heads, hq, n, batch)
+        batch = 1 << 10
+        most = 16 * ((1 << 20) // (heads * per) - 8) + 15
+        for n, want in ((most, taken), (most + 1, refused)):
+            kv = _kv(heads=heads, batch=batch, maxp=1 << 22, ts=1 << 22)
+            assert _shared(lib, kv, hq=hq, max_len=n, scratch=None) == want, (heads, hq, n)
