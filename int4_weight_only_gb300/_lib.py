@@ -890,7 +890,9 @@ def w4_attn_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     the first one's row of the table names; those are read once for the group.
     kv_len counts them; a sequence has at least shared[i] tokens, or 0.  scratch
     (w4_attn_shared_scratch_bytes, uninitialised) is allocated for the call when
-    not given.  B * Hkv * (max_len / 16 + 8) is 2^30 at most (see include/w4.h)."""
+    not given.  B * Hkv * (max_len / 16 + 8) is 2^30 at most (see include/w4.h).
+    For long or widely shared prefixes: where less than about 100 MB of keys and
+    values would be read again, w4_attn_decode on the same tables is faster."""
     kv, pool, batch = _paged_kv(k_cache, v_cache, kv_len, table)
     qs = _need_view(q, torch.bfloat16, 3, "q")
     B, Hq, D = q.shape

@@ -328,9 +328,9 @@ struct Walk {
 //
 // Where a pair has one tile only, nothing runs while that tile's softmax does.  Heads of 64
 // are bound by that: there tiles A and B are the same rows over every second block of keys, and
-// are added at the end (a twin, a unit a block: a call for 8 sequences behind 65536 tokens, 32 / 8
-// heads, 48.5 -> 40.5 us).  Heads of 128 are not (a block of theirs is 64 KB, 1.5 us of the
-// measured copy rate when all SMs read): 41.0 us for 28 / 4 heads, as twins 44.6.
+// are added at the end (a twin, a unit a block: a call for 8 sequences behind 65536 tokens with one of
+// their own, 32 / 8 heads, 49.9 -> 39.9 us).  Heads of 128 are not (a block of theirs is 64 KB, 1.5 us
+// of the measured copy rate when all SMs read): 39.1 us for 28 / 4 heads; as twins 3.6 more.
 __host__ __device__ constexpr bool has_twins(int D) { return D == 64; }
 struct SharedGroup {
     int t0, nq, len;            // first sequence, sequences, shared keys

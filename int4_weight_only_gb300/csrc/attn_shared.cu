@@ -358,7 +358,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_shared_join(const SharedArgs a
         const int b = (int)(row / a.Hq);
         const RowParts r = row_parts<D>(a, b, (int)(row - (long long)b * a.Hq), HP, workers, ctas);
         const int n = r.np + r.no;
-        constexpr int U = WPR == 8 || WPR == 2 ? 8 : 4; // parts whose loads are in flight together
+        // Parts whose loads are in flight together.  28 / 4 heads of 128, 4 and 8 of them: 224 rows (8 warps
+        // a row) 21.9 and 21.0 us a call, 896 (4) 28.4 and 27.7, but 1024 rows of 64 23.9 and 25.5,
+        // 1792 (2) 55.6 and 54.5, 7168 (1) 145.8 and 147.0; 2 of them up to 2.9 us slower.
+        constexpr int U = WPR == 8 || WPR == 2 ? 8 : 4;
         for (int x0 = (warp % WPR) * PW + lane / LP; x0 < n; x0 += WPR * PW * U) {
             float2 ml[U];
             float4 t[U];

@@ -8,9 +8,9 @@
 // counterparts, eight at a time, so that their loads or stores are in flight together.  Measured
 // in a graph: 8192 tokens of 2048 values to 8 rows each (302 MB) 45.1 us, back 43.3: 0.98 and 1.02
 // of the measured copy rate (one row after the other, back: 53); 333 x 3580, 6 rows and a
-// shared one (8-byte words) 4.3 us; 16 x 2048 1.6.  2048 tokens of 4096, 4092, 4094 and 4095
-// values, 8 rows and a shared one: 23.7, 25.9, 28.5, 30.3 us there, 22.6, 25.0, 25.3, 40.8 back
-// (a value a thread: 43 and 63 for the last two widths).
+// shared one (8-byte words) 4.4 us; 16 x 2048 1.7.  2048 tokens of 4096, 4092, 4094 and 4095
+// values to 8 rows: 24.4, 27.2, 31.6, 31.2 us there, 21.1, 23.2, 23.7, 41.3 back, with a shared row
+// 22.6, 24.7, 25.2, 47.0 (a value a thread: 43 there and 63 back for the last two widths).
 #include "block_device.cuh"
 #include "w4_internal.h"
 

@@ -26,8 +26,11 @@
 // Bound by the instructions of the selection (16384 tokens of 256 experts: issue slots 72 % busy
 // with 32 warps an SM, HBM under 1 %; 770 instructions a token for k = 8, 60 a round before
 // the lanes kept their heads as keys, 50 since; scores and a bias add 225, groups 470).  Measured in
-// a graph: 16384 x 256 22.5 us without a bias, 29.0 with, 36.3 in 8 groups ranked by two
-// scores (17 MB of logits are 2.7 us); 1003 x 60 9.5; 16 x 128 in one CTA 4.3.
+// a graph: 16384 x 256 22.6 us without a bias, 29.0 with, 36.4 in 8 groups ranked by two
+// scores (17 MB of logits are 2.7 us); 16384 x 384 34, 45 and 59, x 1024 65, 94 and 118 (the
+// registers of 512 threads an SM); 1003 x 60 9.4; 16 x 128 in one CTA 4.4.  Rows with one
+// dominant score leave the others' within its errors, and more is ranked again: softmax of
+// logits of deviation 3, 5 and 8 with a bias of 0.03 46, 90 and 146 us (of 1.3: 30).
 #include "block_device.cuh"
 #include "w4_internal.h"
 
@@ -97,7 +100,8 @@ template <int V> __device__ __forceinline__ void load_logits(const RouteArgs& a,
 __device__ __forceinline__ float soft_num(float x, float m) { return m == kInf ? (x == kInf ? 1.f : 0.f) : expf(x - m); }
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + expf(-x)); }
 // The same for comparisons, by the hardware's 2^x (2^-22) and reciprocal (2^-23).
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f;                  // (softmax weights not renormalised, whose
+                                                              // sum is of these: 1.2e-7 off in the norm)
 __device__ __forceinline__ float rcp_approx(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

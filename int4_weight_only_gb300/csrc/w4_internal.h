@@ -298,7 +298,8 @@ int launch_attn_shared_join(const SharedArgs& a, int sm_count, cudaStream_t stre
 
 // ---------------------------------------------------------------- experts
 // Routing (moe_route.cu).  Up to kRouteOne tokens one CTA does everything; more go to
-// kRouteBlocks CTAs at most, whose counts by expert a second kernel adds up.
+// kRouteBlocks CTAs at most, whose counts by expert a second kernel adds up: one an SM of a GB300,
+// a constant so that the workspace's size follows from T and E without a device.
 constexpr int kRouteOne = 64;
 constexpr int kRouteBlocks = 152;
 struct RouteArgs {
