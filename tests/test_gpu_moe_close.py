@@ -153,6 +153,22 @@ def test_a_few_close_groups(w4, E, G, top, above, near, k, bias, score):
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G,top,above,near,k", [(64, 8, 4, 3, [2, 2], 6), (256, 8, 4, 2, [2, 3, 2, 4], 8),
+                                                  (96, 32, 9, 7, [2, 2, 2, 3], 8)])
+def test_a_few_close_groups_by_their_best(w4, E, G, top, above, near, k, score):
+    """Ranked by one biased score, of which the border groups' lie within an fp32 rounding."""
+    z, b = close_groups(E, G, above, near, 150, score, True, E + top, 1e-7)
+    kept = []
+    for dtype in (np.float32, np.float64):
+        s = probabilities(z.numpy(), score, dtype) + b.numpy().astype(dtype)
+        kept.append(np.sort(np.argsort(-s.reshape(150, G, -1).max(2), axis=1, kind="stable")[:, :top], axis=1))
+    # (of two border groups, the host's fp32 exponential happens to order all rows on some machines)
+    assert len(near) == 2 or (kept[0] != kept[1]).any()
+    for rows in (150, 40):
+        check(w4, z[:rows], k, b, score, G, top, 1, what=f"E {E} {G} groups {near} {score}")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("near", [[8, 8, 8, 7], [8, 8, 8, 8], [8, 8, 8, 9]])
 def test_as_many_candidates_of_close_groups_as_lanes(w4, near, score):
     z, b = close_groups(256, 8, 2, near, 120, score, False, sum(near), 1.5e-7)
